@@ -47,7 +47,8 @@
  *   - A handle may be used from several threads and streams at once; set its options before
  *     sharing it (hashgrid_set_option is not synchronised with running calls).
  *   - The compute calls may be captured into CUDA graphs: their host-side checks only query
- *     pointer attributes, and each call is a single kernel launch on cuda_stream.
+ *     pointer attributes, and each call is a single kernel launch on cuda_stream (the layer
+ *     and optimiser calls at the end of this file: one launch or a few, all on cuda_stream).
  */
 #ifndef HASHGRID_H
 #define HASHGRID_H
@@ -63,7 +64,12 @@ typedef struct hashgrid_s *hashgrid_t; /* opaque, library-owned */
 
 /* Table storage type. fp16 tables are read as IEEE binary16 and converted exactly to fp32
  * (subnormals kept); interpolation and gradients are fp32 ([Repro-HG] section 5). */
-enum hashgrid_dtype { HASHGRID_F32 = 0, HASHGRID_F16 = 1 };
+enum hashgrid_dtype {
+    HASHGRID_F32 = 0,
+    HASHGRID_F16 = 1,
+    HASHGRID_BF16 = 2, /* layers and optimiser tensors; not a table type */
+    HASHGRID_E4M3 = 3  /* 8-bit optimiser states only */
+};
 
 enum hashgrid_status {
     HASHGRID_OK = 0,
@@ -362,6 +368,152 @@ enum hashgrid_backward_mode {
 };
 int hashgrid_set_option(hashgrid_t h, int option, int value);
 int hashgrid_get_option(hashgrid_t h, int option, int *value);
+
+/* =======================================================================================
+ * The trainable head behind the encoding: linear layers of any width with their gradients,
+ * and one AdamW step over all of the head's tensors.
+ *
+ * hashgrid_mlp_forward evaluates one fixed head; these calls train a head of any shape:
+ * encode, one hashgrid_linear_forward per layer, one hashgrid_linear_backward per layer
+ * from the last to the first, whose dL_dx is the dL_dout of hashgrid_backward, then one
+ * hashgrid_adamw_step over the weights and biases.
+ * ======================================================================================= */
+
+typedef struct hashgrid_linear_s *hashgrid_linear_t; /* opaque, library-owned */
+
+/* act(z) of a layer and its derivative: NONE z; RELU max(z, 0), derivative 1 for z > 0 else 0;
+ * GELU z (1 + erf(z / sqrt 2)) / 2; SILU z / (1 + exp(-z)). A NaN gives 0 under RELU. */
+enum hashgrid_activation {
+    HASHGRID_ACT_NONE = 0,
+    HASHGRID_ACT_RELU = 1,
+    HASHGRID_ACT_GELU = 2,
+    HASHGRID_ACT_SILU = 3
+};
+
+#define HASHGRID_MAX_WIDTH 65536 /* largest in and out of a layer */
+
+/*
+ * hashgrid_linear_create -- a layer of `in` inputs and `out` outputs (1 <= in, out <=
+ * HASHGRID_MAX_WIDTH) whose operands are of dtype HASHGRID_F16 or HASHGRID_BF16. The handle
+ * holds no weights and no device memory; it may be used from several threads and streams.
+ */
+int hashgrid_linear_create(int in, int out, int dtype, int activation, hashgrid_linear_t *layer);
+int hashgrid_linear_destroy(hashgrid_linear_t layer);
+/* The create arguments, written to the non-NULL pointers (host ints). */
+int hashgrid_linear_params(hashgrid_linear_t layer, int *in, int *out, int *dtype, int *activation);
+
+/*
+ * hashgrid_linear_forward -- N rows through the layer:
+ *   z[n][o] = sum_i x[n][i] w[o][i] + b[o];   y[n][o] = act(z[n][o]) + residual[n][o].
+ *
+ * Products of 16-bit operands are exact and summed in fp32; bias, activation and residual are
+ * applied in fp32, and y (and z) are rounded once, on the way out.
+ *
+ * x: [N, in] of the layer's dtype, rows ldx elements apart; w: [out][in] of the layer's dtype,
+ * contiguous (a torch Linear weight); b: [out] fp32 or NULL; residual: [N, out] of y_dtype,
+ * rows ldr apart, or NULL; y: [N, out] of y_dtype (HASHGRID_F32 or the layer's dtype), rows
+ * ldy apart; z: NULL, or [N, out] contiguous of the layer's dtype, which the backward pass of
+ * a layer with an activation reads. Elements of y's rows beyond `out` are left as they were.
+ * Strides are at least the row's width (any value, odd ones included); 0 <= N < 2^31 - 256.
+ * residual may be y itself (with ldr == ldy); no other output may overlap an input.
+ * device_status: as for hashgrid_mlp_forward (NULL, or a device int the caller sets to 0 and
+ * the kernel sets to 1 if a bounded wait ran out, y being incomplete then).
+ */
+int hashgrid_linear_forward(hashgrid_linear_t layer, const void *x, int64_t ldx, int64_t N, const void *w,
+                            const float *b, const void *residual, int64_t ldr, void *y, int64_t ldy, int y_dtype,
+                            void *z, int *device_status, void *cuda_stream);
+
+/* Bytes of workspace that hashgrid_linear_backward needs for N rows (0 for a NULL layer or an
+ * invalid N). Depends on the layer's sizes and N only. */
+size_t hashgrid_linear_workspace(hashgrid_linear_t layer, int64_t N);
+
+/*
+ * hashgrid_linear_backward -- gradients of a loss with respect to a layer's input, weights and
+ * bias (the residual's gradient is dL_dy itself):
+ *   dz[n][o] = dL_dy[n][o] act'(z[n][o]);   dL_dx[n][i] = sum_o dz[n][o] w[o][i];
+ *   dL_dw[o][i] = sum_n dz[n][o] x[n][i];   dL_db[o] = sum_n dz[n][o].
+ *
+ * dz is rounded to the layer's dtype before it enters the two products (without an activation,
+ * or with RELU, that changes nothing); sums are fp32, and dL_db sums the unrounded dz. All sums
+ * run in a fixed order: equal calls on one kind of device give equal bits.
+ *
+ * dL_dy: [N, out] of the layer's dtype, rows lddy apart; x, ldx, w: as in the forward call; z:
+ * [N, out] contiguous, as the forward call wrote it (NULL with HASHGRID_ACT_NONE). dL_dx:
+ * [N, in] of dx_dtype (HASHGRID_F32, as hashgrid_backward takes it, or the layer's dtype), rows
+ * lddx apart; dL_dw: [out][in] of dw_dtype (HASHGRID_F32 or the layer's dtype), contiguous;
+ * dL_db: [out] fp32. Each of the three may be NULL, and is not computed then; all are
+ * OVERWRITTEN. N = 0 writes zeros to dL_dw and dL_db. No output may overlap an input.
+ * workspace: workspace_bytes >= hashgrid_linear_workspace(layer, N) of device memory that no
+ * other call uses until this one has finished (a captured graph uses it at every replay); its
+ * contents need no preparation and mean nothing afterwards.
+ */
+int hashgrid_linear_backward(hashgrid_linear_t layer, const void *dL_dy, int64_t lddy, const void *x, int64_t ldx,
+                             int64_t N, const void *w, const void *z, void *dL_dx, int64_t lddx, int dx_dtype,
+                             void *dL_dw, int dw_dtype, float *dL_db, void *workspace, size_t workspace_bytes,
+                             int *device_status, void *cuda_stream);
+
+typedef struct hashgrid_adamw_s *hashgrid_adamw_t; /* opaque, library-owned */
+
+#define HASHGRID_ADAMW_BLOCK 256 /* elements of an 8-bit state that share a scale */
+#define HASHGRID_ADAMW_MAX_TENSORS 65536
+
+/* One tensor of an AdamW step: n contiguous elements of each array. The struct is host memory,
+ * read by hashgrid_adamw_create; its pointers are device pointers. */
+struct hashgrid_adamw_tensor {
+    void *param;          /* updated */
+    void *grad;           /* read; cleared when the step's zero_grad is set */
+    void *m, *v;          /* moments of state_dtype; fp32: m and v; E4M3: see below */
+    float *m_scale;       /* E4M3: [ceil(n / 256)] (4-byte aligned); else NULL */
+    float *v_scale;       /* E4M3: [ceil(n / 256)] (4-byte aligned); else NULL */
+    void *copy;           /* NULL, or [n] of copy_dtype: receives the updated parameter, rounded */
+    int64_t n;            /* >= 0 */
+    int32_t param_dtype;  /* HASHGRID_F32, _F16 or _BF16 */
+    int32_t grad_dtype;   /* HASHGRID_F32, _F16 or _BF16 */
+    int32_t state_dtype;  /* HASHGRID_F32 or HASHGRID_E4M3 */
+    int32_t copy_dtype;   /* HASHGRID_F16 or _BF16 (ignored without a copy) */
+    float lr_scale;       /* the tensor's learning rate is lr * lr_scale (a table's is several times a weight's) */
+    float weight_decay;   /* >= 0 */
+};
+
+/*
+ * hashgrid_adamw_create -- checks a list of tensors (1 <= count <= HASHGRID_ADAMW_MAX_TENSORS)
+ * and keeps their addresses. The arrays must stay allocated while the handle is stepped, and
+ * no two of them may overlap. The handle belongs to the device that is current now.
+ */
+int hashgrid_adamw_create(const struct hashgrid_adamw_tensor *tensors, int count, hashgrid_adamw_t *opt);
+int hashgrid_adamw_destroy(hashgrid_adamw_t opt);
+
+/*
+ * hashgrid_adamw_step -- one AdamW step (decoupled weight decay) over all tensors of the list.
+ * Per element, in fp32, each operation rounded to nearest, at step t >= 1:
+ *   m = beta1 m + (1 - beta1) g;   v = beta2 v + (1 - beta2) g^2;
+ *   param = param (1 - lr lr_scale weight_decay)
+ *           - lr lr_scale (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps).
+ * (1 / (1 - beta^t) is computed in fp64 and multiplied as fp32.) Unlike hashgrid_adam_step,
+ * elements with a zero gradient decay too.
+ *
+ * 8-bit states (HASHGRID_E4M3): m is stored as codes c with m = c * m_scale[i / 256], v as
+ * codes of its square root, v = (c * v_scale[i / 256])^2, which halves the range that its 8
+ * bits must span. The step is computed from the fp32 values before they are stored; a block's
+ * new scale is its largest magnitude / 448 and its codes are x * (448 / largest) rounded to
+ * e4m3. A nonzero v is stored as the smallest positive code at least (a v that vanished beside
+ * an m that did not would blow up the next step). m and v that are not finite are stored as
+ * NaN, and stay out of their block's scale; a block whose largest magnitude is below 2^-100 is
+ * stored as zeros. Zeroed codes and scales are the state before step 1.
+ * seed = 0 rounds codes to nearest even; any other seed rounds them stochastically (up with the
+ * probability of the part cut off, in steps of 2^-16), which lets an average move by less than
+ * half a code: the 32 random bits of element i of tensor k are
+ *   mix(lo(i) ^ mix(seed * 0x9E3779B1 + t * 0x85EBCA77 + k * 0xC2B2AE3D + hi(i) * 0x27D4EB2F)),
+ * mix(h): h ^= h >> 16; h *= 0x7FEB352D; h ^= h >> 15; h *= 0x846CA68B; h ^= h >> 16 (all
+ * mod 2^32); the low 16 bits r serve m, the high 16 v, each adding (16 r + 8) / 2^20 of a code.
+ *
+ * device_step: NULL, or a device int64 that the kernel reads t from (then `step` is ignored
+ * and a t < 1 leaves everything as it was), so that a captured graph can be replayed while the
+ * caller counts on the device. 0 <= beta1, beta2 < 1; eps > 0; lr finite. zero_grad != 0 sets
+ * the gradients to zero after they are read.
+ */
+int hashgrid_adamw_step(hashgrid_adamw_t opt, int64_t step, const int64_t *device_step, float lr, float beta1,
+                        float beta2, float eps, uint32_t seed, int zero_grad, void *cuda_stream);
 
 /* Library version string. */
 const char *hashgrid_version(void);

@@ -22,6 +22,14 @@ LIB_PATH = os.path.join(HERE, "libhashgrid_checked.so" if CHECKED else "libhashg
 
 HASHGRID_F32 = 0
 HASHGRID_F16 = 1
+HASHGRID_BF16 = 2
+HASHGRID_E4M3 = 3
+
+HASHGRID_ACT_NONE = 0
+HASHGRID_ACT_RELU = 1
+HASHGRID_ACT_GELU = 2
+HASHGRID_ACT_SILU = 3
+HASHGRID_ADAMW_BLOCK = 256
 
 HASHGRID_OK = 0
 HASHGRID_ERR_ARG = 1
@@ -65,6 +73,15 @@ class HashGridError(RuntimeError):
         self.code = code
 
 
+class AdamwTensor(ctypes.Structure):
+    """``struct hashgrid_adamw_tensor``."""
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("copy", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("state_dtype", ctypes.c_int32), ("copy_dtype", ctypes.c_int32), ("lr_scale", ctypes.c_float),
+                ("weight_decay", ctypes.c_float)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built: run `python multiresolution_hash_grid_b200/build.py"
@@ -89,6 +106,16 @@ def _load() -> ctypes.CDLL:
         "hashgrid_adam_step": (i32, [vp, vp, vp, vp, vp, i64, ctypes.c_float, ctypes.c_float, ctypes.c_float,
                                      ctypes.c_float, i32, vp]),
         "hashgrid_mlp_forward": (i32, [vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "hashgrid_linear_create": (i32, [i32, i32, i32, i32, ctypes.POINTER(vp)]),
+        "hashgrid_linear_destroy": (i32, [vp]),
+        "hashgrid_linear_params": (i32, [vp] + [ctypes.POINTER(i32)] * 4),
+        "hashgrid_linear_forward": (i32, [vp, vp, i64, i64, vp, vp, vp, i64, vp, i64, i32, vp, vp, vp]),
+        "hashgrid_linear_workspace": (sz, [vp, i64]),
+        "hashgrid_linear_backward": (i32, [vp, vp, i64, vp, i64, i64, vp, vp, vp, i64, i32, vp, i32, vp, vp, sz, vp, vp]),
+        "hashgrid_adamw_create": (i32, [ctypes.POINTER(AdamwTensor), i32, ctypes.POINTER(vp)]),
+        "hashgrid_adamw_destroy": (i32, [vp]),
+        "hashgrid_adamw_step": (i32, [vp, i64, vp, ctypes.c_float, ctypes.c_float, ctypes.c_float, ctypes.c_float,
+                                      ctypes.c_uint32, i32, vp]),
         "hashgrid_debug_indices": (i32, [vp, vp, i64, vp, vp]),
         "hashgrid_probe": (i32, [i32, i32, i32, vp, sz, i64, vp, ctypes.POINTER(i64), vp]),
         "hashgrid_last_error": (ctypes.c_char_p, []),
@@ -215,6 +242,59 @@ def hashgrid_debug_indices(h: int, x, N: int, idx_out, stream=None) -> None:
     _check(lib.hashgrid_debug_indices(h, _ptr(x), N, _ptr(idx_out), _stream(stream)))
 
 
+def hashgrid_linear_create(in_features: int, out_features: int, dtype: int = HASHGRID_BF16,
+                           activation: int = HASHGRID_ACT_NONE) -> int:
+    h = ctypes.c_void_p()
+    _check(lib.hashgrid_linear_create(in_features, out_features, dtype, activation, ctypes.byref(h)))
+    return h.value
+
+
+def hashgrid_linear_destroy(layer: int) -> None:
+    _check(lib.hashgrid_linear_destroy(layer))
+
+
+def hashgrid_linear_params(layer: int) -> dict:
+    vals = [ctypes.c_int() for _ in range(4)]
+    _check(lib.hashgrid_linear_params(layer, *[ctypes.byref(v) for v in vals]))
+    return dict(zip(("in", "out", "dtype", "activation"), (v.value for v in vals)))
+
+
+def hashgrid_linear_forward(layer: int, x, ldx: int, N: int, w, b, residual, ldr: int, y, ldy: int, y_dtype: int, z=None,
+                            device_status=None, stream=None) -> None:
+    _check(lib.hashgrid_linear_forward(layer, _ptr(x), ldx, N, _ptr(w), _ptr(b), _ptr(residual), ldr, _ptr(y), ldy,
+                                       y_dtype, _ptr(z), _ptr(device_status), _stream(stream)))
+
+
+def hashgrid_linear_workspace(layer: int, N: int) -> int:
+    return int(lib.hashgrid_linear_workspace(layer, N))
+
+
+def hashgrid_linear_backward(layer: int, dL_dy, lddy: int, x, ldx: int, N: int, w, z, dL_dx, lddx: int, dx_dtype: int,
+                             dL_dw, dw_dtype: int, dL_db, workspace, workspace_bytes: int, device_status=None,
+                             stream=None) -> None:
+    _check(lib.hashgrid_linear_backward(layer, _ptr(dL_dy), lddy, _ptr(x), ldx, N, _ptr(w), _ptr(z), _ptr(dL_dx), lddx,
+                                        dx_dtype, _ptr(dL_dw), dw_dtype, _ptr(dL_db), _ptr(workspace), workspace_bytes,
+                                        _ptr(device_status), _stream(stream)))
+
+
+def hashgrid_adamw_create(tensors) -> int:
+    """``tensors``: AdamwTensor structs (device pointers)."""
+    arr = (AdamwTensor * max(1, len(tensors)))(*tensors)
+    h = ctypes.c_void_p()
+    _check(lib.hashgrid_adamw_create(arr, len(tensors), ctypes.byref(h)))
+    return h.value
+
+
+def hashgrid_adamw_destroy(opt: int) -> None:
+    _check(lib.hashgrid_adamw_destroy(opt))
+
+
+def hashgrid_adamw_step(opt: int, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.99, eps: float = 1e-8,
+                        seed: int = 0, zero_grad: bool = False, device_step=None, stream=None) -> None:
+    _check(lib.hashgrid_adamw_step(opt, step, _ptr(device_step), lr, beta1, beta2, eps, seed & 0xFFFFFFFF,
+                                   1 if zero_grad else 0, _stream(stream)))
+
+
 def hashgrid_probe(kind: int, width: int, pattern: int, buf, buf_bytes: int, ops: int, sink=None,
                    stream=None) -> int:
     """Runs one memory-system probe (include/hashgrid_probe.h); returns the number of lane
@@ -277,3 +357,197 @@ class HashGrid:
         idx = torch.empty((x.shape[0], self.L, 1 << self.D), dtype=torch.int32, device=x.device)
         hashgrid_debug_indices(self.handle, x, x.shape[0], idx, stream)
         return idx
+
+
+def _dtype_code(t, name: str) -> int:
+    """HASHGRID_* code of a torch tensor's type."""
+    code = {"torch.float32": HASHGRID_F32, "torch.float16": HASHGRID_F16, "torch.bfloat16": HASHGRID_BF16,
+            "torch.float8_e4m3fn": HASHGRID_E4M3}.get(str(t.dtype))
+    if code is None:
+        raise HashGridError(HASHGRID_ERR_ARG, f"{name} has type {t.dtype}")
+    return code
+
+
+def _rows(t, n, width: int, dtypes, name: str) -> int:
+    """Checks a [n, width] tensor with contiguous rows and returns its row stride."""
+    if t.dim() != 2 or t.shape[1] != width or (n is not None and t.shape[0] != n):
+        raise HashGridError(HASHGRID_ERR_ARG, f"{name} has shape {tuple(t.shape)}, [{'N' if n is None else n}, {width}] is wanted")
+    if _dtype_code(t, name) not in dtypes:
+        raise HashGridError(HASHGRID_ERR_ARG, f"{name} has type {t.dtype}")
+    if width > 1 and t.stride(1) != 1:
+        raise HashGridError(HASHGRID_ERR_ARG, f"{name}: the elements of a row must be contiguous (strides {t.stride()})")
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def _flat(t, shape, dtypes, name: str) -> None:
+    """Checks a contiguous tensor of the given shape."""
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise HashGridError(HASHGRID_ERR_ARG, f"{name} has shape {tuple(t.shape)}, strides {t.stride()}: contiguous {tuple(shape)} is wanted")
+    if _dtype_code(t, name) not in dtypes:
+        raise HashGridError(HASHGRID_ERR_ARG, f"{name} has type {t.dtype}")
+
+
+class Linear:
+    """A linear layer with its activation and residual, and its gradients (``hashgrid_linear_*``):
+    ``z = x w^T + b``, ``y = act(z) + residual``. Holds a handle only; weights are arguments. Tensors
+    are [N, features] with contiguous rows (any row stride), of the layer's 16-bit type where not
+    said otherwise."""
+
+    def __init__(self, in_features: int, out_features: int, dtype: int = HASHGRID_BF16,
+                 activation: int = HASHGRID_ACT_NONE):
+        self.in_features, self.out_features, self.dtype, self.activation = in_features, out_features, dtype, activation
+        self.handle = hashgrid_linear_create(in_features, out_features, dtype, activation)
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h and lib is not None:
+            lib.hashgrid_linear_destroy(h)
+            self.handle = None
+
+    def _torch_dtype(self):
+        import torch
+        return torch.float16 if self.dtype == HASHGRID_F16 else torch.bfloat16
+
+    def forward(self, x, w, b=None, residual=None, y=None, z=None, device_status=None, stream=None):
+        """Returns y. ``w`` [out, in] contiguous; ``b`` [out] fp32; ``y`` (allocated if None, of ``residual``'s
+        type or else the layer's) and ``residual`` of the layer's type or fp32; ``z``: a contiguous [N, out] tensor
+        that receives the pre-activation, for ``backward``."""
+        import torch
+        N, own = x.shape[0], (self.dtype,)
+        ldx = _rows(x, None, self.in_features, own, "x")
+        _flat(w, (self.out_features, self.in_features), own, "w")
+        if b is not None:
+            _flat(b, (self.out_features,), (HASHGRID_F32,), "b")
+        if y is None:
+            y = torch.empty((N, self.out_features), device=x.device,
+                            dtype=self._torch_dtype() if residual is None else residual.dtype)
+            _record(y, stream)
+        ldy = _rows(y, N, self.out_features, (self.dtype, HASHGRID_F32), "y")
+        y_dtype = _dtype_code(y, "y")
+        ldr = 0 if residual is None else _rows(residual, N, self.out_features, (y_dtype,), "residual")
+        if z is not None:
+            _flat(z, (N, self.out_features), own, "z")
+        hashgrid_linear_forward(self.handle, x, ldx, N, w, b, residual, ldr, y, ldy, y_dtype, z, device_status, stream)
+        return y
+
+    def workspace(self, N: int, device):
+        """Workspace for ``backward`` over up to N rows."""
+        import torch
+        return torch.empty(max(16, hashgrid_linear_workspace(self.handle, N)), dtype=torch.uint8, device=device)
+
+    def backward(self, dL_dy, x, w, z=None, dL_dx=True, dL_dw=True, dL_db=True, workspace=None, device_status=None,
+                 stream=None):
+        """Returns (dL_dx, dL_dw, dL_db). Each is a tensor to write (dL_dx and dL_dw of the layer's type or fp32, dL_db
+        fp32), True to allocate it (the layer's type, fp32, fp32), or None to leave it out. ``z``: what ``forward``
+        wrote (not needed without an activation)."""
+        import torch
+        N, own, either = dL_dy.shape[0], (self.dtype,), (self.dtype, HASHGRID_F32)
+        lddy = _rows(dL_dy, None, self.out_features, own, "dL_dy")
+        ldx = _rows(x, N, self.in_features, own, "x")
+        _flat(w, (self.out_features, self.in_features), own, "w")
+        if z is not None:
+            _flat(z, (N, self.out_features), own, "z")
+        if dL_dx is True:
+            dL_dx = torch.empty((N, self.in_features), device=x.device, dtype=self._torch_dtype())
+            _record(dL_dx, stream)
+        if dL_dw is True:
+            dL_dw = torch.empty((self.out_features, self.in_features), device=x.device, dtype=torch.float32)
+            _record(dL_dw, stream)
+        if dL_db is True:
+            dL_db = torch.empty(self.out_features, device=x.device, dtype=torch.float32)
+            _record(dL_db, stream)
+        lddx = 0 if dL_dx is None else _rows(dL_dx, N, self.in_features, either, "dL_dx")
+        if dL_dw is not None:
+            _flat(dL_dw, (self.out_features, self.in_features), either, "dL_dw")
+        if dL_db is not None:
+            _flat(dL_db, (self.out_features,), (HASHGRID_F32,), "dL_db")
+        if workspace is None:
+            workspace = self.workspace(N, x.device)
+            _record(workspace, stream)
+        hashgrid_linear_backward(self.handle, dL_dy, lddy, x, ldx, N, w, z, dL_dx, lddx,
+                                 HASHGRID_F32 if dL_dx is None else _dtype_code(dL_dx, "dL_dx"), dL_dw,
+                                 HASHGRID_F32 if dL_dw is None else _dtype_code(dL_dw, "dL_dw"), dL_db, workspace,
+                                 workspace.numel() * workspace.element_size(), device_status, stream)
+        return dL_dx, dL_dw, dL_db
+
+
+def _record(t, stream) -> None:
+    """A tensor that was allocated here is used on ``stream``: torch must not hand it out again before."""
+    if stream is None or not t.is_cuda:
+        return
+    import torch
+    t.record_stream(torch.cuda.ExternalStream(stream, device=t.device) if isinstance(stream, int) else stream)
+
+
+class AdamW:
+    """One AdamW step over a list of tensors (``hashgrid_adamw_*``). Holds references to the tensors: they are
+    updated in place, and the gradients are read from the same tensors at every step.
+
+    params, grads: contiguous tensors, fp32, fp16 or bf16. m, v: the moments, allocated as zeros if None: fp32, or
+    with ``bits=8`` e4m3 codes (torch.float8_e4m3fn or uint8) with ``block_scales = (m_scales, v_scales)``, one fp32
+    tensor of ceil(n / 256) values per tensor each. copies: 16-bit tensors that receive the updated parameters.
+    lr_scale, weight_decay: one number, or one per tensor."""
+
+    def __init__(self, params, grads, m=None, v=None, bits: int = 32, block_scales=None, copies=None, lr_scale=1.0,
+                 weight_decay=0.0):
+        import torch
+        params, grads = list(params), list(grads)
+        count = len(params)
+        if (m is None) != (v is None):
+            raise HashGridError(HASHGRID_ERR_ARG, "m and v come together")
+        if bits not in (8, 32):
+            raise HashGridError(HASHGRID_ERR_ARG, f"bits = {bits} is neither 8 nor 32")
+        if m is None:
+            kind = torch.float32 if bits == 32 else torch.float8_e4m3fn
+            m, v = ([torch.zeros(p.shape, dtype=torch.uint8 if bits == 8 else kind, device=p.device).view(kind)
+                     for p in params] for _ in range(2))
+        m, v = list(m), list(v)
+        coded = [t.element_size() == 1 for t in m]
+        if block_scales is None and any(coded):
+            block_scales = tuple([torch.zeros(-(-p.numel() // HASHGRID_ADAMW_BLOCK), device=p.device) for p in params]
+                                 for _ in range(2))
+        ms, vs = (list(block_scales[0]), list(block_scales[1])) if block_scales is not None else ([None] * count,) * 2
+        copies = list(copies) if copies is not None else [None] * count
+        lr_scale = [float(lr_scale)] * count if isinstance(lr_scale, (int, float)) else [float(s) for s in lr_scale]
+        weight_decay = ([float(weight_decay)] * count if isinstance(weight_decay, (int, float))
+                        else [float(d) for d in weight_decay])
+        for name, lst in (("grads", grads), ("m", m), ("v", v), ("block_scales", ms), ("block_scales", vs),
+                          ("copies", copies), ("lr_scale", lr_scale), ("weight_decay", weight_decay)):
+            if len(lst) != count:
+                raise HashGridError(HASHGRID_ERR_ARG, f"{name}: {len(lst)} entries for {count} parameters")
+        self.params, self.grads, self.m, self.v = params, grads, m, v
+        self.m_scales, self.v_scales, self.copies = ms, vs, copies
+        tensors = []
+        for k, p in enumerate(params):
+            n = p.numel()
+            for name, t in (("param", p), ("grad", grads[k]), ("m", m[k]), ("v", v[k]), ("copy", copies[k])):
+                if t is not None and (t.numel() != n or not t.is_contiguous()):
+                    raise HashGridError(HASHGRID_ERR_ARG, f"tensor {k}: {name} has shape {tuple(t.shape)}, strides {t.stride()}: "
+                                                          f"{n} contiguous elements are wanted")
+            for t in (m[k], v[k]):
+                if (t.element_size() == 1) != coded[k] or not (coded[k] or t.dtype == torch.float32) or                         (coded[k] and t.dtype not in (torch.float8_e4m3fn, torch.uint8)):
+                    raise HashGridError(HASHGRID_ERR_ARG, f"tensor {k}: states of type {m[k].dtype} and {v[k].dtype}")
+            blocks = -(-n // HASHGRID_ADAMW_BLOCK)
+            for t in (ms[k], vs[k]):
+                if coded[k] and (t is None or t.dtype != torch.float32 or t.numel() != blocks or not t.is_contiguous()):
+                    raise HashGridError(HASHGRID_ERR_ARG, f"tensor {k}: {blocks} contiguous fp32 scales are wanted")
+            tensors.append(AdamwTensor(
+                _ptr(p), _ptr(grads[k]), _ptr(m[k]), _ptr(v[k]), _ptr(ms[k]) if coded[k] else None,
+                _ptr(vs[k]) if coded[k] else None, _ptr(copies[k]), n, _dtype_code(p, "param"), _dtype_code(grads[k], "grad"),
+                HASHGRID_E4M3 if coded[k] else HASHGRID_F32,
+                HASHGRID_BF16 if copies[k] is None else _dtype_code(copies[k], "copy"), lr_scale[k], weight_decay[k]))
+        self.handle = hashgrid_adamw_create(tensors)
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h and lib is not None:
+            lib.hashgrid_adamw_destroy(h)
+            self.handle = None
+
+    def step(self, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.99, eps: float = 1e-8, seed: int = 0,
+             zero_grad: bool = False, device_step=None, stream=None) -> None:
+        """One step, t = ``step`` (from 1 on), or the int64 CUDA tensor ``device_step``'s value."""
+        if device_step is not None and not isinstance(device_step, int) and (
+                str(device_step.dtype) != "torch.int64" or device_step.numel() != 1):
+            raise HashGridError(HASHGRID_ERR_ARG, "device_step is one int64")
+        hashgrid_adamw_step(self.handle, step, lr, beta1, beta2, eps, seed, zero_grad, device_step, stream)

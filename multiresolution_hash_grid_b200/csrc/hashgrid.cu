@@ -19,9 +19,12 @@
 #include <new>
 #include <string>
 #include <type_traits>
+#include <vector>
 
 #include "hashgrid.h"
+#include "hg_adamw.cuh"
 #include "hg_device.cuh"
+#include "hg_linear.cuh"
 #include "hg_mlp.cuh"
 #include "hg_nd.cuh"
 #include "hg_probe.cuh"
@@ -41,6 +44,20 @@ struct hashgrid_s {
     int backward_mode;    // HASHGRID_BACKWARD_*
     int schedule;         // HASHGRID_SCHEDULE_*
     hg::LevelParams lp;
+};
+
+struct hashgrid_linear_s {
+    int in, out, dtype, act;
+};
+
+struct hashgrid_adamw_s {
+    int device;
+    std::vector<hg::adamw::Tensor> tensors;  // `first` counts blocks within the tensor's launch
+    struct Launch {
+        int begin, count;  // tensors
+        uint32_t blocks;
+    };
+    std::vector<Launch> launches;
 };
 
 namespace {
@@ -100,10 +117,10 @@ PFN_memGetAddressRange address_range_fn() {
 // Checks one buffer argument that the call will access over [p, p + bytes): not NULL,
 // 16-byte aligned, device memory of the current device or managed memory, and (where the
 // driver reports the allocation's range) the whole extent inside the allocation.
-int check_buffer(const void* p, size_t bytes, const char* name) {
+int check_buffer(const void* p, size_t bytes, const char* name, size_t align = 16) {
     if (p == nullptr) return fail(HASHGRID_ERR_ARG, "%s is NULL", name);
-    if (reinterpret_cast<uintptr_t>(p) % 16 != 0)
-        return fail(HASHGRID_ERR_ALIGN, "%s (%p) is not 16-byte aligned", name, p);
+    if (reinterpret_cast<uintptr_t>(p) % align != 0)
+        return fail(HASHGRID_ERR_ALIGN, "%s (%p) is not %zu-byte aligned", name, p, align);
     cudaPointerAttributes a;
     cudaError_t e = cudaPointerGetAttributes(&a, p);
     if (e != cudaSuccess) {
@@ -552,7 +569,8 @@ int run_checked(cudaStream_t s, std::initializer_list<CheckBuf> bufs, const char
     if (flags != 0) {
         const unsigned int zero = 0;
         cudaMemcpyToSymbol(hg::g_check_flags, &zero, sizeof zero);
-        static const char* names[hg::kChkRoles] = {"x", "table", "output", "dL_dout", "dL_dtable", "adam_m", "adam_v"};
+        static const char* names[hg::kChkRoles] = {"x", "table", "output", "dL_dout", "dL_dtable", "adam_m", "adam_v",
+                                                   "weights", "bias", "residual", "z", "workspace", "AdamW tensor"};
         std::string which;
         for (int i = 0; i < hg::kChkRoles; ++i)
             if (flags & (1u << i)) which += std::string(which.empty() ? "" : ", ") + names[i];
@@ -570,6 +588,181 @@ int run_checked(cudaStream_t s, std::initializer_list<CheckBuf> bufs, const char
 
 size_t table_bytes(const hashgrid_s* h) {
     return (size_t)h->L * ((size_t)1 << h->log2T) * (size_t)h->F * (h->dtype == HASHGRID_F16 ? 2 : 4);
+}
+
+int check_layer(const hashgrid_linear_s* layer) {
+    if (layer == nullptr) return fail(HASHGRID_ERR_ARG, "layer is NULL");
+    return ok();
+}
+
+// Bytes of a row-major [rows, cols] array whose rows lie ld elements apart.
+size_t strided_bytes(int64_t rows, int64_t cols, int64_t ld, size_t elem) {
+    return rows == 0 ? 0 : ((size_t)(rows - 1) * (size_t)ld + (size_t)cols) * elem;
+}
+
+// One strided array of a layer call: its row stride and then its extent.
+int check_rows(const void* p, int64_t rows, int64_t cols, int64_t ld, size_t elem, const char* name) {
+    if (ld < cols) return fail(HASHGRID_ERR_ARG, "%s: row stride %lld is below its width %lld", name, (long long)ld, (long long)cols);
+    if (ld > ((int64_t)1 << 40)) return fail(HASHGRID_ERR_ARG, "%s: row stride %lld is too large", name, (long long)ld);
+    return check_buffer(p, strided_bytes(rows, cols, ld, elem), name);
+}
+
+constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 256;
+
+int check_row_count(int64_t N) {
+    if (N < 0 || N >= kMaxRows) return fail(HASHGRID_ERR_ARG, "N = %lld outside [0, 2^31 - 256)", (long long)N);
+    return ok();
+}
+
+int check_out_type(const hashgrid_linear_s* layer, int dtype, const char* name) {
+    if (dtype != HASHGRID_F32 && dtype != layer->dtype)
+        return fail(HASHGRID_ERR_ARG, "%s = %d is neither HASHGRID_F32 nor the layer's dtype %d", name, dtype, layer->dtype);
+    return ok();
+}
+
+// The backward pass's workspace: dz (where it has to be computed), then the parts of db.
+struct LinearWork {
+    int64_t lddz;   // elements
+    int parts;      // row shares of the db sums
+    size_t dz, sums, bytes;  // offsets, total
+};
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+LinearWork linear_work(const hashgrid_linear_s* l, int64_t N) {
+    LinearWork w;
+    w.lddz = (l->out + 7) / 8 * 8;
+    w.parts = (int)std::min<int64_t>(256, (N + 63) / 64);
+    w.dz = 0;
+    w.sums = l->act == HASHGRID_ACT_NONE ? 0 : align256((size_t)N * w.lddz * 2);
+    w.bytes = w.sums + align256((size_t)w.parts * l->out * sizeof(float));
+    return w;
+}
+
+template <typename T>
+int launch_product(const hg::linear::Operand& A, const hg::linear::Operand& B, int64_t M, int64_t N, int64_t K,
+                   const hg::linear::Epilogue& e, const char* what, cudaStream_t s) {
+    const dim3 grid((unsigned)((M + hg::linear::kTileM - 1) / hg::linear::kTileM),
+                    (unsigned)((N + hg::linear::kTileN - 1) / hg::linear::kTileN));
+    hg::linear::product_kernel<T><<<grid, 256, 0, s>>>(A, B, M, N, K, e);
+    return launch_status(what);
+}
+
+template <typename T>
+int launch_linear_forward(const hashgrid_linear_s* l, const void* x, int64_t ldx, int64_t N, const void* w,
+                          const hg::linear::Epilogue& e, int* status, cudaStream_t s) {
+    (void)status;
+    return launch_product<T>({x, ldx, 1}, {w, l->in, 1}, N, l->out, l->in, e, "linear_forward", s);
+}
+
+template <typename T>
+int launch_linear_backward(const hashgrid_linear_s* l, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                           int64_t N, const void* w, const void* z, void* dx, int64_t lddx, int dx_dtype, void* dw,
+                           int dw_dtype, float* db, char* work, int* status, cudaStream_t s) {
+    (void)status;
+    const LinearWork lw = linear_work(l, N);
+    const void* dz = dy;
+    int64_t lddz = lddy;
+    const bool convert = l->act != HASHGRID_ACT_NONE && (dx != nullptr || dw != nullptr);
+    if (convert || db != nullptr) {
+        T* to = convert ? reinterpret_cast<T*>(work + lw.dz) : nullptr;
+        float* sums = db != nullptr ? reinterpret_cast<float*>(work + lw.sums) : nullptr;
+        const dim3 grid((unsigned)((l->out + 31) / 32), (unsigned)lw.parts);
+        hg::linear::slope_kernel<T><<<grid, 256, 0, s>>>(static_cast<const T*>(dy), lddy, static_cast<const T*>(z), N,
+                                                        l->out, l->act, to, lw.lddz, sums);
+        if (int rc = launch_status("linear_backward")) return rc;
+        if (convert) {
+            dz = to;
+            lddz = lw.lddz;
+        }
+        if (db != nullptr) {
+            hg::linear::sum_parts_kernel<<<(unsigned)((l->out + 255) / 256), 256, 0, s>>>(sums, lw.parts, l->out, db);
+            if (int rc = launch_status("linear_backward")) return rc;
+        }
+    }
+    if (dx != nullptr) {
+        const hg::linear::Epilogue e{nullptr, nullptr, dx, nullptr, 0, lddx, 0, dx_dtype == HASHGRID_F32, hg::linear::kNoAct};
+        if (int rc = launch_product<T>({dz, lddz, 1}, {w, 1, l->in}, N, l->in, l->out, e, "linear_backward", s)) return rc;
+    }
+    if (dw != nullptr) {
+        const hg::linear::Epilogue e{nullptr, nullptr, dw, nullptr, 0, l->in, 0, dw_dtype == HASHGRID_F32, hg::linear::kNoAct};
+        if (int rc = launch_product<T>({dz, 1, lddz}, {x, 1, ldx}, l->out, l->in, N, e, "linear_backward", s)) return rc;
+    }
+    return ok();
+}
+
+int adamw_bytes(int dtype) { return dtype == HASHGRID_F32 ? 4 : dtype == HASHGRID_E4M3 ? 1 : 2; }
+
+bool float_type(int dtype) { return dtype == HASHGRID_F32 || dtype == HASHGRID_F16 || dtype == HASHGRID_BF16; }
+
+// Checks one tensor of an AdamW list.
+int check_adamw_tensor(const hashgrid_adamw_tensor& t, int k) {
+    char name[64];
+    if (t.n < 0 || t.n >= ((int64_t)1 << 38)) return fail(HASHGRID_ERR_ARG, "tensor %d: n = %lld outside [0, 2^38)", k, (long long)t.n);
+    if (!float_type(t.param_dtype) || !float_type(t.grad_dtype))
+        return fail(HASHGRID_ERR_ARG, "tensor %d: param_dtype %d and grad_dtype %d must be HASHGRID_F32, _F16 or _BF16", k, t.param_dtype, t.grad_dtype);
+    if (t.state_dtype != HASHGRID_F32 && t.state_dtype != HASHGRID_E4M3)
+        return fail(HASHGRID_ERR_ARG, "tensor %d: state_dtype %d is neither HASHGRID_F32 nor HASHGRID_E4M3", k, t.state_dtype);
+    if (t.copy != nullptr && t.copy_dtype != HASHGRID_F16 && t.copy_dtype != HASHGRID_BF16)
+        return fail(HASHGRID_ERR_ARG, "tensor %d: copy_dtype %d is neither HASHGRID_F16 nor HASHGRID_BF16", k, t.copy_dtype);
+    if (!std::isfinite(t.lr_scale) || !std::isfinite(t.weight_decay) || t.weight_decay < 0.f)
+        return fail(HASHGRID_ERR_ARG, "tensor %d: lr_scale %g and weight_decay %g must be finite, weight_decay >= 0", k, t.lr_scale, t.weight_decay);
+    const bool coded = t.state_dtype == HASHGRID_E4M3;
+    if (!coded && (t.m_scale != nullptr || t.v_scale != nullptr))
+        return fail(HASHGRID_ERR_ARG, "tensor %d: fp32 states have no scales", k);
+    if (t.n == 0) return ok();
+    const size_t n = (size_t)t.n, scales = (n + HASHGRID_ADAMW_BLOCK - 1) / HASHGRID_ADAMW_BLOCK * sizeof(float);
+    struct { const void* p; size_t bytes; const char* what; size_t align; bool need; } arrays[] = {
+        {t.param, n * adamw_bytes(t.param_dtype), "param", 16, true},
+        {t.grad, n * adamw_bytes(t.grad_dtype), "grad", 16, true},
+        {t.m, n * adamw_bytes(t.state_dtype), "m", 16, true},
+        {t.v, n * adamw_bytes(t.state_dtype), "v", 16, true},
+        {t.m_scale, scales, "m_scale", 4, coded},
+        {t.v_scale, scales, "v_scale", 4, coded},
+        {t.copy, n * 2, "copy", 16, t.copy != nullptr},
+    };
+    for (const auto& a : arrays) {
+        if (!a.need) continue;
+        snprintf(name, sizeof name, "tensor %d: %s", k, a.what);
+        if (int rc = check_buffer(a.p, a.bytes, name, a.align)) return rc;
+    }
+    return ok();
+}
+
+// No two arrays of a list may share bytes: the kernel's warps run in no order.
+int check_adamw_overlap(const hashgrid_adamw_tensor* tensors, int count) {
+    struct Range { uintptr_t lo, hi; int k; };
+    std::vector<Range> r;
+    for (int k = 0; k < count; ++k) {
+        const hashgrid_adamw_tensor& t = tensors[k];
+        const size_t n = (size_t)t.n, scales = (n + HASHGRID_ADAMW_BLOCK - 1) / HASHGRID_ADAMW_BLOCK * sizeof(float);
+        auto add = [&](const void* p, size_t bytes) {
+            if (p != nullptr && bytes != 0) r.push_back({(uintptr_t)p, (uintptr_t)p + bytes, k});
+        };
+        add(t.param, n * adamw_bytes(t.param_dtype));
+        add(t.grad, n * adamw_bytes(t.grad_dtype));
+        add(t.m, n * adamw_bytes(t.state_dtype));
+        add(t.v, n * adamw_bytes(t.state_dtype));
+        add(t.m_scale, scales);
+        add(t.v_scale, scales);
+        add(t.copy, n * 2);
+    }
+    std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+    for (size_t i = 1; i < r.size(); ++i)
+        if (r[i].lo < r[i - 1].hi)
+            return fail(HASHGRID_ERR_ARG, "arrays of tensors %d and %d overlap", r[i - 1].k, r[i].k);
+    return ok();
+}
+
+template <int kCap>
+int launch_adamw(const hashgrid_adamw_s* o, const hashgrid_adamw_s::Launch& l, hg::adamw::Params a, cudaStream_t s) {
+    hg::adamw::List<kCap> list;
+    list.count = (uint32_t)l.count;
+    list.blocks = l.blocks;
+    std::memcpy(list.t, o->tensors.data() + l.begin, sizeof(hg::adamw::Tensor) * l.count);
+    const unsigned blocks = (l.blocks + hg::adamw::kWarps - 1) / hg::adamw::kWarps;
+    hg::adamw::step_kernel<kCap><<<blocks, 32 * hg::adamw::kWarps, 0, s>>>(list, a);
+    return launch_status("adamw_step");
 }
 
 }  // namespace
@@ -913,6 +1106,224 @@ int hashgrid_debug_indices(hashgrid_t h, const float* x, int64_t N, uint32_t* id
         else
             hg::indices_kernel<<<(unsigned)blocks, threads, 0, s>>>(h->lp, x, N, idx_out);
         return launch_status("debug_indices");
+    });
+}
+
+int hashgrid_linear_create(int in, int out, int dtype, int activation, hashgrid_linear_t* layer) {
+    if (layer == nullptr) return fail(HASHGRID_ERR_ARG, "layer handle pointer is NULL");
+    *layer = nullptr;
+    if (in < 1 || in > HASHGRID_MAX_WIDTH || out < 1 || out > HASHGRID_MAX_WIDTH)
+        return fail(HASHGRID_ERR_ARG, "in = %d and out = %d must lie in [1, %d]", in, out, HASHGRID_MAX_WIDTH);
+    if (dtype != HASHGRID_F16 && dtype != HASHGRID_BF16)
+        return fail(HASHGRID_ERR_ARG, "dtype = %d is neither HASHGRID_F16 nor HASHGRID_BF16", dtype);
+    if (activation < HASHGRID_ACT_NONE || activation > HASHGRID_ACT_SILU)
+        return fail(HASHGRID_ERR_ARG, "activation = %d is not a HASHGRID_ACT_* value", activation);
+    hashgrid_linear_s* l = new (std::nothrow) hashgrid_linear_s;
+    if (l == nullptr) return fail(HASHGRID_ERR_OOM, "out of host memory");
+    l->in = in;
+    l->out = out;
+    l->dtype = dtype;
+    l->act = activation;
+    *layer = l;
+    return ok();
+}
+
+int hashgrid_linear_destroy(hashgrid_linear_t layer) {
+    delete layer;
+    return ok();
+}
+
+int hashgrid_linear_params(hashgrid_linear_t l, int* in, int* out, int* dtype, int* activation) {
+    if (int rc = check_layer(l)) return rc;
+    if (in) *in = l->in;
+    if (out) *out = l->out;
+    if (dtype) *dtype = l->dtype;
+    if (activation) *activation = l->act;
+    return ok();
+}
+
+int hashgrid_linear_forward(hashgrid_linear_t l, const void* x, int64_t ldx, int64_t N, const void* w, const float* b,
+                            const void* residual, int64_t ldr, void* y, int64_t ldy, int y_dtype, void* z,
+                            int* device_status, void* cuda_stream) {
+    if (int rc = check_layer(l)) return rc;
+    if (int rc = check_row_count(N)) return rc;
+    if (int rc = check_out_type(l, y_dtype, "y_dtype")) return rc;
+    if (N == 0) return ok();
+    const size_t ys = y_dtype == HASHGRID_F32 ? 4 : 2;
+    if (int rc = check_rows(x, N, l->in, ldx, 2, "x")) return rc;
+    if (int rc = check_buffer(w, (size_t)l->in * l->out * 2, "w")) return rc;
+    if (b != nullptr)
+        if (int rc = check_buffer(b, (size_t)l->out * sizeof(float), "b")) return rc;
+    if (residual != nullptr)
+        if (int rc = check_rows(residual, N, l->out, ldr, ys, "residual")) return rc;
+    if (int rc = check_rows(y, N, l->out, ldy, ys, "y")) return rc;
+    if (z != nullptr)
+        if (int rc = check_buffer(z, (size_t)N * l->out * 2, "z")) return rc;
+    if (device_status != nullptr)
+        if (int rc = check_buffer(device_status, sizeof(int), "device_status")) return rc;
+    const hg::linear::Epilogue e{b, residual, y, z, ldr, ldy, l->out, y_dtype == HASHGRID_F32, l->act};
+    cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+    return run_checked(s, {{hg::kChkX, x, strided_bytes(N, l->in, ldx, 2)}, {hg::kChkWeights, w, (size_t)l->in * l->out * 2},
+                           {hg::kChkBias, b, (size_t)l->out * sizeof(float)}, {hg::kChkResidual, residual, strided_bytes(N, l->out, ldr, ys)},
+                           {hg::kChkOut, y, strided_bytes(N, l->out, ldy, ys)}, {hg::kChkZ, z, (size_t)N * l->out * 2}},
+                       "linear_forward", [&]() -> int {
+        return l->dtype == HASHGRID_F16 ? launch_linear_forward<__half>(l, x, ldx, N, w, e, device_status, s)
+                                        : launch_linear_forward<__nv_bfloat16>(l, x, ldx, N, w, e, device_status, s);
+    });
+}
+
+size_t hashgrid_linear_workspace(hashgrid_linear_t layer, int64_t N) {
+    if (layer == nullptr || N < 1 || N >= kMaxRows) return 0;
+    return linear_work(layer, N).bytes;
+}
+
+int hashgrid_linear_backward(hashgrid_linear_t l, const void* dL_dy, int64_t lddy, const void* x, int64_t ldx, int64_t N,
+                             const void* w, const void* z, void* dL_dx, int64_t lddx, int dx_dtype, void* dL_dw,
+                             int dw_dtype, float* dL_db, void* workspace, size_t workspace_bytes, int* device_status,
+                             void* cuda_stream) {
+    if (int rc = check_layer(l)) return rc;
+    if (int rc = check_row_count(N)) return rc;
+    if (int rc = check_out_type(l, dx_dtype, "dx_dtype")) return rc;
+    if (int rc = check_out_type(l, dw_dtype, "dw_dtype")) return rc;
+    const size_t xs = dx_dtype == HASHGRID_F32 ? 4 : 2, wb = (size_t)l->in * l->out * (dw_dtype == HASHGRID_F32 ? 4 : 2);
+    const size_t bb = (size_t)l->out * sizeof(float);
+    if (dL_dw != nullptr)
+        if (int rc = check_buffer(dL_dw, wb, "dL_dw")) return rc;
+    if (dL_db != nullptr)
+        if (int rc = check_buffer(dL_db, bb, "dL_db")) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+    if (N == 0) {
+        if (dL_dw != nullptr && cudaMemsetAsync(dL_dw, 0, wb, s) != cudaSuccess) return launch_status("linear_backward");
+        if (dL_db != nullptr && cudaMemsetAsync(dL_db, 0, bb, s) != cudaSuccess) return launch_status("linear_backward");
+        return ok();
+    }
+    if (dL_dx == nullptr && dL_dw == nullptr && dL_db == nullptr) return ok();
+    if (int rc = check_rows(dL_dy, N, l->out, lddy, 2, "dL_dy")) return rc;
+    if (dL_dw != nullptr)
+        if (int rc = check_rows(x, N, l->in, ldx, 2, "x")) return rc;
+    if (dL_dx != nullptr) {
+        if (int rc = check_buffer(w, (size_t)l->in * l->out * 2, "w")) return rc;
+        if (int rc = check_rows(dL_dx, N, l->in, lddx, xs, "dL_dx")) return rc;
+    }
+    if (l->act != HASHGRID_ACT_NONE)
+        if (int rc = check_buffer(z, (size_t)N * l->out * 2, "z")) return rc;
+    const size_t need = hashgrid_linear_workspace(l, N);
+    if (workspace_bytes < need)
+        return fail(HASHGRID_ERR_ARG, "workspace of %zu bytes, %zu are needed for N = %lld", workspace_bytes, need, (long long)N);
+    if (int rc = check_buffer(workspace, need, "workspace")) return rc;
+    if (device_status != nullptr)
+        if (int rc = check_buffer(device_status, sizeof(int), "device_status")) return rc;
+    return run_checked(s, {{hg::kChkX, x, strided_bytes(N, l->in, ldx, 2)}, {hg::kChkWeights, w, (size_t)l->in * l->out * 2},
+                           {hg::kChkBias, dL_db, bb}, {hg::kChkDout, dL_dy, strided_bytes(N, l->out, lddy, 2)},
+                           {hg::kChkZ, z, (size_t)N * l->out * 2}, {hg::kChkWork, workspace, need}},
+                       "linear_backward", [&]() -> int {
+        char* ws = static_cast<char*>(workspace);
+        return l->dtype == HASHGRID_F16
+                   ? launch_linear_backward<__half>(l, dL_dy, lddy, x, ldx, N, w, z, dL_dx, lddx, dx_dtype, dL_dw, dw_dtype, dL_db, ws, device_status, s)
+                   : launch_linear_backward<__nv_bfloat16>(l, dL_dy, lddy, x, ldx, N, w, z, dL_dx, lddx, dx_dtype, dL_dw, dw_dtype, dL_db, ws, device_status, s);
+    });
+}
+
+int hashgrid_adamw_create(const hashgrid_adamw_tensor* tensors, int count, hashgrid_adamw_t* opt) {
+    if (opt == nullptr) return fail(HASHGRID_ERR_ARG, "optimiser handle pointer is NULL");
+    *opt = nullptr;
+    if (tensors == nullptr) return fail(HASHGRID_ERR_ARG, "tensors is NULL");
+    if (count < 1 || count > HASHGRID_ADAMW_MAX_TENSORS)
+        return fail(HASHGRID_ERR_ARG, "count = %d outside [1, %d]", count, HASHGRID_ADAMW_MAX_TENSORS);
+    for (int k = 0; k < count; ++k)
+        if (int rc = check_adamw_tensor(tensors[k], k)) return rc;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return fail(HASHGRID_ERR_CUDA, "cudaGetDevice failed");
+    }
+    try {
+        if (int rc = check_adamw_overlap(tensors, count)) return rc;
+        auto* o = new hashgrid_adamw_s;
+        *opt = o;
+        o->device = dev;
+        constexpr uint64_t kMostBlocks = (uint64_t)1 << 31;  // 256-element blocks of one launch
+        uint64_t blocks = 0;
+        int begin = 0;
+        for (int k = 0; k < count; ++k) {
+            const hashgrid_adamw_tensor& t = tensors[k];
+            if (t.n == 0) continue;
+            const uint64_t own = ((uint64_t)t.n + HASHGRID_ADAMW_BLOCK - 1) / HASHGRID_ADAMW_BLOCK;
+            const int have = (int)o->tensors.size();
+            if (have > begin && (have - begin == hg::adamw::kLarge || blocks + own > kMostBlocks)) {
+                o->launches.push_back({begin, have - begin, (uint32_t)blocks});
+                begin = have;
+                blocks = 0;
+            }
+            hg::adamw::Tensor d;
+            d.p = t.param;
+            d.g = t.grad;
+            d.m = t.m;
+            d.v = t.v;
+            d.ms = t.m_scale;
+            d.vs = t.v_scale;
+            d.copy = t.copy;
+            d.n = t.n;
+            d.first = (uint32_t)blocks;
+            d.types = (uint32_t)t.param_dtype | (uint32_t)t.grad_dtype << 4 | (uint32_t)t.state_dtype << 8 |
+                      (uint32_t)(t.copy ? t.copy_dtype : (int)hg::adamw::kNone) << 12 | (uint32_t)k << 16;
+            d.lr_scale = t.lr_scale;
+            d.decay = t.weight_decay;
+            o->tensors.push_back(d);
+            blocks += own;
+        }
+        if ((int)o->tensors.size() > begin) o->launches.push_back({begin, (int)o->tensors.size() - begin, (uint32_t)blocks});
+    } catch (const std::bad_alloc&) {
+        delete *opt;
+        *opt = nullptr;
+        return fail(HASHGRID_ERR_OOM, "out of host memory");
+    }
+    return ok();
+}
+
+int hashgrid_adamw_destroy(hashgrid_adamw_t opt) {
+    delete opt;
+    return ok();
+}
+
+int hashgrid_adamw_step(hashgrid_adamw_t o, int64_t step, const int64_t* device_step, float lr, float beta1, float beta2,
+                        float eps, uint32_t seed, int zero_grad, void* cuda_stream) {
+    if (o == nullptr) return fail(HASHGRID_ERR_ARG, "optimiser handle is NULL");
+    if (device_step == nullptr && step < 1) return fail(HASHGRID_ERR_ARG, "step = %lld must be >= 1", (long long)step);
+    if (!(beta1 >= 0.f && beta1 < 1.f) || !(beta2 >= 0.f && beta2 < 1.f))
+        return fail(HASHGRID_ERR_ARG, "betas (%g, %g) must lie in [0, 1)", beta1, beta2);
+    if (!(eps > 0.f) || !std::isfinite(eps) || !std::isfinite(lr))
+        return fail(HASHGRID_ERR_ARG, "lr = %g and eps = %g must be finite, eps > 0", lr, eps);
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return fail(HASHGRID_ERR_CUDA, "cudaGetDevice failed");
+    }
+    if (dev != o->device) return fail(HASHGRID_ERR_ARG, "the tensors live on device %d but device %d is current", o->device, dev);
+    if (device_step != nullptr)
+        if (int rc = check_buffer(device_step, sizeof(int64_t), "device_step", 8)) return rc;
+    hg::adamw::Params a;
+    a.lr = lr;
+    a.b1 = beta1;
+    a.b2 = beta2;
+    a.o1 = (float)(1.0 - (double)beta1);
+    a.o2 = (float)(1.0 - (double)beta2);
+    a.eps = eps;
+    a.db1 = beta1;
+    a.db2 = beta2;
+    a.c1 = device_step ? 0.f : (float)(1.0 / (1.0 - std::pow((double)beta1, (double)step)));
+    a.c2 = device_step ? 0.f : (float)(1.0 / (1.0 - std::pow((double)beta2, (double)step)));
+    a.seed = seed;
+    a.step = (uint32_t)step;
+    a.zero_grad = zero_grad;
+    a.device_step = device_step;
+    cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+    return run_checked(s, {}, "adamw_step", [&]() -> int {
+        for (const auto& l : o->launches)
+            if (int rc = l.count <= hg::adamw::kSmall ? launch_adamw<hg::adamw::kSmall>(o, l, a, s)
+                                                      : launch_adamw<hg::adamw::kLarge>(o, l, a, s))
+                return rc;
+        return ok();
     });
 }
 

@@ -23,7 +23,13 @@ enum CheckRole {
     kChkGrad = 4,   // table gradient (reduced into; Adam reads and may clear it)
     kChkM = 5,      // Adam first moment
     kChkV = 6,      // Adam second moment
-    kChkRoles = 7
+    kChkWeights = 7,   // layer weights (read)
+    kChkBias = 8,      // bias (read) or its gradient (written)
+    kChkResidual = 9,  // residual rows (read)
+    kChkZ = 10,        // pre-activation rows (written, or read by the backward pass)
+    kChkWork = 11,     // workspace
+    kChkAdamw = 12,    // any array of an AdamW list (held against its own length)
+    kChkRoles = 13
 };
 
 struct CheckRanges {
