@@ -620,49 +620,171 @@ int check_out_type(const hashgrid_linear_s* layer, int dtype, const char* name) 
     return ok();
 }
 
-// The backward pass's workspace: dz (where it has to be computed), then the parts of db.
+typedef CUresult (*PFN_tensorMapEncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+PFN_tensorMapEncodeTiled tensor_map_fn() {
+    static PFN_tensorMapEncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<PFN_tensorMapEncodeTiled>(p);
+    }();
+    return fn;
+}
+
+int device_sms() {
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+}
+
+// An operand of a product: a row-major [outer, inner] array of 16-bit elements, rows ld apart. mn:
+// its rows run along k (it is read "transposed").
+struct Array {
+    const void* p;
+    int64_t outer, inner, ld;
+    bool mn;
+    int role;
+};
+
+int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+// Tile width of a product: as few column tiles of at most 256 as there are, then more and
+// narrower ones until every SM has a tile, down to 32 columns; a multiple of 16.
+int tile_width(int64_t M, int64_t N, int sms) {
+    const int64_t mt = ceil_div(M, hg::linear::kBm);
+    int64_t nt = ceil_div(N, 256);
+    while (mt * nt < sms && ceil_div(N, nt) > 32) ++nt;
+    return ceil_div(ceil_div(N, nt), 16) * 16;
+}
+
+// One operand's share of a stage, and its tensor map where TMA can copy it: rows (of more than
+// one) must start on 16-byte boundaries.
+int set_side(hg::linear::Side& s, CUtensorMap& map, const Array& a, int rows_wanted, const char* what) {
+    s.p = a.p;
+    s.ld = a.ld;
+    s.bytes = strided_bytes(a.outer, a.inner, a.ld, 2);
+    s.outer = a.outer;
+    s.inner = a.inner;
+    s.mn = a.mn;
+    s.role = a.role;
+    s.direct = a.outer > 1 && a.ld % 8 != 0;
+    const int64_t extent = a.mn ? a.inner : a.outer;  // rows beyond it are not staged: what they would give is not stored
+    if (a.mn) {
+        s.box_rows = hg::linear::kBk;
+        s.boxes = ceil_div(std::min<int64_t>(rows_wanted, extent), 64);
+    } else {
+        s.box_rows = (int)std::min<int64_t>(rows_wanted, ceil_div(extent, 8) * 8);
+        s.boxes = 1;
+    }
+    if (s.direct) return ok();
+    const cuuint64_t dims[2] = {(cuuint64_t)a.inner, (cuuint64_t)a.outer};
+    const cuuint64_t strides[1] = {(cuuint64_t)(a.outer > 1 ? a.ld : (a.inner + 7) / 8 * 8) * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)s.box_rows}, ones[2] = {1, 1};
+    PFN_tensorMapEncodeTiled encode = tensor_map_fn();
+    const CUresult r = encode == nullptr ? CUDA_ERROR_NOT_SUPPORTED
+                                         : encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(a.p), dims, strides, box, ones,
+                                                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(HASHGRID_ERR_CUDA, "%s: encoding a tensor map failed (%d)", what, (int)r);
+    return ok();
+}
+
+bool vector_rows(const void* p, int64_t ld, size_t elem) { return p == nullptr || ((size_t)ld * elem) % 16 == 0; }
+
+// D[M, N] = A B^T over K on the tensor cores. splits > 1: K is cut into so many parts, each an
+// fp32 [M, N] of its own in e.out.
+template <typename T>
+int launch_gemm(const Array& A, const Array& B, int64_t M, int64_t N, int64_t K, hg::linear::Epilogue e, int bn, int splits,
+                int* status, const char* what, cudaStream_t s) {
+    namespace hl = hg::linear;
+    hl::Gemm g;
+    std::memset(&g, 0, sizeof g);
+    if (int rc = set_side(g.a, g.ta, A, hl::kBm, what)) return rc;
+    if (int rc = set_side(g.b, g.tb, B, bn, what)) return rc;
+    g.M = M;
+    g.N = N;
+    g.bn = bn;
+    g.columns = ceil_div(bn, 32) * 32;
+    g.tmem_columns = 64;
+    while ((int)g.tmem_columns < 2 * g.columns) g.tmem_columns *= 2;
+    g.stage_bytes = hl::kStageA + (B.mn ? ceil_div(bn, 64) * 64 : bn) * 128;
+    const int sms = device_sms();
+    const bool direct = g.a.direct || g.b.direct;
+    // Two blocks a SM where tensor memory and shared memory allow: one's loads and stores then fill the other's gaps.
+    const int per_sm = !direct && g.tmem_columns <= 256 ? 2 : 1;
+    const int budget = (per_sm == 2 ? 113 : 227) * 1024;
+    g.stages = std::min(hl::kMaxStages, (budget - (int)hl::gemm_smem(0, 0)) / g.stage_bytes);
+    g.kblocks = ceil_div(K, hl::kBk);
+    g.kblocks_per_split = ceil_div(g.kblocks, splits);
+    g.mt = ceil_div(M, hl::kBm);
+    g.nt = ceil_div(N, bn);
+    const uint32_t type = std::is_same<T, __half>::value ? 0u : 1u;
+    g.idesc = (1u << 4) | (type << 7) | (type << 10) | ((A.mn ? 1u : 0u) << 15) | ((B.mn ? 1u : 0u) << 16) |
+              ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(hl::kBm >> 4) << 24);
+    g.e = e;
+    const size_t os = e.out_f32 ? 4 : 2;
+    g.e.vectors = vector_rows(e.out, e.ldo, os) && vector_rows(e.residual, e.ldr, os) && vector_rows(e.z, e.ldz, 2);
+    g.split_stride = splits > 1 ? M * N : 0;
+    if (g.split_stride % 4 != 0) g.e.vectors = 0;
+    g.status = status;
+    const int64_t tiles = (int64_t)g.mt * g.nt;
+    if (tiles > (1 << 30)) return fail(HASHGRID_ERR_ARG, "%s: too many tiles", what);
+    const size_t smem = hl::gemm_smem(g.stages, g.stage_bytes);
+    const dim3 grid((unsigned)std::min<int64_t>(tiles, std::max(1, per_sm * sms / splits)), (unsigned)splits);
+    auto k = direct ? hl::gemm_kernel<T, true> : hl::gemm_kernel<T, false>;
+    if (int rc = prepare_smem(k, smem)) return rc;
+    k<<<grid, direct ? hl::kThreadsDirect : hl::kThreads, smem, s>>>(g);
+    return launch_status(what);
+}
+
+// The backward pass's workspace: dz (where it has to be computed), the parts of db, the parts of dw.
 struct LinearWork {
     int64_t lddz;   // elements
     int parts;      // row shares of the db sums
-    size_t dz, sums, bytes;  // offsets, total
+    int splits;     // row shares of dw
+    size_t dz, sums, dw, bytes;  // offsets, total
 };
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
+// dw sums over the rows: so many shares of them that every SM has a tile of one, each of 8 or
+// more 64-row steps.
 LinearWork linear_work(const hashgrid_linear_s* l, int64_t N) {
     LinearWork w;
+    constexpr int kSms = 148;  // the workspace's size may not depend on the device
     w.lddz = (l->out + 7) / 8 * 8;
     w.parts = (int)std::min<int64_t>(256, (N + 63) / 64);
+    const int64_t tiles = (int64_t)ceil_div(l->out, hg::linear::kBm) * ceil_div(l->in, 256);
+    w.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kSms / tiles, N / (8 * hg::linear::kBk)));
     w.dz = 0;
     w.sums = l->act == HASHGRID_ACT_NONE ? 0 : align256((size_t)N * w.lddz * 2);
-    w.bytes = w.sums + align256((size_t)w.parts * l->out * sizeof(float));
+    w.dw = w.sums + align256((size_t)w.parts * l->out * sizeof(float));
+    w.bytes = w.dw + (w.splits > 1 ? align256((size_t)w.splits * l->in * l->out * sizeof(float)) : 0);
     return w;
-}
-
-template <typename T>
-int launch_product(const hg::linear::Operand& A, const hg::linear::Operand& B, int64_t M, int64_t N, int64_t K,
-                   const hg::linear::Epilogue& e, const char* what, cudaStream_t s) {
-    const dim3 grid((unsigned)((M + hg::linear::kTileM - 1) / hg::linear::kTileM),
-                    (unsigned)((N + hg::linear::kTileN - 1) / hg::linear::kTileN));
-    hg::linear::product_kernel<T><<<grid, 256, 0, s>>>(A, B, M, N, K, e);
-    return launch_status(what);
 }
 
 template <typename T>
 int launch_linear_forward(const hashgrid_linear_s* l, const void* x, int64_t ldx, int64_t N, const void* w,
                           const hg::linear::Epilogue& e, int* status, cudaStream_t s) {
-    (void)status;
-    return launch_product<T>({x, ldx, 1}, {w, l->in, 1}, N, l->out, l->in, e, "linear_forward", s);
+    return launch_gemm<T>({x, N, l->in, ldx, false, hg::kChkX}, {w, l->out, l->in, l->in, false, hg::kChkWeights}, N, l->out, l->in, e,
+                          tile_width(N, l->out, device_sms()), 1, status, "linear_forward", s);
 }
 
 template <typename T>
 int launch_linear_backward(const hashgrid_linear_s* l, const void* dy, int64_t lddy, const void* x, int64_t ldx,
                            int64_t N, const void* w, const void* z, void* dx, int64_t lddx, int dx_dtype, void* dw,
                            int dw_dtype, float* db, char* work, int* status, cudaStream_t s) {
-    (void)status;
+    static const char* what = "linear_backward";
     const LinearWork lw = linear_work(l, N);
-    const void* dz = dy;
-    int64_t lddz = lddy;
+    Array dz{dy, N, l->out, lddy, false, hg::kChkDout};
     const bool convert = l->act != HASHGRID_ACT_NONE && (dx != nullptr || dw != nullptr);
     if (convert || db != nullptr) {
         T* to = convert ? reinterpret_cast<T*>(work + lw.dz) : nullptr;
@@ -670,23 +792,36 @@ int launch_linear_backward(const hashgrid_linear_s* l, const void* dy, int64_t l
         const dim3 grid((unsigned)((l->out + 31) / 32), (unsigned)lw.parts);
         hg::linear::slope_kernel<T><<<grid, 256, 0, s>>>(static_cast<const T*>(dy), lddy, static_cast<const T*>(z), N,
                                                         l->out, l->act, to, lw.lddz, sums);
-        if (int rc = launch_status("linear_backward")) return rc;
-        if (convert) {
-            dz = to;
-            lddz = lw.lddz;
-        }
+        if (int rc = launch_status(what)) return rc;
+        if (convert) dz = Array{to, N, l->out, lw.lddz, false, hg::kChkWork};
         if (db != nullptr) {
-            hg::linear::sum_parts_kernel<<<(unsigned)((l->out + 255) / 256), 256, 0, s>>>(sums, lw.parts, l->out, db);
-            if (int rc = launch_status("linear_backward")) return rc;
+            hg::linear::sum_parts_kernel<float><<<(unsigned)((l->out + 255) / 256), 256, 0, s>>>(sums, lw.parts, l->out, db, hg::kChkBias);
+            if (int rc = launch_status(what)) return rc;
         }
     }
     if (dx != nullptr) {
-        const hg::linear::Epilogue e{nullptr, nullptr, dx, nullptr, 0, lddx, 0, dx_dtype == HASHGRID_F32, hg::linear::kNoAct};
-        if (int rc = launch_product<T>({dz, lddz, 1}, {w, 1, l->in}, N, l->in, l->out, e, "linear_backward", s)) return rc;
+        const hg::linear::Epilogue e{nullptr, nullptr, dx, nullptr, 0, lddx, 0, dx_dtype == HASHGRID_F32, hg::linear::kNoAct, hg::kChkOut, 0};
+        if (int rc = launch_gemm<T>(dz, {w, l->out, l->in, l->in, true, hg::kChkWeights}, N, l->in, l->out, e,
+                                    tile_width(N, l->in, device_sms()), 1, status, what, s))
+            return rc;
     }
     if (dw != nullptr) {
-        const hg::linear::Epilogue e{nullptr, nullptr, dw, nullptr, 0, l->in, 0, dw_dtype == HASHGRID_F32, hg::linear::kNoAct};
-        if (int rc = launch_product<T>({dz, 1, lddz}, {x, 1, ldx}, l->out, l->in, N, e, "linear_backward", s)) return rc;
+        const bool parts = lw.splits > 1;
+        float* out = reinterpret_cast<float*>(work + lw.dw);
+        const hg::linear::Epilogue e{nullptr, nullptr, parts ? out : dw, nullptr, 0, l->in, 0, parts || dw_dtype == HASHGRID_F32,
+                                     hg::linear::kNoAct, parts ? hg::kChkWork : hg::kChkGrad, 0};
+        const int bn = parts ? ceil_div(ceil_div(l->in, ceil_div(l->in, 256)), 16) * 16 : tile_width(l->out, l->in, device_sms());
+        dz.mn = true;
+        if (int rc = launch_gemm<T>(dz, {x, N, l->in, ldx, true, hg::kChkX}, l->out, l->in, N, e, bn, lw.splits, status, what, s)) return rc;
+        if (parts) {
+            const int64_t n = (int64_t)l->in * l->out;
+            const unsigned blocks = (unsigned)((n + 255) / 256);
+            if (dw_dtype == HASHGRID_F32)
+                hg::linear::sum_parts_kernel<float><<<blocks, 256, 0, s>>>(out, lw.splits, n, static_cast<float*>(dw), hg::kChkGrad);
+            else
+                hg::linear::sum_parts_kernel<T><<<blocks, 256, 0, s>>>(out, lw.splits, n, static_cast<T*>(dw), hg::kChkGrad);
+            return launch_status(what);
+        }
     }
     return ok();
 }
@@ -1161,7 +1296,7 @@ int hashgrid_linear_forward(hashgrid_linear_t l, const void* x, int64_t ldx, int
         if (int rc = check_buffer(z, (size_t)N * l->out * 2, "z")) return rc;
     if (device_status != nullptr)
         if (int rc = check_buffer(device_status, sizeof(int), "device_status")) return rc;
-    const hg::linear::Epilogue e{b, residual, y, z, ldr, ldy, l->out, y_dtype == HASHGRID_F32, l->act};
+    const hg::linear::Epilogue e{b, residual, y, z, ldr, ldy, l->out, y_dtype == HASHGRID_F32, l->act, hg::kChkOut, 0};
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
     return run_checked(s, {{hg::kChkX, x, strided_bytes(N, l->in, ldx, 2)}, {hg::kChkWeights, w, (size_t)l->in * l->out * 2},
                            {hg::kChkBias, b, (size_t)l->out * sizeof(float)}, {hg::kChkResidual, residual, strided_bytes(N, l->out, ldr, ys)},
@@ -1215,7 +1350,8 @@ int hashgrid_linear_backward(hashgrid_linear_t l, const void* dL_dy, int64_t ldd
         if (int rc = check_buffer(device_status, sizeof(int), "device_status")) return rc;
     return run_checked(s, {{hg::kChkX, x, strided_bytes(N, l->in, ldx, 2)}, {hg::kChkWeights, w, (size_t)l->in * l->out * 2},
                            {hg::kChkBias, dL_db, bb}, {hg::kChkDout, dL_dy, strided_bytes(N, l->out, lddy, 2)},
-                           {hg::kChkZ, z, (size_t)N * l->out * 2}, {hg::kChkWork, workspace, need}},
+                           {hg::kChkZ, z, (size_t)N * l->out * 2}, {hg::kChkWork, workspace, need},
+                           {hg::kChkOut, dL_dx, dL_dx ? strided_bytes(N, l->in, lddx, xs) : 0}, {hg::kChkGrad, dL_dw, wb}},
                        "linear_backward", [&]() -> int {
         char* ws = static_cast<char*>(workspace);
         return l->dtype == HASHGRID_F16

@@ -48,7 +48,14 @@ __device__ __forceinline__ bool in_bounds(const void* p, uint32_t bytes) {
     atomicOr(&g_check_flags, 1u << R);
     return false;
 }
+__device__ __forceinline__ bool in_bounds_role(int role, const void* p, uint32_t bytes) {
+    const uint64_t a = (uint64_t)(uintptr_t)p;
+    if (a >= g_check_ranges.lo[role] && a + bytes <= g_check_ranges.hi[role]) return true;
+    atomicOr(&g_check_flags, 1u << role);
+    return false;
+}
 #else
+__device__ __forceinline__ constexpr bool in_bounds_role(int, const void*, uint32_t) { return true; }
 template <int R>
 __device__ __forceinline__ constexpr bool in_bounds(const void*, uint32_t) {
     return true;
