@@ -146,7 +146,7 @@ def _ptr(a) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -359,10 +359,16 @@ class HashGrid:
         return idx
 
 
+_CODES: dict = {}
+
+
 def _dtype_code(t, name: str) -> int:
     """HASHGRID_* code of a torch tensor's type."""
-    code = {"torch.float32": HASHGRID_F32, "torch.float16": HASHGRID_F16, "torch.bfloat16": HASHGRID_BF16,
-            "torch.float8_e4m3fn": HASHGRID_E4M3}.get(str(t.dtype))
+    if not _CODES:
+        import torch
+        _CODES.update({torch.float32: HASHGRID_F32, torch.float16: HASHGRID_F16, torch.bfloat16: HASHGRID_BF16,
+                       torch.float8_e4m3fn: HASHGRID_E4M3})
+    code = _CODES.get(t.dtype)
     if code is None:
         raise HashGridError(HASHGRID_ERR_ARG, f"{name} has type {t.dtype}")
     return code

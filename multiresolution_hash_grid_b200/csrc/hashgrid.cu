@@ -1448,7 +1448,7 @@ int hashgrid_adamw_step(hashgrid_adamw_t o, int64_t step, const int64_t* device_
     a.db1 = beta1;
     a.db2 = beta2;
     a.c1 = device_step ? 0.f : (float)(1.0 / (1.0 - std::pow((double)beta1, (double)step)));
-    a.c2 = device_step ? 0.f : (float)(1.0 / (1.0 - std::pow((double)beta2, (double)step)));
+    a.root2 = device_step ? 0.f : (float)std::sqrt(1.0 / (1.0 - std::pow((double)beta2, (double)step)));
     a.seed = seed;
     a.step = (uint32_t)step;
     a.zero_grad = zero_grad;

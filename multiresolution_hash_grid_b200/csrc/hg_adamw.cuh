@@ -3,7 +3,8 @@
 // Per element, at step t (fp32, each operation rounded to nearest, no contraction, so that
 // the 8-bit codes that follow from it are reproducible bit for bit):
 //   m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2;
-//   p = p (1 - lr wd) - lr (m c1) / (sqrt(v c2) + eps),  c = 1 / (1 - b^t).
+//   p = p (1 - lr wd) - lr (m c1) / (sqrt(v) sqrt(c2) + eps),  c = 1 / (1 - b^t)
+// (one root serves the step and the 8-bit state).
 // States are fp32, or e4m3 codes with one fp32 scale per 256 elements; v is held as its
 // square root there, since 8 bits of v itself would span half the orders of magnitude.
 //
@@ -49,7 +50,7 @@ struct Tensor {
 };
 
 struct Params {
-    float lr, b1, b2, o1, o2, eps, c1, c2;  // o = 1 - b
+    float lr, b1, b2, o1, o2, eps, c1, root2;  // o = 1 - b, c1 = 1/(1-b1^t), root2 = sqrt(1/(1-b2^t))
     double db1, db2;
     uint32_t seed, step;
     int zero_grad;
@@ -65,14 +66,14 @@ struct List {
 };
 
 template <int R>
-__device__ __forceinline__ bool inside(const void* base, int64_t n, int64_t i, int k) {
+__device__ __forceinline__ bool inside(int64_t n, int64_t i, int k) {
 #ifdef HASHGRID_CHECKED
     if (i < 0 || i + k > n) {
         atomicOr(&g_check_flags, 1u << R);
         return false;
     }
 #endif
-    (void)base; (void)n; (void)i; (void)k;
+    (void)n; (void)i; (void)k;
     return true;
 }
 
@@ -89,136 +90,269 @@ __device__ __forceinline__ uint32_t pack(float a, float b, int type) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Elements i..i+3 of an array of `n`, as fp32 (zeros beyond its end). i is a multiple of 4 and
-// the base 16-byte aligned, so a group of four lies on its own size.
-__device__ __forceinline__ void load4(const void* base, int type, int64_t i, int64_t n, float (&x)[4]) {
-    if (i + 4 <= n) {
-        if (!inside<kChkAdamw>(base, n, i, 4)) return;
-        if (type == kF32) {
+// Elements i..i+3 of an array of `n`, as fp32 pairs (zeros beyond its end). i is a multiple of 4
+// and the base 16-byte aligned, so a group of four lies on its own size.
+template <bool kFull>
+__device__ __forceinline__ void load4(const void* base, int type, int64_t i, int64_t n, float2* x) {
+    if (kFull || i + 4 <= n) {
+        if (!inside<kChkAdamw>(n, i, 4)) {
+            x[0] = x[1] = make_float2(0.f, 0.f);
+        } else if (type == kF32) {
             const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
-            x[0] = q.x; x[1] = q.y; x[2] = q.z; x[3] = q.w;
+            x[0] = make_float2(q.x, q.y);
+            x[1] = make_float2(q.z, q.w);
         } else {
             const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i);
-            const float2 lo = unpack(q.x, type), hi = unpack(q.y, type);
-            x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
+            x[0] = unpack(q.x, type);
+            x[1] = unpack(q.y, type);
         }
-        return;
-    }
+    } else {
+        float y[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        x[k] = 0.f;
-        if (i + k < n && inside<kChkAdamw>(base, n, i + k, 1)) {
-            if (type == kF32) x[k] = static_cast<const float*>(base)[i + k];
-            else x[k] = unpack(static_cast<const uint16_t*>(base)[i + k], type).x;
+        for (int k = 0; k < 4; ++k) {
+            y[k] = 0.f;
+            if (i + k < n && inside<kChkAdamw>(n, i + k, 1)) {
+                if (type == kF32) y[k] = static_cast<const float*>(base)[i + k];
+                else y[k] = unpack(static_cast<const uint16_t*>(base)[i + k], type).x;
+            }
         }
+        x[0] = make_float2(y[0], y[1]);
+        x[1] = make_float2(y[2], y[3]);
     }
 }
 
-__device__ __forceinline__ void store4(void* base, int type, int64_t i, int64_t n, const float (&x)[4]) {
-    if (i + 4 <= n) {
-        if (!inside<kChkAdamw>(base, n, i, 4)) return;
+template <bool kFull>
+__device__ __forceinline__ void store4(void* base, int type, int64_t i, int64_t n, const float2* x) {
+    if (kFull || i + 4 <= n) {
+        if (!inside<kChkAdamw>(n, i, 4)) return;
         if (type == kF32)
-            *reinterpret_cast<float4*>(static_cast<float*>(base) + i) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4*>(static_cast<float*>(base) + i) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
         else
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + i) =
-                make_uint2(pack(x[0], x[1], type), pack(x[2], x[3], type));
-        return;
-    }
+                make_uint2(pack(x[0].x, x[0].y, type), pack(x[1].x, x[1].y, type));
+    } else {
+        const float y[4] = {x[0].x, x[0].y, x[1].x, x[1].y};
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (i + k < n && inside<kChkAdamw>(base, n, i + k, 1)) {
-            if (type == kF32) static_cast<float*>(base)[i + k] = x[k];
-            else static_cast<uint16_t*>(base)[i + k] = (uint16_t)pack(x[k], 0.f, type);
-        }
+        for (int k = 0; k < 4; ++k)
+            if (i + k < n && inside<kChkAdamw>(n, i + k, 1)) {
+                if (type == kF32) static_cast<float*>(base)[i + k] = y[k];
+                else static_cast<uint16_t*>(base)[i + k] = (uint16_t)pack(y[k], 0.f, type);
+            }
+    }
 }
 
+template <bool kFull>
 __device__ __forceinline__ uint32_t load_codes(const void* base, int64_t i, int64_t n) {
     const uint8_t* c = static_cast<const uint8_t*>(base);
-    if (i + 4 <= n) return inside<kChkAdamw>(base, n, i, 4) ? *reinterpret_cast<const uint32_t*>(c + i) : 0u;
     uint32_t w = 0;
+    if (kFull || i + 4 <= n) {
+        if (inside<kChkAdamw>(n, i, 4)) w = *reinterpret_cast<const uint32_t*>(c + i);
+    } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (i + k < n && inside<kChkAdamw>(base, n, i + k, 1)) w |= (uint32_t)c[i + k] << (8 * k);
+        for (int k = 0; k < 4; ++k)
+            if (i + k < n && inside<kChkAdamw>(n, i + k, 1)) w |= (uint32_t)c[i + k] << (8 * k);
+    }
     return w;
 }
 
+template <bool kFull>
 __device__ __forceinline__ void store_codes(void* base, int64_t i, int64_t n, uint32_t w) {
     uint8_t* c = static_cast<uint8_t*>(base);
-    if (i + 4 <= n) {
-        if (inside<kChkAdamw>(base, n, i, 4)) *reinterpret_cast<uint32_t*>(c + i) = w;
+    if (kFull || i + 4 <= n) {
+        if (inside<kChkAdamw>(n, i, 4)) *reinterpret_cast<uint32_t*>(c + i) = w;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i + k < n && inside<kChkAdamw>(n, i + k, 1)) c[i + k] = (uint8_t)(w >> (8 * k));
+    }
+}
+
+// The two e4m3 codes in the low half of w, without their scale.
+__device__ __forceinline__ float2 decode2(uint32_t w) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+    return __half22float2(__half2(h));
+}
+
+// Pairs of fp32 operations, each rounded to nearest. Sums stay single: a packed product followed by
+// a packed sum came out contracted (one rounding less than the states' definition has).
+__device__ __forceinline__ uint64_t pair(float2 a) { return (uint64_t)__float_as_uint(a.y) << 32 | __float_as_uint(a.x); }
+__device__ __forceinline__ float2 unpair(uint64_t a) {
+    return make_float2(__uint_as_float((uint32_t)a), __uint_as_float((uint32_t)(a >> 32)));
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair(a)), "l"(pair(b)));
+    return unpair(d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(pair(a)), "l"(pair(b)), "l"(pair(c)));
+    return unpair(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, both(-1.f), a); }  // one rounding
+
+// y >= 0 with its mantissa cut to three bits after a random part of a code (`up` of 2^20 parts)
+// was added: for y < 2^-6, where e4m3 is spaced evenly by 2^-9, 2^-6 is added first, which puts
+// y where floats of three mantissa bits have that very spacing.
+__device__ __forceinline__ float2 stochastic2(float2 y, uint32_t up0, uint32_t up1) {
+    const float2 low = make_float2(y.x < 0x1p-6f ? 0x1p-6f : 0.f, y.y < 0x1p-6f ? 0x1p-6f : 0.f);
+    float2 s = add2(y, low);
+    s.x = __uint_as_float((__float_as_uint(s.x) + up0) & ~0xFFFFFu);
+    s.y = __uint_as_float((__float_as_uint(s.y) + up1) & ~0xFFFFFu);
+    return sub2(s, low);
+}
+
+// Codes of 4 x 2 values x (the lane's share of a 256-element block), and the block's scale.
+// kRoot: the values are square roots, and a positive one is coded as 2^-9 at least. A code above
+// 448, which a random part can make of a value that was rounded up to just above 448, saturates in
+// the conversion.
+template <bool kRoot>
+__device__ __forceinline__ float encode(const float2 (&x)[4], const uint32_t (&h)[8], bool nearest, uint32_t (&w)[2]) {
+    const float inf = __uint_as_float(0x7f800000u);
+    float top = 0.f;
+    float2 spoiled = both(0.f);  // stays 0 while everything is finite
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+        top = fmaxf(fmaxf(top, fabsf(x[a].x)), fabsf(x[a].y));
+        spoiled = fma2(x[a], both(0.f), spoiled);
+    }
+    const bool finite = !__any_sync(0xffffffffu, !(spoiled.x + spoiled.y == 0.f));
+    if (!finite) {
+        top = 0.f;
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            if (fabsf(x[a].x) < inf) top = fmaxf(top, fabsf(x[a].x));
+            if (fabsf(x[a].y) < inf) top = fmaxf(top, fabsf(x[a].y));
+        }
+    }
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // magnitudes order as their bits do
+    const float scale = __fdiv_rn(top, kTop);
+    // a block whose reciprocal could overflow is stored as zeros
+    const float inverse = top > 0x1p-100f ? __fdiv_rn(kTop, top) : 0.f;
+    uint32_t c[4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+        float2 y = mul2(x[a], both(inverse));
+        if (!nearest) {
+            const uint32_t u0 = ((kRoot ? h[2 * a] >> 12 : h[2 * a] << 4) & 0xffff0u) + 8u;
+            const uint32_t u1 = ((kRoot ? h[2 * a + 1] >> 12 : h[2 * a + 1] << 4) & 0xffff0u) + 8u;
+            if (kRoot) {
+                y = stochastic2(y, u0, u1);
+            } else {
+                const float2 s = stochastic2(make_float2(fabsf(y.x), fabsf(y.y)), u0, u1);
+                y = make_float2(copysignf(s.x, y.x), copysignf(s.y, y.y));
+            }
+        }
+        if (kRoot) y = make_float2(fmaxf(y.x, x[a].x > 0.f ? 0x1p-9f : 0.f), fmaxf(y.y, x[a].y > 0.f ? 0x1p-9f : 0.f));
+        if (!finite) {
+            if (!(fabsf(x[a].x) < inf)) y.x = __uint_as_float(0x7fc00000u);
+            if (!(fabsf(x[a].y) < inf)) y.y = __uint_as_float(0x7fc00000u);
+        }
+        c[a] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+    }
+    w[0] = __byte_perm(c[0], c[1], 0x5410);
+    w[1] = __byte_perm(c[2], c[3], 0x5410);
+    return scale;
+}
+
+struct Rates {
+    float c1, root2, rate, keep;  // 1/(1-b1^t), sqrt(1/(1-b2^t)), lr * lr_scale, 1 - rate * decay
+    uint32_t step;
+};
+
+// One 256-element block. kP, kG, kS: the types of parameter, gradient and states where the compiler
+// may know them (-1: only the list does); kFull: the block lies wholly inside the tensor.
+template <int kP, int kG, int kS, bool kFull>
+__device__ __forceinline__ void step_block(const Tensor& T, const Params& a, const Rates& r, int64_t blk, int lane) {
+    const int tp = kP >= 0 ? kP : (int)(T.types & 15), tg = kG >= 0 ? kG : (int)(T.types >> 4 & 15),
+              ts = kS >= 0 ? kS : (int)(T.types >> 8 & 15), tc = (int)(T.types >> 12 & 15);
+    const int64_t base = blk * kBlock;
+    const int64_t n = T.n;
+    const int64_t at[2] = {base + 4 * lane, base + 128 + 4 * lane};
+    float2 p[4], g[4], m[4], v[4], root[4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        load4<kFull>(T.g, tg, at[k], n, g + 2 * k);
+        load4<kFull>(T.p, tp, at[k], n, p + 2 * k);
+    }
+    if (ts == kF32) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            load4<kFull>(T.m, kF32, at[k], n, m + 2 * k);
+            load4<kFull>(T.v, kF32, at[k], n, v + 2 * k);
+        }
+    } else {
+        const float ms = T.ms[blk], vs = T.vs[blk];
+        uint32_t cm[2], cv[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            cm[k] = load_codes<kFull>(T.m, at[k], n);
+            cv[k] = load_codes<kFull>(T.v, at[k], n);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            m[k] = mul2(decode2(cm[k >> 1] >> 16 * (k & 1)), both(ms));
+            v[k] = mul2(decode2(cv[k >> 1] >> 16 * (k & 1)), both(vs));
+            v[k] = mul2(v[k], v[k]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        m[k] = add2(mul2(m[k], both(a.b1)), mul2(g[k], both(a.o1)));
+        v[k] = add2(mul2(v[k], both(a.b2)), mul2(mul2(g[k], g[k]), both(a.o2)));
+        root[k] = make_float2(__fsqrt_rn(v[k].x), __fsqrt_rn(v[k].y));
+        const float2 d = add2(mul2(root[k], both(r.root2)), both(a.eps)), s = mul2(m[k], both(r.c1));
+        // the quotient alone is not correctly rounded (2 ulp of a step): a division in full costs a tenth of an 8-bit step
+        p[k] = sub2(mul2(p[k], both(r.keep)), mul2(both(r.rate), make_float2(__fdividef(s.x, d.x), __fdividef(s.y, d.y))));
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        store4<kFull>(T.p, tp, at[k], n, p + 2 * k);
+        if (tc != kNone) store4<kFull>(T.copy, tc, at[k], n, p + 2 * k);
+        if (a.zero_grad) {
+            const float2 z[2] = {};
+            store4<kFull>(T.g, tg, at[k], n, z);
+        }
+    }
+    if (ts == kF32) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            store4<kFull>(T.m, kF32, at[k], n, m + 2 * k);
+            store4<kFull>(T.v, kF32, at[k], n, v + 2 * k);
+        }
         return;
     }
+    uint32_t h[8] = {}, w[2];
+    const bool nearest = a.seed == 0;
+    if (!nearest) {
+        const uint32_t key = probe::mix32(a.seed * 0x9E3779B1u + r.step * 0x85EBCA77u + (T.types >> 16) * 0xC2B2AE3Du +
+                                          (uint32_t)((uint64_t)base >> 32) * 0x27D4EB2Fu);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (i + k < n && inside<kChkAdamw>(base, n, i + k, 1)) c[i + k] = (uint8_t)(w >> (8 * k));
-}
-
-__device__ __forceinline__ void decode(uint32_t w, float scale, float (&x)[4]) {
-    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-    const float2 a = __half22float2(__half2(lo)), b = __half22float2(__half2(hi));
-    x[0] = __fmul_rn(a.x, scale);
-    x[1] = __fmul_rn(a.y, scale);
-    x[2] = __fmul_rn(b.x, scale);
-    x[3] = __fmul_rn(b.y, scale);
-}
-
-// y >= 0 with its mantissa cut to three bits after a random part of a code was added: for
-// y < 2^-6, where e4m3 is spaced evenly by 2^-9, 2^-6 is added first, which puts y where floats
-// of three mantissa bits have that very spacing.
-__device__ __forceinline__ float stochastic(float y, uint32_t r16) {
-    const float low = y < 0x1p-6f ? 0x1p-6f : 0.f;
-    const uint32_t bits = (__float_as_uint(__fadd_rn(y, low)) + (r16 * 16u + 8u)) & ~0xFFFFFu;
-    return fminf(__fsub_rn(__uint_as_float(bits), low), kTop);
-}
-
-// Codes of 2 x 4 values x (the lane's share of a 256-element block), and the block's scale.
-// kRoot: the values are square roots, and a positive one is coded as 2^-9 at least.
-template <bool kRoot>
-__device__ __forceinline__ float encode(const float (&x)[2][4], const uint32_t (&h)[2][4], bool nearest, uint32_t (&w)[2]) {
-    float top = 0.f;
-#pragma unroll
-    for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float y = fabsf(x[a][k]);
-            top = fmaxf(top, y < __int_as_float(0x7f800000) ? y : 0.f);  // neither infinity nor NaN
-        }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float scale = __fdiv_rn(top, kTop);
-    // a block whose reciprocal overflows holds nothing that its codes could stand for
-    float inverse = top > 0x1p-100f ? __fdiv_rn(kTop, top) : 0.f;
-#pragma unroll
-    for (int a = 0; a < 2; ++a) {
-        float q[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float v = x[a][k];
-            float y = __fmul_rn(fabsf(v), inverse);
-            if (!nearest) y = stochastic(y, kRoot ? h[a][k] >> 16 : h[a][k] & 0xffffu);
-            if (kRoot && v > 0.f) y = fmaxf(y, 0x1p-9f);
-            y = v < 0.f ? -y : y;
-            if (!(fabsf(v) < __int_as_float(0x7f800000))) y = __int_as_float(0x7fc00000);
-            q[k] = y;
-        }
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[2], q[3]), __NV_SATFINITE, __NV_E4M3);
-        w[a] = lo | hi << 16;
+        for (int k = 0; k < 8; ++k) h[k] = probe::mix32(((uint32_t)at[k >> 2] + (k & 3)) ^ key);
     }
-    return scale;
+    const float ms = encode<false>(m, h, nearest, w);
+    store_codes<kFull>(T.m, at[0], n, w[0]);
+    store_codes<kFull>(T.m, at[1], n, w[1]);
+    const float vs = encode<true>(root, h, nearest, w);
+    store_codes<kFull>(T.v, at[0], n, w[0]);
+    store_codes<kFull>(T.v, at[1], n, w[1]);
+    if (lane == 0) {
+        T.ms[blk] = ms;
+        T.vs[blk] = vs;
+    }
 }
 
 template <int kCap>
 __global__ void __launch_bounds__(32 * kWarps) step_kernel(const __grid_constant__ List<kCap> list, const Params a) {
-    float c1 = a.c1, c2 = a.c2;
-    uint32_t step = a.step;
+    Rates r{a.c1, a.root2, 0.f, 0.f, a.step};
     if (a.device_step != nullptr) {
         const int64_t t = *a.device_step;
         if (t < 1) return;
-        step = (uint32_t)t;
-        c1 = (float)(1.0 / (1.0 - pow(a.db1, (double)t)));
-        c2 = (float)(1.0 / (1.0 - pow(a.db2, (double)t)));
+        r.step = (uint32_t)t;
+        r.c1 = (float)(1.0 / (1.0 - pow(a.db1, (double)t)));
+        r.root2 = (float)sqrt(1.0 / (1.0 - pow(a.db2, (double)t)));
     }
     const int lane = threadIdx.x & 31;
     const uint32_t b = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -229,86 +363,24 @@ __global__ void __launch_bounds__(32 * kWarps) step_kernel(const __grid_constant
         if (list.t[mid].first <= b) lo = mid; else hi = mid;
     }
     const Tensor& T = list.t[lo];
-    const int64_t n = T.n, blk = b - T.first, base = blk * kBlock;
-    const int tp = T.types & 15, tg = (T.types >> 4) & 15, ts = (T.types >> 8) & 15, tc = (T.types >> 12) & 15;
-    const int64_t at[2] = {base + 4 * lane, base + 128 + 4 * lane};
-
-    float p[2][4], g[2][4], m[2][4], v[2][4];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        load4(T.g, tg, at[k], n, g[k]);
-        load4(T.p, tp, at[k], n, p[k]);
+    const int64_t blk = b - T.first;
+    r.rate = __fmul_rn(T.lr_scale, a.lr);
+    r.keep = (float)(1.0 - (double)T.lr_scale * (double)a.lr * (double)T.decay);
+    if ((blk + 1) * kBlock > T.n) return step_block<-1, -1, -1, false>(T, a, r, blk, lane);
+    switch (T.types & 0xfffu) {
+#define HG_ADAMW_CASE(P, G, S) \
+    case P | G << 4 | S << 8: return step_block<P, G, S, true>(T, a, r, blk, lane);
+        HG_ADAMW_CASE(kF32, kF32, kF32)
+        HG_ADAMW_CASE(kF32, kBf16, kF32)
+        HG_ADAMW_CASE(kBf16, kBf16, kF32)
+        HG_ADAMW_CASE(kF16, kF16, kF32)
+        HG_ADAMW_CASE(kF32, kF32, kE4m3)
+        HG_ADAMW_CASE(kF32, kBf16, kE4m3)
+        HG_ADAMW_CASE(kBf16, kBf16, kE4m3)
+        HG_ADAMW_CASE(kF16, kF16, kE4m3)
+#undef HG_ADAMW_CASE
     }
-    if (ts == kF32) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            load4(T.m, kF32, at[k], n, m[k]);
-            load4(T.v, kF32, at[k], n, v[k]);
-        }
-    } else {
-        const float ms = T.ms[blk], vs = T.vs[blk];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            decode(load_codes(T.m, at[k], n), ms, m[k]);
-            decode(load_codes(T.v, at[k], n), vs, v[k]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[k][j] = __fmul_rn(v[k][j], v[k][j]);
-        }
-    }
-    const float rate = __fmul_rn(T.lr_scale, a.lr);
-    const float keep = (float)(1.0 - (double)T.lr_scale * (double)a.lr * (double)T.decay);
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float gj = g[k][j];
-            m[k][j] = __fadd_rn(__fmul_rn(m[k][j], a.b1), __fmul_rn(gj, a.o1));
-            v[k][j] = __fadd_rn(__fmul_rn(v[k][j], a.b2), __fmul_rn(__fmul_rn(gj, gj), a.o2));
-            const float d = __fadd_rn(__fsqrt_rn(__fmul_rn(v[k][j], c2)), a.eps);
-            const float u = __fmul_rn(rate, __fdiv_rn(__fmul_rn(m[k][j], c1), d));
-            p[k][j] = __fsub_rn(__fmul_rn(p[k][j], keep), u);
-        }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        store4(T.p, tp, at[k], n, p[k]);
-        if (tc != kNone) store4(T.copy, tc, at[k], n, p[k]);
-        if (a.zero_grad) {
-            const float z[4] = {0.f, 0.f, 0.f, 0.f};
-            store4(T.g, tg, at[k], n, z);
-        }
-    }
-    if (ts == kF32) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            store4(T.m, kF32, at[k], n, m[k]);
-            store4(T.v, kF32, at[k], n, v[k]);
-        }
-        return;
-    }
-    uint32_t h[2][4] = {}, w[2];
-    const bool nearest = a.seed == 0;
-    if (!nearest) {
-        const uint32_t key = probe::mix32(a.seed * 0x9E3779B1u + step * 0x85EBCA77u + (T.types >> 16) * 0xC2B2AE3Du +
-                                          (uint32_t)((uint64_t)base >> 32) * 0x27D4EB2Fu);
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) h[k][j] = probe::mix32((uint32_t)(at[k] + j) ^ key);
-    }
-    const float ms = encode<false>(m, h, nearest, w);
-    store_codes(T.m, at[0], n, w[0]);
-    store_codes(T.m, at[1], n, w[1]);
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[k][j] = __fsqrt_rn(v[k][j]);
-    const float vs = encode<true>(v, h, nearest, w);
-    store_codes(T.v, at[0], n, w[0]);
-    store_codes(T.v, at[1], n, w[1]);
-    if (lane == 0) {
-        T.ms[blk] = ms;
-        T.vs[blk] = vs;
-    }
+    step_block<-1, -1, -1, true>(T, a, r, blk, lane);  // the rarer pairs of types
 }
 
 }  // namespace adamw
