@@ -489,8 +489,9 @@ int hashgrid_adamw_destroy(hashgrid_adamw_t opt);
  *   m = beta1 m + (1 - beta1) g;   v = beta2 v + (1 - beta2) g^2;
  *   param = param (1 - lr lr_scale weight_decay)
  *           - lr lr_scale (m / (1 - beta1^t)) / (sqrt(v) / sqrt(1 - beta2^t) + eps).
- * (1 / (1 - beta1^t) and sqrt(1 / (1 - beta2^t)) are computed in fp64 and multiplied as fp32.) Unlike hashgrid_adam_step,
- * elements with a zero gradient decay too.
+ * (1 / (1 - beta1^t) and sqrt(1 / (1 - beta2^t)) are computed in fp64 and multiplied as fp32; the
+ * root and the quotient are off by at most 2 units in the last place.) Unlike
+ * hashgrid_adam_step, elements with a zero gradient decay too.
  *
  * 8-bit states (HASHGRID_E4M3): m is stored as codes c with m = c * m_scale[i / 256], v as
  * codes of its square root, v = (c * v_scale[i / 256])^2, which halves the range that its 8
@@ -509,7 +510,7 @@ int hashgrid_adamw_destroy(hashgrid_adamw_t opt);
  *
  * device_step: NULL, or a device int64 that the kernel reads t from (then `step` is ignored
  * and a t < 1 leaves everything as it was), so that a captured graph can be replayed while the
- * caller counts on the device. 0 <= beta1, beta2 < 1; eps > 0; lr finite. zero_grad != 0 sets
+ * caller counts on the device. 0 <= beta1, beta2 < 1; eps >= 2^-126; lr finite. zero_grad != 0 sets
  * the gradients to zero after they are read.
  */
 int hashgrid_adamw_step(hashgrid_adamw_t opt, int64_t step, const int64_t *device_step, float lr, float beta1,

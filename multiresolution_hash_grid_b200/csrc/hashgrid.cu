@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -55,7 +56,7 @@ struct hashgrid_adamw_s {
     std::vector<hg::adamw::Tensor> tensors;  // `first` counts blocks within the tensor's launch
     struct Launch {
         int begin, count;  // tensors
-        uint32_t blocks;
+        uint32_t blocks;   // of 256 elements
     };
     std::vector<Launch> launches;
 };
@@ -1378,37 +1379,41 @@ int hashgrid_adamw_create(const hashgrid_adamw_tensor* tensors, int count, hashg
         auto* o = new hashgrid_adamw_s;
         *opt = o;
         o->device = dev;
-        constexpr uint64_t kMostBlocks = (uint64_t)1 << 31;  // 256-element blocks of one launch
-        uint64_t blocks = 0;
-        int begin = 0;
-        for (int k = 0; k < count; ++k) {
-            const hashgrid_adamw_tensor& t = tensors[k];
-            if (t.n == 0) continue;
-            const uint64_t own = ((uint64_t)t.n + HASHGRID_ADAMW_BLOCK - 1) / HASHGRID_ADAMW_BLOCK;
-            const int have = (int)o->tensors.size();
-            if (have > begin && (have - begin == hg::adamw::kLarge || blocks + own > kMostBlocks)) {
-                o->launches.push_back({begin, have - begin, (uint32_t)blocks});
-                begin = have;
-                blocks = 0;
+        auto blocks_of = [](int64_t n) { return ((uint64_t)n + HASHGRID_ADAMW_BLOCK - 1) / HASHGRID_ADAMW_BLOCK; };
+        for (int k = 0; k < count;) {
+            // one launch: as many tensors as its list takes, at most 2^31 blocks
+            uint64_t blocks = 0;
+            int end = k, have = 0;
+            for (; end < count && have < hg::adamw::kLarge; ++end) {
+                const uint64_t own = blocks_of(tensors[end].n);
+                if (have > 0 && blocks + own > ((uint64_t)1 << 31)) break;
+                blocks += own;
+                have += own != 0;
             }
-            hg::adamw::Tensor d;
-            d.p = t.param;
-            d.g = t.grad;
-            d.m = t.m;
-            d.v = t.v;
-            d.ms = t.m_scale;
-            d.vs = t.v_scale;
-            d.copy = t.copy;
-            d.n = t.n;
-            d.first = (uint32_t)blocks;
-            d.types = (uint32_t)t.param_dtype | (uint32_t)t.grad_dtype << 4 | (uint32_t)t.state_dtype << 8 |
-                      (uint32_t)(t.copy ? t.copy_dtype : (int)hg::adamw::kNone) << 12 | (uint32_t)k << 16;
-            d.lr_scale = t.lr_scale;
-            d.decay = t.weight_decay;
-            o->tensors.push_back(d);
-            blocks += own;
+            const int begin = (int)o->tensors.size();
+            uint32_t first = 0;
+            for (; k < end; ++k) {
+                const hashgrid_adamw_tensor& t = tensors[k];
+                if (t.n == 0) continue;
+                hg::adamw::Tensor d;
+                d.p = t.param;
+                d.g = t.grad;
+                d.m = t.m;
+                d.v = t.v;
+                d.ms = t.m_scale;
+                d.vs = t.v_scale;
+                d.copy = t.copy;
+                d.n = t.n;
+                d.first = first;
+                d.types = (uint32_t)t.param_dtype | (uint32_t)t.grad_dtype << 4 | (uint32_t)t.state_dtype << 8 |
+                          (uint32_t)(t.copy ? t.copy_dtype : (int)hg::adamw::kNone) << 12 | (uint32_t)k << 16;
+                d.lr_scale = t.lr_scale;
+                d.decay = t.weight_decay;
+                o->tensors.push_back(d);
+                first += (uint32_t)blocks_of(t.n);
+            }
+            if (have > 0) o->launches.push_back({begin, have, (uint32_t)blocks});
         }
-        if ((int)o->tensors.size() > begin) o->launches.push_back({begin, (int)o->tensors.size() - begin, (uint32_t)blocks});
     } catch (const std::bad_alloc&) {
         delete *opt;
         *opt = nullptr;
@@ -1428,8 +1433,8 @@ int hashgrid_adamw_step(hashgrid_adamw_t o, int64_t step, const int64_t* device_
     if (device_step == nullptr && step < 1) return fail(HASHGRID_ERR_ARG, "step = %lld must be >= 1", (long long)step);
     if (!(beta1 >= 0.f && beta1 < 1.f) || !(beta2 >= 0.f && beta2 < 1.f))
         return fail(HASHGRID_ERR_ARG, "betas (%g, %g) must lie in [0, 1)", beta1, beta2);
-    if (!(eps > 0.f) || !std::isfinite(eps) || !std::isfinite(lr))
-        return fail(HASHGRID_ERR_ARG, "lr = %g and eps = %g must be finite, eps > 0", lr, eps);
+    if (!(eps >= FLT_MIN) || !std::isfinite(eps) || !std::isfinite(lr))
+        return fail(HASHGRID_ERR_ARG, "lr = %g and eps = %g must be finite, eps at least 2^-126", lr, eps);
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess) {
         cudaGetLastError();

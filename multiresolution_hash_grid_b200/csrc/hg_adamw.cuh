@@ -15,7 +15,8 @@
 // whatever its type, is read and written in whole coalesced vectors (16, 8 or 4 bytes a lane),
 // and a block's largest magnitude is a shuffle reduction within the warp. The list of tensors
 // travels as a kernel parameter: no device copy of it to keep, and a captured graph holds it
-// by value.
+// by value. (A warp that walked four neighbouring blocks, to find their tensor and rates once, was
+// slower: 77 against 73.5 us for 2^24 fp32 elements.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -193,23 +194,30 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
 __device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, both(-1.f), a); }  // one rounding
 
-// y >= 0 with its mantissa cut to three bits after a random part of a code (`up` of 2^20 parts)
-// was added: for y < 2^-6, where e4m3 is spaced evenly by 2^-9, 2^-6 is added first, which puts
-// y where floats of three mantissa bits have that very spacing.
-__device__ __forceinline__ float2 stochastic2(float2 y, uint32_t up0, uint32_t up1) {
-    const float2 low = make_float2(y.x < 0x1p-6f ? 0x1p-6f : 0.f, y.y < 0x1p-6f ? 0x1p-6f : 0.f);
-    float2 s = add2(y, low);
-    s.x = __uint_as_float((__float_as_uint(s.x) + up0) & ~0xFFFFFu);
-    s.y = __uint_as_float((__float_as_uint(s.y) + up1) & ~0xFFFFFu);
-    return sub2(s, low);
+// The e4m3 code of y in [0, 448], rounded up with the probability of the part cut off (`up` of 2^20
+// parts of a code are added and the rest cut). Times 2^-120, e4m3's smallest normal number is
+// fp32's, and the code is the top of the float's bits, subnormal codes included.
+__device__ __forceinline__ uint32_t stochastic_code(float y, uint32_t up) {
+    return (__float_as_uint(__fmul_rn(fminf(fabsf(y), kTop), 0x1p-120f)) + up) >> 20;
 }
 
-// Codes of 4 x 2 values x (the lane's share of a 256-element block), and the block's scale.
-// kRoot: the values are square roots, and a positive one is coded as 2^-9 at least. A code above
-// 448, which a random part can make of a value that was rounded up to just above 448, saturates in
-// the conversion.
-template <bool kRoot>
-__device__ __forceinline__ float encode(const float2 (&x)[4], const uint32_t (&h)[8], bool nearest, uint32_t (&w)[2]) {
+__device__ __forceinline__ float reciprocal(float d) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    return r;
+}
+
+// Off by at most 2 units in the last place, which moves a code only from within 2^-21 of a border. The
+// correctly rounded root takes some ten instructions more (see the kernel's comment).
+__device__ __forceinline__ float square_root(float v) {
+    float r;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// The largest finite magnitude of a 256-element block, 4 x 2 of whose values are this lane's. `finite`:
+// nothing else is among them.
+__device__ __forceinline__ float block_top(const float2 (&x)[4], bool& finite) {
     const float inf = __uint_as_float(0x7f800000u);
     float top = 0.f;
     float2 spoiled = both(0.f);  // stays 0 while everything is finite
@@ -218,7 +226,7 @@ __device__ __forceinline__ float encode(const float2 (&x)[4], const uint32_t (&h
         top = fmaxf(fmaxf(top, fabsf(x[a].x)), fabsf(x[a].y));
         spoiled = fma2(x[a], both(0.f), spoiled);
     }
-    const bool finite = !__any_sync(0xffffffffu, !(spoiled.x + spoiled.y == 0.f));
+    finite = !__any_sync(0xffffffffu, !(spoiled.x + spoiled.y == 0.f));
     if (!finite) {
         top = 0.f;
 #pragma unroll
@@ -227,34 +235,41 @@ __device__ __forceinline__ float encode(const float2 (&x)[4], const uint32_t (&h
             if (fabsf(x[a].y) < inf) top = fmaxf(top, fabsf(x[a].y));
         }
     }
-    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // magnitudes order as their bits do
-    const float scale = __fdiv_rn(top, kTop);
-    // a block whose reciprocal could overflow is stored as zeros
-    const float inverse = top > 0x1p-100f ? __fdiv_rn(kTop, top) : 0.f;
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // magnitudes order as their bits do
+}
+
+// Codes of the lane's values times `inverse` = 448 / their block's top. kRoot: the values are
+// square roots, and a positive one is coded as 2^-9 at least.
+template <bool kRoot>
+__device__ __forceinline__ void encode(const float2 (&x)[4], const uint32_t (&h)[8], bool nearest, float inverse, bool finite,
+                                       uint32_t (&w)[2]) {
+    const float inf = __uint_as_float(0x7f800000u);
     uint32_t c[4];
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
         float2 y = mul2(x[a], both(inverse));
-        if (!nearest) {
-            const uint32_t u0 = ((kRoot ? h[2 * a] >> 12 : h[2 * a] << 4) & 0xffff0u) + 8u;
-            const uint32_t u1 = ((kRoot ? h[2 * a + 1] >> 12 : h[2 * a + 1] << 4) & 0xffff0u) + 8u;
+        if (nearest) {
+            if (kRoot) y = make_float2(fmaxf(y.x, x[a].x > 0.f ? 0x1p-9f : 0.f), fmaxf(y.y, x[a].y > 0.f ? 0x1p-9f : 0.f));
+            c[a] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+        } else {
+            uint32_t c0 = stochastic_code(y.x, ((kRoot ? h[2 * a] >> 12 : h[2 * a] << 4) & 0xffff0u) | 8u);
+            uint32_t c1 = stochastic_code(y.y, ((kRoot ? h[2 * a + 1] >> 12 : h[2 * a + 1] << 4) & 0xffff0u) | 8u);
             if (kRoot) {
-                y = stochastic2(y, u0, u1);
+                c0 = max(c0, min(__float_as_uint(x[a].x), 1u));
+                c1 = max(c1, min(__float_as_uint(x[a].y), 1u));
             } else {
-                const float2 s = stochastic2(make_float2(fabsf(y.x), fabsf(y.y)), u0, u1);
-                y = make_float2(copysignf(s.x, y.x), copysignf(s.y, y.y));
+                c0 |= __float_as_uint(y.x) >> 24 & 0x80u;
+                c1 |= __float_as_uint(y.y) >> 24 & 0x80u;
             }
+            c[a] = c0 | c1 << 8;
         }
-        if (kRoot) y = make_float2(fmaxf(y.x, x[a].x > 0.f ? 0x1p-9f : 0.f), fmaxf(y.y, x[a].y > 0.f ? 0x1p-9f : 0.f));
         if (!finite) {
-            if (!(fabsf(x[a].x) < inf)) y.x = __uint_as_float(0x7fc00000u);
-            if (!(fabsf(x[a].y) < inf)) y.y = __uint_as_float(0x7fc00000u);
+            if (!(fabsf(x[a].x) < inf)) c[a] = (c[a] & 0xff00u) | 0x7fu;
+            if (!(fabsf(x[a].y) < inf)) c[a] = (c[a] & 0xffu) | 0x7f00u;
         }
-        c[a] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
     }
     w[0] = __byte_perm(c[0], c[1], 0x5410);
     w[1] = __byte_perm(c[2], c[3], 0x5410);
-    return scale;
 }
 
 struct Rates {
@@ -302,10 +317,10 @@ __device__ __forceinline__ void step_block(const Tensor& T, const Params& a, con
     for (int k = 0; k < 4; ++k) {
         m[k] = add2(mul2(m[k], both(a.b1)), mul2(g[k], both(a.o1)));
         v[k] = add2(mul2(v[k], both(a.b2)), mul2(mul2(g[k], g[k]), both(a.o2)));
-        root[k] = make_float2(__fsqrt_rn(v[k].x), __fsqrt_rn(v[k].y));
+        root[k] = make_float2(square_root(v[k].x), square_root(v[k].y));
         const float2 d = add2(mul2(root[k], both(r.root2)), both(a.eps)), s = mul2(m[k], both(r.c1));
         // the quotient alone is not correctly rounded (2 ulp of a step): a division in full costs a tenth of an 8-bit step
-        p[k] = sub2(mul2(p[k], both(r.keep)), mul2(both(r.rate), make_float2(__fdividef(s.x, d.x), __fdividef(s.y, d.y))));
+        p[k] = sub2(mul2(p[k], both(r.keep)), mul2(both(r.rate), mul2(s, make_float2(reciprocal(d.x), reciprocal(d.y)))));
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -332,20 +347,25 @@ __device__ __forceinline__ void step_block(const Tensor& T, const Params& a, con
 #pragma unroll
         for (int k = 0; k < 8; ++k) h[k] = probe::mix32(((uint32_t)at[k >> 2] + (k & 3)) ^ key);
     }
-    const float ms = encode<false>(m, h, nearest, w);
+    bool mf, vf;
+    const float mt = block_top(m, mf), vt = block_top(root, vf);
+    // One division a lane gives all four quotients: lane 0 and 1 the scale and the inverse of m, 2 and 3 of
+    // v. A block whose inverse could overflow is stored as zeros.
+    const float t = lane & 2 ? vt : mt;
+    float q = __fdiv_rn(lane & 1 ? kTop : t, lane & 1 ? t : kTop);
+    if ((lane & 1) && !(t > 0x1p-100f)) q = 0.f;
+    encode<false>(m, h, nearest, __shfl_sync(0xffffffffu, q, 1), mf, w);
     store_codes<kFull>(T.m, at[0], n, w[0]);
     store_codes<kFull>(T.m, at[1], n, w[1]);
-    const float vs = encode<true>(root, h, nearest, w);
+    encode<true>(root, h, nearest, __shfl_sync(0xffffffffu, q, 3), vf, w);
     store_codes<kFull>(T.v, at[0], n, w[0]);
     store_codes<kFull>(T.v, at[1], n, w[1]);
-    if (lane == 0) {
-        T.ms[blk] = ms;
-        T.vs[blk] = vs;
-    }
+    if (lane == 0) T.ms[blk] = q;
+    if (lane == 2) T.vs[blk] = q;
 }
 
 template <int kCap>
-__global__ void __launch_bounds__(32 * kWarps) step_kernel(const __grid_constant__ List<kCap> list, const Params a) {
+__global__ void __launch_bounds__(32 * kWarps, 4) step_kernel(const __grid_constant__ List<kCap> list, const Params a) {
     Rates r{a.c1, a.root2, 0.f, 0.f, a.step};
     if (a.device_step != nullptr) {
         const int64_t t = *a.device_step;
@@ -363,9 +383,9 @@ __global__ void __launch_bounds__(32 * kWarps) step_kernel(const __grid_constant
         if (list.t[mid].first <= b) lo = mid; else hi = mid;
     }
     const Tensor& T = list.t[lo];
-    const int64_t blk = b - T.first;
     r.rate = __fmul_rn(T.lr_scale, a.lr);
     r.keep = (float)(1.0 - (double)T.lr_scale * (double)a.lr * (double)T.decay);
+    const int64_t blk = b - T.first;
     if ((blk + 1) * kBlock > T.n) return step_block<-1, -1, -1, false>(T, a, r, blk, lane);
     switch (T.types & 0xfffu) {
 #define HG_ADAMW_CASE(P, G, S) \
@@ -380,7 +400,7 @@ __global__ void __launch_bounds__(32 * kWarps) step_kernel(const __grid_constant
         HG_ADAMW_CASE(kF16, kF16, kE4m3)
 #undef HG_ADAMW_CASE
     }
-    step_block<-1, -1, -1, true>(T, a, r, blk, lane);  // the rarer pairs of types
+    step_block<-1, -1, -1, true>(T, a, r, blk, lane);  // rarer pairs of types
 }
 
 }  // namespace adamw
