@@ -416,16 +416,22 @@ int hashgrid_linear_params(hashgrid_linear_t layer, int *in, int *out, int *dtyp
  * a layer with an activation reads. Elements of y's rows beyond `out` are left as they were.
  * Strides are at least the row's width (any value, odd ones included); 0 <= N < 2^31 - 256.
  * residual may be y itself (with ldr == ldy); no other output may overlap an input.
+ * workspace: workspace_bytes >= hashgrid_linear_forward_workspace(layer, N, ldx) of device memory
+ * that no other call uses until this one has finished (a captured graph uses it at every
+ * replay); its contents need no preparation and mean nothing afterwards.
  * device_status: as for hashgrid_mlp_forward (NULL, or a device int the caller sets to 0 and
  * the kernel sets to 1 if a bounded wait ran out, y being incomplete then).
  */
 int hashgrid_linear_forward(hashgrid_linear_t layer, const void *x, int64_t ldx, int64_t N, const void *w,
                             const float *b, const void *residual, int64_t ldr, void *y, int64_t ldy, int y_dtype,
-                            void *z, int *device_status, void *cuda_stream);
+                            void *z, void *workspace, size_t workspace_bytes, int *device_status, void *cuda_stream);
 
-/* Bytes of workspace that hashgrid_linear_backward needs for N rows (0 for a NULL layer or an
- * invalid N). Depends on the layer's sizes and N only. */
-size_t hashgrid_linear_workspace(hashgrid_linear_t layer, int64_t N);
+/* Bytes of workspace that the two calls need for N rows of these strides (0 for a NULL layer or
+ * an N outside [1, 2^31 - 256)). The forward call needs some only where rows do not begin on
+ * 16-byte boundaries (ldx or `in` no multiple of 8); a NULL workspace will do where it is 0. For
+ * given layer and strides the size does not shrink as N grows. */
+size_t hashgrid_linear_forward_workspace(hashgrid_linear_t layer, int64_t N, int64_t ldx);
+size_t hashgrid_linear_backward_workspace(hashgrid_linear_t layer, int64_t N, int64_t lddy, int64_t ldx);
 
 /*
  * hashgrid_linear_backward -- gradients of a loss with respect to a layer's input, weights and
@@ -443,9 +449,7 @@ size_t hashgrid_linear_workspace(hashgrid_linear_t layer, int64_t N);
  * lddx apart; dL_dw: [out][in] of dw_dtype (HASHGRID_F32 or the layer's dtype), contiguous;
  * dL_db: [out] fp32. Each of the three may be NULL, and is not computed then; all are
  * OVERWRITTEN. N = 0 writes zeros to dL_dw and dL_db. No output may overlap an input.
- * workspace: workspace_bytes >= hashgrid_linear_workspace(layer, N) of device memory that no
- * other call uses until this one has finished (a captured graph uses it at every replay); its
- * contents need no preparation and mean nothing afterwards.
+ * workspace: as for the forward call, of hashgrid_linear_backward_workspace bytes.
  */
 int hashgrid_linear_backward(hashgrid_linear_t layer, const void *dL_dy, int64_t lddy, const void *x, int64_t ldx,
                              int64_t N, const void *w, const void *z, void *dL_dx, int64_t lddx, int dx_dtype,

@@ -109,8 +109,9 @@ def _load() -> ctypes.CDLL:
         "hashgrid_linear_create": (i32, [i32, i32, i32, i32, ctypes.POINTER(vp)]),
         "hashgrid_linear_destroy": (i32, [vp]),
         "hashgrid_linear_params": (i32, [vp] + [ctypes.POINTER(i32)] * 4),
-        "hashgrid_linear_forward": (i32, [vp, vp, i64, i64, vp, vp, vp, i64, vp, i64, i32, vp, vp, vp]),
-        "hashgrid_linear_workspace": (sz, [vp, i64]),
+        "hashgrid_linear_forward": (i32, [vp, vp, i64, i64, vp, vp, vp, i64, vp, i64, i32, vp, vp, sz, vp, vp]),
+        "hashgrid_linear_forward_workspace": (sz, [vp, i64, i64]),
+        "hashgrid_linear_backward_workspace": (sz, [vp, i64, i64, i64]),
         "hashgrid_linear_backward": (i32, [vp, vp, i64, vp, i64, i64, vp, vp, vp, i64, i32, vp, i32, vp, vp, sz, vp, vp]),
         "hashgrid_adamw_create": (i32, [ctypes.POINTER(AdamwTensor), i32, ctypes.POINTER(vp)]),
         "hashgrid_adamw_destroy": (i32, [vp]),
@@ -260,13 +261,18 @@ def hashgrid_linear_params(layer: int) -> dict:
 
 
 def hashgrid_linear_forward(layer: int, x, ldx: int, N: int, w, b, residual, ldr: int, y, ldy: int, y_dtype: int, z=None,
-                            device_status=None, stream=None) -> None:
+                            workspace=None, workspace_bytes: int = 0, device_status=None, stream=None) -> None:
     _check(lib.hashgrid_linear_forward(layer, _ptr(x), ldx, N, _ptr(w), _ptr(b), _ptr(residual), ldr, _ptr(y), ldy,
-                                       y_dtype, _ptr(z), _ptr(device_status), _stream(stream)))
+                                       y_dtype, _ptr(z), _ptr(workspace), workspace_bytes, _ptr(device_status),
+                                       _stream(stream)))
 
 
-def hashgrid_linear_workspace(layer: int, N: int) -> int:
-    return int(lib.hashgrid_linear_workspace(layer, N))
+def hashgrid_linear_forward_workspace(layer: int, N: int, ldx: int) -> int:
+    return int(lib.hashgrid_linear_forward_workspace(layer, N, ldx))
+
+
+def hashgrid_linear_backward_workspace(layer: int, N: int, lddy: int, ldx: int) -> int:
+    return int(lib.hashgrid_linear_backward_workspace(layer, N, lddy, ldx))
 
 
 def hashgrid_linear_backward(layer: int, dL_dy, lddy: int, x, ldx: int, N: int, w, z, dL_dx, lddx: int, dx_dtype: int,
@@ -402,6 +408,7 @@ class Linear:
     def __init__(self, in_features: int, out_features: int, dtype: int = HASHGRID_BF16,
                  activation: int = HASHGRID_ACT_NONE):
         self.in_features, self.out_features, self.dtype, self.activation = in_features, out_features, dtype, activation
+        self._shape = (out_features, in_features)
         self.handle = hashgrid_linear_create(in_features, out_features, dtype, activation)
 
     def __del__(self):
@@ -414,17 +421,18 @@ class Linear:
         import torch
         return torch.float16 if self.dtype == HASHGRID_F16 else torch.bfloat16
 
-    def forward(self, x, w, b=None, residual=None, y=None, z=None, device_status=None, stream=None):
+    def forward(self, x, w, b=None, residual=None, y=None, z=None, workspace=None, device_status=None, stream=None):
         """Returns y. ``w`` [out, in] contiguous; ``b`` [out] fp32; ``y`` (allocated if None, of ``residual``'s
         type or else the layer's) and ``residual`` of the layer's type or fp32; ``z``: a contiguous [N, out] tensor
-        that receives the pre-activation, for ``backward``."""
-        import torch
+        that receives the pre-activation, for ``backward``; ``workspace``: bytes from ``workspace()`` (allocated if
+        None; only rows that do not begin on 16-byte boundaries need any)."""
         N, own = x.shape[0], (self.dtype,)
         ldx = _rows(x, None, self.in_features, own, "x")
-        _flat(w, (self.out_features, self.in_features), own, "w")
+        _flat(w, self._shape, own, "w")
         if b is not None:
-            _flat(b, (self.out_features,), (HASHGRID_F32,), "b")
+            _flat(b, self._shape[:1], (HASHGRID_F32,), "b")
         if y is None:
+            import torch
             y = torch.empty((N, self.out_features), device=x.device,
                             dtype=self._torch_dtype() if residual is None else residual.dtype)
             _record(y, stream)
@@ -433,13 +441,28 @@ class Linear:
         ldr = 0 if residual is None else _rows(residual, N, self.out_features, (y_dtype,), "residual")
         if z is not None:
             _flat(z, (N, self.out_features), own, "z")
-        hashgrid_linear_forward(self.handle, x, ldx, N, w, b, residual, ldr, y, ldy, y_dtype, z, device_status, stream)
+        size = 0
+        if workspace is not None:
+            size = workspace.numel() * workspace.element_size()
+        elif ldx % 8 or self.in_features % 8:
+            size = lib.hashgrid_linear_forward_workspace(self.handle, N, ldx)
+            workspace = self._scratch(size, x.device, stream)
+        hashgrid_linear_forward(self.handle, x, ldx, N, w, b, residual, ldr, y, ldy, y_dtype, z, workspace, size,
+                                device_status, stream)
         return y
 
-    def workspace(self, N: int, device):
-        """Workspace for ``backward`` over up to N rows."""
+    def workspace(self, N: int, device, lddy: int | None = None, ldx: int | None = None):
+        """Workspace for ``forward`` and ``backward`` over up to N rows, of these row strides (any, if None)."""
+        odd = lambda width, ld: 2 * width + 1 if ld is None else ld  # noqa: E731
+        need = [hashgrid_linear_forward_workspace(self.handle, N, odd(self.in_features, ldx)),
+                hashgrid_linear_backward_workspace(self.handle, N, odd(self.out_features, lddy), odd(self.in_features, ldx))]
+        return self._scratch(max(need), device, None)
+
+    def _scratch(self, size: int, device, stream):
         import torch
-        return torch.empty(max(16, hashgrid_linear_workspace(self.handle, N)), dtype=torch.uint8, device=device)
+        t = torch.empty(max(16, size), dtype=torch.uint8, device=device)
+        _record(t, stream)
+        return t
 
     def backward(self, dL_dy, x, w, z=None, dL_dx=True, dL_dw=True, dL_db=True, workspace=None, device_status=None,
                  stream=None):
@@ -450,7 +473,7 @@ class Linear:
         N, own, either = dL_dy.shape[0], (self.dtype,), (self.dtype, HASHGRID_F32)
         lddy = _rows(dL_dy, None, self.out_features, own, "dL_dy")
         ldx = _rows(x, N, self.in_features, own, "x")
-        _flat(w, (self.out_features, self.in_features), own, "w")
+        _flat(w, self._shape, own, "w")
         if z is not None:
             _flat(z, (N, self.out_features), own, "z")
         if dL_dx is True:
@@ -464,12 +487,11 @@ class Linear:
             _record(dL_db, stream)
         lddx = 0 if dL_dx is None else _rows(dL_dx, N, self.in_features, either, "dL_dx")
         if dL_dw is not None:
-            _flat(dL_dw, (self.out_features, self.in_features), either, "dL_dw")
+            _flat(dL_dw, self._shape, either, "dL_dw")
         if dL_db is not None:
             _flat(dL_db, (self.out_features,), (HASHGRID_F32,), "dL_db")
         if workspace is None:
-            workspace = self.workspace(N, x.device)
-            _record(workspace, stream)
+            workspace = self._scratch(lib.hashgrid_linear_backward_workspace(self.handle, N, lddy, ldx), x.device, stream)
         hashgrid_linear_backward(self.handle, dL_dy, lddy, x, ldx, N, w, z, dL_dx, lddx,
                                  HASHGRID_F32 if dL_dx is None else _dtype_code(dL_dx, "dL_dx"), dL_dw,
                                  HASHGRID_F32 if dL_dw is None else _dtype_code(dL_dw, "dL_dw"), dL_db, workspace,

@@ -615,6 +615,12 @@ int check_row_count(int64_t N) {
     return ok();
 }
 
+int check_workspace(const void* p, size_t have, size_t need, int64_t N) {
+    if (need == 0) return ok();
+    if (have < need) return fail(HASHGRID_ERR_ARG, "workspace of %zu bytes, %zu are needed for N = %lld", have, need, (long long)N);
+    return check_buffer(p, need, "workspace");
+}
+
 int check_out_type(const hashgrid_linear_s* layer, int dtype, const char* name) {
     if (dtype != HASHGRID_F32 && dtype != layer->dtype)
         return fail(HASHGRID_ERR_ARG, "%s = %d is neither HASHGRID_F32 nor the layer's dtype %d", name, dtype, layer->dtype);
@@ -657,35 +663,43 @@ struct Array {
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// Tile width of a product: as few column tiles of at most 256 as there are, then more and
-// narrower ones until every SM has a tile, down to 32 columns; a multiple of 16.
-int tile_width(int64_t M, int64_t N, int sms) {
+// How a product is cut.
+struct Plan {
+    int bn;       // tile width, a multiple of 16
+    int cluster;  // blocks that share a tile's K, their shares added through shared memory
+    int splits;   // or parts of K that go to a workspace
+    bool pair;    // 256-row tiles by pairs of SMs
+};
+
+// Where 256 x 256 tiles by pairs of SMs occupy the device: those. Else 128-row tiles: as few column tiles
+// as there can be while every SM has one, then narrower ones, down to 64 columns, and if
+// those are still too few, a split of K over up to 8 blocks of a cluster, each with two
+// 64-wide steps at least.
+Plan make_plan(int64_t M, int64_t N, int64_t K, int sms) {
     const int64_t mt = ceil_div(M, hg::linear::kBm);
     int64_t nt = ceil_div(N, 256);
-    while (mt * nt < sms && ceil_div(N, nt) > 32) ++nt;
-    return ceil_div(ceil_div(N, nt), 16) * 16;
+    const int wide = ceil_div(ceil_div(N, nt), 32) * 32;
+    if (N >= 160 && (int64_t)ceil_div(M, 256) * nt >= sms / 2 && K >= 256) return Plan{wide, 1, 1, true};
+    while (mt * nt < sms && ceil_div(N, nt) > 64) ++nt;
+    Plan p{ceil_div(ceil_div(N, nt), 16) * 16, 1, 1, false};
+    const int64_t tiles = mt * ceil_div(N, p.bn);
+    while (p.cluster < 8 && tiles * p.cluster * 2 <= 2 * sms && 4 * p.cluster * hg::linear::kBk <= K) p.cluster *= 2;
+    return p;
 }
 
-// One operand's share of a stage, and its tensor map where TMA can copy it: rows (of more than
-// one) must start on 16-byte boundaries.
-int set_side(hg::linear::Side& s, CUtensorMap& map, const Array& a, int rows_wanted, const char* what) {
-    s.p = a.p;
-    s.ld = a.ld;
-    s.bytes = strided_bytes(a.outer, a.inner, a.ld, 2);
-    s.outer = a.outer;
-    s.inner = a.inner;
+// One operand's share of a stage, and its tensor map. `wanted` rows (or columns) of it are staged at a
+// time; those that the array does not have are left out.
+int set_side(hg::linear::Side& s, CUtensorMap& map, const Array& a, int wanted, const char* what) {
+    const int64_t extent = a.mn ? a.inner : a.outer;
     s.mn = a.mn;
-    s.role = a.role;
-    s.direct = a.outer > 1 && a.ld % 8 != 0;
-    const int64_t extent = a.mn ? a.inner : a.outer;  // rows beyond it are not staged: what they would give is not stored
     if (a.mn) {
         s.box_rows = hg::linear::kBk;
-        s.boxes = ceil_div(std::min<int64_t>(rows_wanted, extent), 64);
+        s.boxes = ceil_div(std::min<int64_t>(wanted, extent), 64);
     } else {
-        s.box_rows = (int)std::min<int64_t>(rows_wanted, ceil_div(extent, 8) * 8);
+        s.box_rows = (int)std::min<int64_t>(wanted, ceil_div(extent, 8) * 8);
         s.boxes = 1;
     }
-    if (s.direct) return ok();
+    s.bytes = s.box_rows * s.boxes * 128;
     const cuuint64_t dims[2] = {(cuuint64_t)a.inner, (cuuint64_t)a.outer};
     const cuuint64_t strides[1] = {(cuuint64_t)(a.outer > 1 ? a.ld : (a.inner + 7) / 8 * 8) * 2};
     const cuuint32_t box[2] = {64, (cuuint32_t)s.box_rows}, ones[2] = {1, 1};
@@ -700,83 +714,146 @@ int set_side(hg::linear::Side& s, CUtensorMap& map, const Array& a, int rows_wan
 
 bool vector_rows(const void* p, int64_t ld, size_t elem) { return p == nullptr || ((size_t)ld * elem) % 16 == 0; }
 
-// D[M, N] = A B^T over K on the tensor cores. splits > 1: K is cut into so many parts, each an
+// D[M, N] = A B^T over K on the tensor cores. plan.splits > 1: K is cut into so many parts, each an
 // fp32 [M, N] of its own in e.out.
 template <typename T>
-int launch_gemm(const Array& A, const Array& B, int64_t M, int64_t N, int64_t K, hg::linear::Epilogue e, int bn, int splits,
+int launch_gemm(const Array& A, const Array& B, int64_t M, int64_t N, int64_t K, const hg::linear::Epilogue& e, const Plan& plan,
                 int* status, const char* what, cudaStream_t s) {
     namespace hl = hg::linear;
+    const int bn = plan.bn, splits = std::max(plan.splits, plan.cluster), group = plan.pair ? 2 : 1;
     hl::Gemm g;
     std::memset(&g, 0, sizeof g);
     if (int rc = set_side(g.a, g.ta, A, hl::kBm, what)) return rc;
-    if (int rc = set_side(g.b, g.tb, B, bn, what)) return rc;
+    if (int rc = set_side(g.b, g.tb, B, bn / group, what)) return rc;
     g.M = M;
     g.N = N;
     g.bn = bn;
     g.columns = ceil_div(bn, 32) * 32;
     g.tmem_columns = 64;
     while ((int)g.tmem_columns < 2 * g.columns) g.tmem_columns *= 2;
-    g.stage_bytes = hl::kStageA + (B.mn ? ceil_div(bn, 64) * 64 : bn) * 128;
-    const int sms = device_sms();
-    const bool direct = g.a.direct || g.b.direct;
-    // Two blocks a SM where tensor memory and shared memory allow: one's loads and stores then fill the other's gaps.
-    const int per_sm = !direct && g.tmem_columns <= 256 ? 2 : 1;
-    const int budget = (per_sm == 2 ? 113 : 227) * 1024;
-    g.stages = std::min(hl::kMaxStages, (budget - (int)hl::gemm_smem(0, 0)) / g.stage_bytes);
     g.kblocks = ceil_div(K, hl::kBk);
     g.kblocks_per_split = ceil_div(g.kblocks, splits);
-    g.mt = ceil_div(M, hl::kBm);
+    g.mt = ceil_div(M, hl::kBm * group);
     g.nt = ceil_div(N, bn);
-    const uint32_t type = std::is_same<T, __half>::value ? 0u : 1u;
-    g.idesc = (1u << 4) | (type << 7) | (type << 10) | ((A.mn ? 1u : 0u) << 15) | ((B.mn ? 1u : 0u) << 16) |
-              ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(hl::kBm >> 4) << 24);
-    g.e = e;
-    const size_t os = e.out_f32 ? 4 : 2;
-    g.e.vectors = vector_rows(e.out, e.ldo, os) && vector_rows(e.residual, e.ldr, os) && vector_rows(e.z, e.ldz, 2);
-    g.split_stride = splits > 1 ? M * N : 0;
-    if (g.split_stride % 4 != 0) g.e.vectors = 0;
-    g.status = status;
+    const int sms = device_sms();
     const int64_t tiles = (int64_t)g.mt * g.nt;
     if (tiles > (1 << 30)) return fail(HASHGRID_ERR_ARG, "%s: too many tiles", what);
-    const size_t smem = hl::gemm_smem(g.stages, g.stage_bytes);
-    const dim3 grid((unsigned)std::min<int64_t>(tiles, std::max(1, per_sm * sms / splits)), (unsigned)splits);
-    auto k = direct ? hl::gemm_kernel<T, true> : hl::gemm_kernel<T, false>;
+    // B stays in shared memory where one column tile covers it, it is small and its block has several tiles to compute.
+    g.resident = splits == 1 && group == 1 && g.nt == 1 && g.kblocks * g.b.bytes <= 32 * 1024 && g.mt > 2 * sms;
+    const int kept = g.resident ? g.kblocks * g.b.bytes : 0;
+    g.stage_bytes = g.a.bytes + (g.resident ? 0 : g.b.bytes);
+    g.cluster = plan.cluster;
+    // Two blocks a SM where tensor memory and shared memory allow: one's loads and stores then fill the other's gaps. The MMA
+    // reads 128 rows (two boxes) of A whatever the product has: the staging area behind the stages keeps that in bounds.
+    const int per_sm = group == 1 && g.tmem_columns <= 256 ? 2 : 1;
+    const int budget = (per_sm == 2 ? 113 : 227) * 1024 - 1024;  // less what the kernel has of its own
+    g.stages = std::min(hl::kMaxStages, (budget - kept - (int)hl::gemm_smem(0)) / g.stage_bytes);
+    if (g.cluster > 1)  // a split product's shares lie in the stages
+        while (g.stages * g.stage_bytes < 4 * ceil_div(bn, 32) * 4096) ++g.stages;
+    const uint32_t type = std::is_same<T, __half>::value ? 0u : 1u;
+    g.idesc = (1u << 4) | (type << 7) | (type << 10) | ((A.mn ? 1u : 0u) << 15) | ((B.mn ? 1u : 0u) << 16) |
+              ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(hl::kBm * group >> 4) << 24);
+    g.e = e;
+    const size_t os = e.out_f32 ? 4 : 2;
+    g.split_stride = plan.splits > 1 ? M * N : 0;
+    const bool vectors = N % 8 == 0 && vector_rows(e.out, e.ldo, os) && vector_rows(e.residual, e.ldr, os) && vector_rows(e.z, e.ldz, 2);
+    g.status = status;
+    const size_t smem = hl::gemm_smem(g.stages * g.stage_bytes + kept);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(plan.cluster > 1 ? tiles : group * std::min<int64_t>(tiles, std::max(1, per_sm * sms / splits / group))),
+                       (unsigned)splits);
+    cfg.blockDim = dim3(hl::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)group;
+    at.val.clusterDim.y = (unsigned)plan.cluster;
+    at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = plan.cluster > 1 || plan.pair ? 1 : 0;
+    auto k = plan.pair ? (vectors ? hl::gemm_kernel<T, true, true> : hl::gemm_kernel<T, true, false>)
+                       : (vectors ? hl::gemm_kernel<T, false, true> : hl::gemm_kernel<T, false, false>);
     if (int rc = prepare_smem(k, smem)) return rc;
-    k<<<grid, direct ? hl::kThreadsDirect : hl::kThreads, smem, s>>>(g);
+    if (cudaLaunchKernelEx(&cfg, k, g) != cudaSuccess) return launch_status(what);
+    return ok();
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// TMA copies arrays whose rows begin on 16-byte boundaries; others are copied into such rows first.
+bool aligned_rows(const Array& a) { return a.outer <= 1 || a.ld % 8 == 0; }
+size_t realigned_bytes(int64_t outer, int64_t inner) { return align256((size_t)outer * ((inner + 7) / 8 * 8) * 2); }
+
+// Copies those of up to two arrays that need it into `work` and points them there.
+int realign(Array* const* arrays, int count, char* work, const char* what, cudaStream_t s) {
+    hg::linear::RealignList l;
+    std::memset(&l, 0, sizeof l);
+    int n = 0;
+    for (int i = 0; i < count; ++i) {
+        Array& a = *arrays[i];
+        if (aligned_rows(a)) continue;
+        hg::linear::Realign& r = l.a[n++];
+        r.p = a.p;
+        r.to = reinterpret_cast<uint16_t*>(work);
+        r.bytes = strided_bytes(a.outer, a.inner, a.ld, 2);
+        r.outer = a.outer;
+        r.ld = a.ld;
+        r.chunks = (a.inner + 7) / 8;
+        r.inner = (int)a.inner;
+        r.role = a.role;
+        l.total += a.outer * r.chunks;
+        if (n == 1) l.first = l.total;
+        work += realigned_bytes(a.outer, a.inner);
+        a = Array{r.to, a.outer, a.inner, r.chunks * 8, a.mn, hg::kChkWork};
+    }
+    if (n == 0) return ok();
+    const int64_t blocks = (l.total + 1023) / 1024;
+    if (blocks > 0x7fffffffLL) return fail(HASHGRID_ERR_ARG, "%s: too many rows to realign", what);
+    hg::linear::realign_kernel<<<(unsigned)blocks, 256, 0, s>>>(l);
     return launch_status(what);
 }
 
-// The backward pass's workspace: dz (where it has to be computed), the parts of db, the parts of dw.
+// The backward pass's workspace: the copies of x and w (or dy) with aligned rows, dz (where it has to be
+// computed), the parts of db, the parts of dw.
 struct LinearWork {
     int64_t lddz;   // elements
     int parts;      // row shares of the db sums
     int splits;     // row shares of dw
-    size_t dz, sums, dw, bytes;  // offsets, total
+    size_t copies, dy, dz, sums, dw, bytes;  // offsets, total
 };
 
-size_t align256(size_t n) { return (n + 255) / 256 * 256; }
-
-// dw sums over the rows: so many shares of them that every SM has a tile of one, each of 8 or
-// more 64-row steps.
-LinearWork linear_work(const hashgrid_linear_s* l, int64_t N) {
+// dw sums over the rows: beyond what a cluster's 8 blocks can share, so many shares of them that
+// every SM has a tile of one.
+LinearWork linear_work(const hashgrid_linear_s* l, int64_t N, int64_t lddy, int64_t ldx) {
     LinearWork w;
     constexpr int kSms = 148;  // the workspace's size may not depend on the device
     w.lddz = (l->out + 7) / 8 * 8;
     w.parts = (int)std::min<int64_t>(256, (N + 63) / 64);
     const int64_t tiles = (int64_t)ceil_div(l->out, hg::linear::kBm) * ceil_div(l->in, 256);
-    w.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kSms / tiles, N / (8 * hg::linear::kBk)));
-    w.dz = 0;
-    w.sums = l->act == HASHGRID_ACT_NONE ? 0 : align256((size_t)N * w.lddz * 2);
+    w.splits = N <= 16384 ? 1 : (int)std::max<int64_t>(1, kSms / tiles);
+    const bool plain = l->act == HASHGRID_ACT_NONE;
+    w.copies = 0;
+    w.dy = (l->in % 8 != 0 ? realigned_bytes(l->out, l->in) : 0) + (ldx % 8 != 0 ? realigned_bytes(N, l->in) : 0);
+    w.dz = w.dy + (plain && lddy % 8 != 0 ? realigned_bytes(N, l->out) : 0);
+    w.sums = w.dz + (plain ? 0 : align256((size_t)N * w.lddz * 2));
     w.dw = w.sums + align256((size_t)w.parts * l->out * sizeof(float));
     w.bytes = w.dw + (w.splits > 1 ? align256((size_t)w.splits * l->in * l->out * sizeof(float)) : 0);
     return w;
 }
 
+size_t forward_work(const hashgrid_linear_s* l, int64_t N, int64_t ldx) {
+    return (l->in % 8 != 0 && l->out > 1 ? realigned_bytes(l->out, l->in) : 0) + (ldx % 8 != 0 && N > 1 ? realigned_bytes(N, l->in) : 0);
+}
+
 template <typename T>
 int launch_linear_forward(const hashgrid_linear_s* l, const void* x, int64_t ldx, int64_t N, const void* w,
-                          const hg::linear::Epilogue& e, int* status, cudaStream_t s) {
-    return launch_gemm<T>({x, N, l->in, ldx, false, hg::kChkX}, {w, l->out, l->in, l->in, false, hg::kChkWeights}, N, l->out, l->in, e,
-                          tile_width(N, l->out, device_sms()), 1, status, "linear_forward", s);
+                          const hg::linear::Epilogue& e, char* work, int* status, cudaStream_t s) {
+    static const char* what = "linear_forward";
+    Array A{x, N, l->in, ldx, false, hg::kChkX}, B{w, l->out, l->in, l->in, false, hg::kChkWeights};
+    Array* both[2] = {&A, &B};
+    if (int rc = realign(both, 2, work, what, s)) return rc;
+    return launch_gemm<T>(A, B, N, l->out, l->in, e, make_plan(N, l->out, l->in, device_sms()), status, what, s);
 }
 
 template <typename T>
@@ -784,8 +861,14 @@ int launch_linear_backward(const hashgrid_linear_s* l, const void* dy, int64_t l
                            int64_t N, const void* w, const void* z, void* dx, int64_t lddx, int dx_dtype, void* dw,
                            int dw_dtype, float* db, char* work, int* status, cudaStream_t s) {
     static const char* what = "linear_backward";
-    const LinearWork lw = linear_work(l, N);
+    const LinearWork lw = linear_work(l, N, lddy, ldx);
     Array dz{dy, N, l->out, lddy, false, hg::kChkDout};
+    Array W{w, l->out, l->in, l->in, true, hg::kChkWeights}, X{x, N, l->in, ldx, true, hg::kChkX};
+    Array* list[2];
+    int n = 0;
+    if (dx != nullptr) list[n++] = &W;
+    if (dw != nullptr) list[n++] = &X;
+    if (int rc = realign(list, n, work + lw.copies, what, s)) return rc;
     const bool convert = l->act != HASHGRID_ACT_NONE && (dx != nullptr || dw != nullptr);
     if (convert || db != nullptr) {
         T* to = convert ? reinterpret_cast<T*>(work + lw.dz) : nullptr;
@@ -800,20 +883,23 @@ int launch_linear_backward(const hashgrid_linear_s* l, const void* dy, int64_t l
             if (int rc = launch_status(what)) return rc;
         }
     }
+    if (!convert && n > 0) {
+        Array* d = &dz;
+        if (int rc = realign(&d, 1, work + lw.dy, what, s)) return rc;
+    }
     if (dx != nullptr) {
-        const hg::linear::Epilogue e{nullptr, nullptr, dx, nullptr, 0, lddx, 0, dx_dtype == HASHGRID_F32, hg::linear::kNoAct, hg::kChkOut, 0};
-        if (int rc = launch_gemm<T>(dz, {w, l->out, l->in, l->in, true, hg::kChkWeights}, N, l->in, l->out, e,
-                                    tile_width(N, l->in, device_sms()), 1, status, what, s))
-            return rc;
+        const hg::linear::Epilogue e{nullptr, nullptr, dx, nullptr, 0, lddx, 0, dx_dtype == HASHGRID_F32, hg::linear::kNoAct, hg::kChkOut};
+        if (int rc = launch_gemm<T>(dz, W, N, l->in, l->out, e, make_plan(N, l->in, l->out, device_sms()), status, what, s)) return rc;
     }
     if (dw != nullptr) {
         const bool parts = lw.splits > 1;
         float* out = reinterpret_cast<float*>(work + lw.dw);
         const hg::linear::Epilogue e{nullptr, nullptr, parts ? out : dw, nullptr, 0, l->in, 0, parts || dw_dtype == HASHGRID_F32,
-                                     hg::linear::kNoAct, parts ? hg::kChkWork : hg::kChkGrad, 0};
-        const int bn = parts ? ceil_div(ceil_div(l->in, ceil_div(l->in, 256)), 16) * 16 : tile_width(l->out, l->in, device_sms());
+                                     hg::linear::kNoAct, parts ? hg::kChkWork : hg::kChkGrad};
+        const Plan plan = parts ? Plan{ceil_div(ceil_div(l->in, ceil_div(l->in, 256)), 16) * 16, 1, lw.splits, false}
+                                : make_plan(l->out, l->in, N, device_sms());
         dz.mn = true;
-        if (int rc = launch_gemm<T>(dz, {x, N, l->in, ldx, true, hg::kChkX}, l->out, l->in, N, e, bn, lw.splits, status, what, s)) return rc;
+        if (int rc = launch_gemm<T>(dz, X, l->out, l->in, N, e, plan, status, what, s)) return rc;
         if (parts) {
             const int64_t n = (int64_t)l->in * l->out;
             const unsigned blocks = (unsigned)((n + 255) / 256);
@@ -1280,7 +1366,7 @@ int hashgrid_linear_params(hashgrid_linear_t l, int* in, int* out, int* dtype, i
 
 int hashgrid_linear_forward(hashgrid_linear_t l, const void* x, int64_t ldx, int64_t N, const void* w, const float* b,
                             const void* residual, int64_t ldr, void* y, int64_t ldy, int y_dtype, void* z,
-                            int* device_status, void* cuda_stream) {
+                            void* workspace, size_t workspace_bytes, int* device_status, void* cuda_stream) {
     if (int rc = check_layer(l)) return rc;
     if (int rc = check_row_count(N)) return rc;
     if (int rc = check_out_type(l, y_dtype, "y_dtype")) return rc;
@@ -1295,22 +1381,31 @@ int hashgrid_linear_forward(hashgrid_linear_t l, const void* x, int64_t ldx, int
     if (int rc = check_rows(y, N, l->out, ldy, ys, "y")) return rc;
     if (z != nullptr)
         if (int rc = check_buffer(z, (size_t)N * l->out * 2, "z")) return rc;
+    const size_t need = forward_work(l, N, ldx);
+    if (int rc = check_workspace(workspace, workspace_bytes, need, N)) return rc;
     if (device_status != nullptr)
         if (int rc = check_buffer(device_status, sizeof(int), "device_status")) return rc;
-    const hg::linear::Epilogue e{b, residual, y, z, ldr, ldy, l->out, y_dtype == HASHGRID_F32, l->act, hg::kChkOut, 0};
+    const hg::linear::Epilogue e{b, residual, y, z, ldr, ldy, l->out, y_dtype == HASHGRID_F32, l->act, hg::kChkOut};
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
     return run_checked(s, {{hg::kChkX, x, strided_bytes(N, l->in, ldx, 2)}, {hg::kChkWeights, w, (size_t)l->in * l->out * 2},
                            {hg::kChkBias, b, (size_t)l->out * sizeof(float)}, {hg::kChkResidual, residual, strided_bytes(N, l->out, ldr, ys)},
-                           {hg::kChkOut, y, strided_bytes(N, l->out, ldy, ys)}, {hg::kChkZ, z, (size_t)N * l->out * 2}},
+                           {hg::kChkOut, y, strided_bytes(N, l->out, ldy, ys)}, {hg::kChkZ, z, (size_t)N * l->out * 2},
+                           {hg::kChkWork, workspace, need}},
                        "linear_forward", [&]() -> int {
-        return l->dtype == HASHGRID_F16 ? launch_linear_forward<__half>(l, x, ldx, N, w, e, device_status, s)
-                                        : launch_linear_forward<__nv_bfloat16>(l, x, ldx, N, w, e, device_status, s);
+        char* ws = static_cast<char*>(workspace);
+        return l->dtype == HASHGRID_F16 ? launch_linear_forward<__half>(l, x, ldx, N, w, e, ws, device_status, s)
+                                        : launch_linear_forward<__nv_bfloat16>(l, x, ldx, N, w, e, ws, device_status, s);
     });
 }
 
-size_t hashgrid_linear_workspace(hashgrid_linear_t layer, int64_t N) {
+size_t hashgrid_linear_forward_workspace(hashgrid_linear_t layer, int64_t N, int64_t ldx) {
     if (layer == nullptr || N < 1 || N >= kMaxRows) return 0;
-    return linear_work(layer, N).bytes;
+    return forward_work(layer, N, ldx);
+}
+
+size_t hashgrid_linear_backward_workspace(hashgrid_linear_t layer, int64_t N, int64_t lddy, int64_t ldx) {
+    if (layer == nullptr || N < 1 || N >= kMaxRows) return 0;
+    return linear_work(layer, N, lddy, ldx).bytes;
 }
 
 int hashgrid_linear_backward(hashgrid_linear_t l, const void* dL_dy, int64_t lddy, const void* x, int64_t ldx, int64_t N,
@@ -1343,10 +1438,8 @@ int hashgrid_linear_backward(hashgrid_linear_t l, const void* dL_dy, int64_t ldd
     }
     if (l->act != HASHGRID_ACT_NONE)
         if (int rc = check_buffer(z, (size_t)N * l->out * 2, "z")) return rc;
-    const size_t need = hashgrid_linear_workspace(l, N);
-    if (workspace_bytes < need)
-        return fail(HASHGRID_ERR_ARG, "workspace of %zu bytes, %zu are needed for N = %lld", workspace_bytes, need, (long long)N);
-    if (int rc = check_buffer(workspace, need, "workspace")) return rc;
+    const size_t need = linear_work(l, N, lddy, ldx).bytes;
+    if (int rc = check_workspace(workspace, workspace_bytes, need, N)) return rc;
     if (device_status != nullptr)
         if (int rc = check_buffer(device_status, sizeof(int), "device_status")) return rc;
     return run_checked(s, {{hg::kChkX, x, strided_bytes(N, l->in, ldx, 2)}, {hg::kChkWeights, w, (size_t)l->in * l->out * 2},

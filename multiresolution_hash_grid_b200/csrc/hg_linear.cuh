@@ -28,27 +28,126 @@ template <> __device__ __forceinline__ __half from_float<__half>(float x) { retu
 template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 template <> __device__ __forceinline__ float from_float<float>(float x) { return x; }
 
-__device__ __forceinline__ float activate(float z, int act) {
-    switch (act) {
-        case kRelu: return z > 0.f ? z : 0.f;
-        case kGelu: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-        case kSilu: return z / (1.f + expf(-z));
-    }
-    return z;
+// Pairs of fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float2 a) { return (uint64_t)__float_as_uint(a.y) << 32 | __float_as_uint(a.x); }
+__device__ __forceinline__ float2 unpair(uint64_t a) {
+    return make_float2(__uint_as_float((uint32_t)a), __uint_as_float((uint32_t)(a >> 32)));
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(pair(a)), "l"(pair(b)), "l"(pair(c)));
+    return unpair(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair(a)), "l"(pair(b)));
+    return unpair(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair(a)), "l"(pair(b)));
+    return unpair(d);
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float2 rcp2(float2 a) { return make_float2(rcp_approx(a.x), rcp_approx(a.y)); }
+
+// The activations come without branches and two at a time, since a layer's output passes through
+// one warp instruction after another while the tensor cores wait for its accumulator.
+//
+// GELU z Phi(z): with the upper tail Q(|z|) = 1 - Phi(|z|) it is max(z, 0) - |z| Q(|z|). Q by Abramowitz
+// and Stegun 7.1.26: erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), off by at
+// most 1.5e-7, which is 7.5e-8 |z| here, 1.3 half steps of fp32. `e` gives exp(-z^2 / 2).
+__device__ __forceinline__ float2 upper_tail(float2 a, float2& e) {
+    const float2 s = mul2(mul2(a, a), both(-0.72134752f));  // -a^2 / 2 in powers of two
+    e = make_float2(exp2_approx(s.x), exp2_approx(s.y));
+    const float2 t = rcp2(fma2(a, both(0.23164190f), both(1.f)));
+    float2 q = fma2(t, both(0.5307027145f), both(-0.7265760135f));
+    q = fma2(q, t, both(0.7107068705f));
+    q = fma2(q, t, both(-0.142248368f));
+    q = fma2(q, t, both(0.127414796f));
+    return mul2(mul2(q, t), e);
+}
+__device__ __forceinline__ float2 magnitude(float2 z) { return make_float2(fabsf(z.x), fabsf(z.y)); }
+
+__device__ __forceinline__ float2 gelu2(float2 z) {
+    float2 e;
+    const float2 a = make_float2(fminf(fabsf(z.x), 64.f), fminf(fabsf(z.y), 64.f));  // Q is 0 there, and 0 times infinity none
+    const float2 q = upper_tail(a, e);
+    return fma2(make_float2(-a.x, -a.y), q, make_float2(z.x > 0.f ? z.x : z.x != z.x ? z.x : 0.f, z.y > 0.f ? z.y : z.y != z.y ? z.y : 0.f));
+}
+// 1 / (1 + exp(-z)); exp2's argument is rounded, which costs |z| 2^-24.
+__device__ __forceinline__ float2 sigmoid2(float2 z) {
+    const float2 s = mul2(z, both(-1.44269504f));
+    return rcp2(add2(make_float2(exp2_approx(s.x), exp2_approx(s.y)), both(1.f)));
 }
 
-// act'(z). GELU: Phi(z) + z phi(z); SILU: s (1 + z (1 - s)).
-__device__ __forceinline__ float slope(float z, int act) {
+// kN values, kN even.
+template <int kN>
+__device__ __forceinline__ void activate(float (&y)[kN], int act) {
     switch (act) {
-        case kRelu: return z > 0.f ? 1.f : 0.f;
+        case kRelu:
+#pragma unroll
+            for (int j = 0; j < kN; ++j) y[j] = y[j] > 0.f ? y[j] : 0.f;
+            break;
         case kGelu:
-            return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
-        case kSilu: {
-            const float s = 1.f / (1.f + expf(-z));
-            return s * (1.f + z * (1.f - s));
-        }
+#pragma unroll
+            for (int j = 0; j < kN; j += 2) {
+                const float2 r = gelu2(make_float2(y[j], y[j + 1]));
+                y[j] = r.x;
+                y[j + 1] = r.y;
+            }
+            break;
+        case kSilu:
+#pragma unroll
+            for (int j = 0; j < kN; j += 2) {
+                const float2 z = make_float2(y[j], y[j + 1]), r = mul2(z, sigmoid2(z));
+                y[j] = r.x;
+                y[j + 1] = r.y;
+            }
+            break;
     }
-    return 1.f;
+}
+
+// d[j] act'(z[j]). GELU: Phi(z) + z phi(z); SILU: s (1 + z (1 - s)).
+template <int kN>
+__device__ __forceinline__ void times_slope(float (&d)[kN], const float (&z)[kN], int act) {
+    switch (act) {
+        case kRelu:
+#pragma unroll
+            for (int j = 0; j < kN; ++j) d[j] = z[j] > 0.f ? d[j] : 0.f;
+            break;
+        case kGelu:
+#pragma unroll
+            for (int j = 0; j < kN; j += 2) {
+                const float2 v = make_float2(z[j], z[j + 1]), a = magnitude(v);
+                float2 e;
+                const float2 q = upper_tail(a, e);
+                const float2 cdf = make_float2(v.x > 0.f ? 1.f - q.x : q.x, v.y > 0.f ? 1.f - q.y : q.y);
+                const float2 s = fma2(mul2(v, both(0.39894228f)), e, cdf);
+                d[j] *= s.x;
+                d[j + 1] *= s.y;
+            }
+            break;
+        case kSilu:
+#pragma unroll
+            for (int j = 0; j < kN; j += 2) {
+                const float2 v = make_float2(z[j], z[j + 1]), s = sigmoid2(v);
+                const float2 r = mul2(s, fma2(v, fma2(s, both(-1.f), both(1.f)), both(1.f)));
+                d[j] *= r.x;
+                d[j + 1] *= r.y;
+            }
+            break;
+    }
 }
 
 // What happens to D[row][col] on its way out; out is of type T or fp32.
@@ -60,7 +159,6 @@ struct Epilogue {
     int64_t ldr, ldo, ldz;
     int out_f32, act;
     int role;              // CheckRole of out
-    int vectors;           // every array takes 16-byte vectors at columns that are multiples of 8
 };
 
 template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
@@ -77,101 +175,152 @@ template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w)
     return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
 }
 
-// One value: any alignment, any width.
+__device__ __forceinline__ float bias1(const Epilogue& e, int64_t col) {
+    return e.bias != nullptr && in_bounds<kChkBias>(e.bias + col, 4) ? __ldg(e.bias + col) : 0.f;
+}
+
 template <typename T>
-__device__ __forceinline__ void emit(const Epilogue& e, int64_t row, int64_t col, float acc) {
-    float z = acc;
-    if (e.bias != nullptr && in_bounds<kChkBias>(e.bias + col, 4)) z += e.bias[col];
-    if (e.z != nullptr) {
-        T* p = static_cast<T*>(e.z) + row * e.ldz + col;
-        if (in_bounds<kChkZ>(p, sizeof(T))) *p = from_float<T>(z);
-    }
-    float y = activate(z, e.act);
+__device__ __forceinline__ float residual1(const Epilogue& e, int64_t row, int64_t col) {
+    if (e.residual == nullptr) return 0.f;
     if (e.out_f32) {
-        if (e.residual != nullptr) {
-            const float* r = static_cast<const float*>(e.residual) + row * e.ldr + col;
-            if (in_bounds<kChkResidual>(r, 4)) y += *r;
-        }
-        float* p = static_cast<float*>(e.out) + row * e.ldo + col;
+        const float* r = static_cast<const float*>(e.residual) + row * e.ldr + col;
+        return in_bounds<kChkResidual>(r, 4) ? *r : 0.f;
+    }
+    const T* r = static_cast<const T*>(e.residual) + row * e.ldr + col;
+    return in_bounds<kChkResidual>(r, sizeof(T)) ? to_float(*r) : 0.f;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_z1(const Epilogue& e, int64_t row, int64_t col, float z) {
+    T* p = static_cast<T*>(e.z) + row * e.ldz + col;
+    if (in_bounds<kChkZ>(p, sizeof(T))) *p = from_float<T>(z);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_y1(const Epilogue& e, void* out, int64_t row, int64_t col, float y) {
+    if (e.out_f32) {
+        float* p = static_cast<float*>(out) + row * e.ldo + col;
         if (in_bounds_role(e.role, p, 4)) *p = y;
     } else {
-        if (e.residual != nullptr) {
-            const T* r = static_cast<const T*>(e.residual) + row * e.ldr + col;
-            if (in_bounds<kChkResidual>(r, sizeof(T))) y += to_float(*r);
-        }
-        T* p = static_cast<T*>(e.out) + row * e.ldo + col;
+        T* p = static_cast<T*>(out) + row * e.ldo + col;
         if (in_bounds_role(e.role, p, sizeof(T))) *p = from_float<T>(y);
     }
 }
 
-// Eight neighbouring values (col a multiple of 8), bias already added, as 16-byte vectors.
+// Where value (row, column) of a 32 x 32 chunk of floats lies: 16-byte units of a row are exchanged by
+// its number, so that both a lane that writes a row and four lanes that read one meet no bank twice.
+__device__ __forceinline__ int unit_of(int row, int unit) { return row * 8 + (unit ^ (row & 7)); }
+
+__device__ __forceinline__ void bias8(const Epilogue& e, int64_t col, float (&b)[8]) {
+    if (e.bias == nullptr || !in_bounds<kChkBias>(e.bias + col, 32)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b[j] = 0.f;
+        return;
+    }
+    const float4 lo = __ldg(reinterpret_cast<const float4*>(e.bias + col)), hi = __ldg(reinterpret_cast<const float4*>(e.bias + col + 4));
+    b[0] = lo.x; b[1] = lo.y; b[2] = lo.z; b[3] = lo.w;
+    b[4] = hi.x; b[5] = hi.y; b[6] = hi.z; b[7] = hi.w;
+}
+
 template <typename T>
-__device__ __forceinline__ void emit8(const Epilogue& e, int64_t row, int64_t col, float (&y)[8]) {
+__device__ __forceinline__ uint4 pack8(const float* y) {
+    return make_uint4(pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3]), pack2<T>(y[4], y[5]), pack2<T>(y[6], y[7]));
+}
+
+// kRows rows (row, row + 8, ...) of eight neighbouring values, bias already added, in 16-byte
+// vectors. Rows from `rows` on are not there. q: the 16-bit residuals, if there are any.
+template <typename T, int kRows>
+__device__ __forceinline__ void emit_vectors(const Epilogue& e, void* out, int64_t row, int64_t rows, int64_t col, float (&y)[kRows][8],
+                                             const uint4 (&q)[kRows]) {
     if (e.z != nullptr) {
         T* p = static_cast<T*>(e.z) + row * e.ldz + col;
-        if (in_bounds<kChkZ>(p, 16))
-            *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3]), pack2<T>(y[4], y[5]), pack2<T>(y[6], y[7]));
+#pragma unroll
+        for (int r = 0; r < kRows; ++r, p += 8 * e.ldz)
+            if (row + 8 * r < rows && in_bounds<kChkZ>(p, 16)) *reinterpret_cast<uint4*>(p) = pack8<T>(y[r]);
     }
-    switch (e.act) {
-        case kRelu:
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = activate(y[j], kRelu);
-            break;
-        case kGelu:
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = activate(y[j], kGelu);
-            break;
-        case kSilu:
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = activate(y[j], kSilu);
-            break;
-    }
+    for (int r = 0; r < kRows; ++r) activate(y[r], e.act);
     if (e.out_f32) {
         if (e.residual != nullptr) {
-            const float* r = static_cast<const float*>(e.residual) + row * e.ldr + col;
-            if (in_bounds<kChkResidual>(r, 32)) {
-                const float4 a = *reinterpret_cast<const float4*>(r), b = *reinterpret_cast<const float4*>(r + 4);
-                y[0] += a.x; y[1] += a.y; y[2] += a.z; y[3] += a.w;
-                y[4] += b.x; y[5] += b.y; y[6] += b.z; y[7] += b.w;
+            const float* p = static_cast<const float*>(e.residual) + row * e.ldr + col;
+#pragma unroll
+            for (int r = 0; r < kRows; ++r, p += 8 * e.ldr)
+                if (row + 8 * r < rows && in_bounds<kChkResidual>(p, 32)) {
+                    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+                    y[r][0] += a.x; y[r][1] += a.y; y[r][2] += a.z; y[r][3] += a.w;
+                    y[r][4] += b.x; y[r][5] += b.y; y[r][6] += b.z; y[r][7] += b.w;
+                }
+        }
+        float* p = static_cast<float*>(out) + row * e.ldo + col;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r, p += 8 * e.ldo)
+            if (row + 8 * r < rows && in_bounds_role(e.role, p, 32)) {
+                *reinterpret_cast<float4*>(p) = make_float4(y[r][0], y[r][1], y[r][2], y[r][3]);
+                *reinterpret_cast<float4*>(p + 4) = make_float4(y[r][4], y[r][5], y[r][6], y[r][7]);
             }
-        }
-        float* p = static_cast<float*>(e.out) + row * e.ldo + col;
-        if (in_bounds_role(e.role, p, 32)) {
-            *reinterpret_cast<float4*>(p) = make_float4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<float4*>(p + 4) = make_float4(y[4], y[5], y[6], y[7]);
-        }
-    } else {
-        if (e.residual != nullptr) {
-            const T* r = static_cast<const T*>(e.residual) + row * e.ldr + col;
-            if (in_bounds<kChkResidual>(r, 16)) {
-                const uint4 q = *reinterpret_cast<const uint4*>(r);
-                const float2 a = unpack2<T>(q.x), b = unpack2<T>(q.y), c = unpack2<T>(q.z), d = unpack2<T>(q.w);
-                y[0] += a.x; y[1] += a.y; y[2] += b.x; y[3] += b.y;
-                y[4] += c.x; y[5] += c.y; y[6] += d.x; y[7] += d.y;
-            }
-        }
-        T* p = static_cast<T*>(e.out) + row * e.ldo + col;
-        if (in_bounds_role(e.role, p, 16))
-            *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3]), pack2<T>(y[4], y[5]), pack2<T>(y[6], y[7]));
+        return;
     }
+    if (e.residual != nullptr) {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const float2 a = unpack2<T>(q[r].x), b = unpack2<T>(q[r].y), c = unpack2<T>(q[r].z), d = unpack2<T>(q[r].w);
+            y[r][0] += a.x; y[r][1] += a.y; y[r][2] += b.x; y[r][3] += b.y;
+            y[r][4] += c.x; y[r][5] += c.y; y[r][6] += d.x; y[r][7] += d.y;
+        }
+    }
+    T* p = static_cast<T*>(out) + row * e.ldo + col;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r, p += 8 * e.ldo)
+        if (row + 8 * r < rows && in_bounds_role(e.role, p, 16)) *reinterpret_cast<uint4*>(p) = pack8<T>(y[r]);
+}
+
+// The 16-bit residuals of kRows rows of eight neighbouring values.
+template <typename T, int kRows>
+__device__ __forceinline__ void load_residuals(const Epilogue& e, int64_t row, int64_t rows, int64_t col, uint4 (&q)[kRows]) {
+    const T* p = static_cast<const T*>(e.residual) + row * e.ldr + col;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r, p += 8 * e.ldr)
+        q[r] = row + 8 * r < rows && in_bounds<kChkResidual>(p, 16) ? *reinterpret_cast<const uint4*>(p) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+// Eight rows of a column, bias already added.
+template <typename T>
+__device__ __forceinline__ void emit_column8(const Epilogue& e, void* out, int64_t row, int rows, int64_t col, float (&y)[8]) {
+    float res[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) res[p] = p < rows ? residual1<T>(e, row + p, col) : 0.f;
+    if (e.z != nullptr)
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+            if (p < rows) store_z1<T>(e, row + p, col, y[p]);
+    activate(y, e.act);
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+        if (p < rows) store_y1<T>(e, out, row + p, col, y[p] + res[p]);
 }
 
 // ---------------------------------------------------------------------------------------
-// The product D[m][n] = sum_k A(m, k) B(n, k) on the tensor cores: tcgen05.mma of 128 x bn x 16
-// with the accumulator in tensor memory.
+// The product D[m][n] = sum_k A(m, k) B(n, k) on the tensor cores: tcgen05.mma of 128 x bn x 16,
+// or of 256 x bn x 16 by a pair of SMs, with the accumulator in tensor memory.
 //
 // An operand is a row-major array with k along its rows ("k-major": x and W of the forward
 // product) or along its columns ("mn-major": W in dx = dz W, dz and x in dW = dz^T x); the
-// tensor cores take both, so nothing is transposed in memory. It is staged 64 values of k at a
-// time in the 128-byte-swizzled layout: rows of 64 contiguous elements (128 bytes), eight to a
+// tensor cores take both, so nothing is transposed in memory. TMA stages it 64 values of k at
+// a time in the 128-byte-swizzled layout: rows of 64 contiguous elements (128 bytes), eight to a
 // 1024-byte group, 16-byte chunk c of row r at chunk c ^ (r % 8). K-major: a row of it is an m (or
-// n) and holds 64 k. Mn-major: a row is a k and holds 64 m, one such box per 64 m.
+// n) and holds 64 k. Mn-major: a row is a k and holds 64 m, one such box per 64 m. Rows of A that the
+// product does not have are not staged; the MMA then multiplies what lies there, and those
+// rows of the accumulator are not read. Where one column tile covers all of N and B is small, B is
+// staged once and stays.
 //
 // Warps: 0-7 read finished accumulators (two for each quarter of the 128 TMEM lanes, taking
-// turns at 32-column chunks), 8 issues the MMAs, 9 issues the TMA copies. Arrays whose rows do
-// not start on 16-byte boundaries cannot be copied by TMA: eight more warps load those with
-// plain loads and write the same layout. Two accumulators alternate, so that the next tile's
-// MMAs run while the last one is written out. Persistent over tiles, n fastest.
+// turns at 32-column chunks), 8 issues the MMAs, 9 the TMA copies. Two accumulators alternate,
+// so that the next tile's MMAs run while the last one is written out. Persistent over tiles, n
+// fastest.
+//
+// A pair (kPair) computes 256 x bn: each block stages its own 128 rows of A and half of B, which
+// halves the shared-memory reads of B per MMA and leaves room for more stages; the first block
+// issues the MMAs of both, and each writes out its own 128 rows.
 //
 // Way out: a 32 x 32 chunk goes from TMEM (a lane holds a row) through 4 KB of shared memory a
 // warp, so that four neighbouring lanes then hold 32 neighbouring columns of a row: bias,
@@ -179,21 +328,15 @@ __device__ __forceinline__ void emit8(const Epilogue& e, int64_t row, int64_t co
 // fp32 until it is stored.
 // ---------------------------------------------------------------------------------------
 constexpr int kBm = 128, kBk = 64;
-constexpr int kOutWarps = 8, kLoadWarps = 8;
-constexpr int kThreads = 32 * (kOutWarps + 2);          // without the loading warps
-constexpr int kThreadsDirect = kThreads + 32 * kLoadWarps;
-constexpr int kMaxStages = 8;
-constexpr int kStageA = kBm * kBk * 2;
+constexpr int kOutWarps = 8;
+constexpr int kThreads = 32 * (kOutWarps + 2);
+constexpr int kMaxStages = 16;
 constexpr int kStaging = kOutWarps * 32 * 32 * 4;
 
-struct Side {             // one operand
-    const void* p;
-    int64_t ld;           // elements between its rows
-    uint64_t bytes;       // extent
-    int64_t outer, inner; // rows and columns of the array
-    int mn, direct;       // k runs along its columns; not copied by TMA
-    int box_rows, boxes;  // boxes of box_rows x 64 elements that make up a stage of it
-    int role;             // CheckRole
+struct Side {             // one operand's share of a stage: `boxes` boxes of box_rows x 64 elements
+    int mn;               // k runs along the array's columns
+    int box_rows, boxes;
+    int bytes;            // of all boxes, what TMA delivers (a multiple of 1024)
 };
 
 struct Gemm {
@@ -202,6 +345,8 @@ struct Gemm {
     int64_t M, N;
     int bn, columns;      // tile width; columns from one accumulator to the next
     int stages, stage_bytes;
+    int resident;         // B is staged once, behind the stages
+    int cluster;          // blocks that share a tile's K (their shares meet in shared memory), or 1
     int kblocks, kblocks_per_split;
     int mt, nt;
     uint32_t idesc, tmem_columns;
@@ -210,8 +355,8 @@ struct Gemm {
     int* status;
 };
 
-__host__ __device__ constexpr size_t gemm_smem(int stages, int stage_bytes) {
-    return 1024 + (size_t)stages * stage_bytes + kStaging + (2 * kMaxStages + 4 + 1) * 8 + 16;
+__host__ __device__ constexpr size_t gemm_smem(int stage_bytes_in_all) {
+    return 1024 + (size_t)stage_bytes_in_all + kStaging + (2 * kMaxStages + 6) * 8 + 16;
 }
 
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
@@ -220,9 +365,32 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
         "l"(map), "r"(bar), "r"(x), "r"(y)
         : "memory");
 }
+// Into this block's memory, with the arrival counted by a barrier of the pair's first block.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc));
+}
+// Arrives at the barrier of the same address in both blocks once the MMAs so far are done.
+__device__ __forceinline__ void commit_pair(uint32_t mbar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(mbar),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
 
 __device__ __forceinline__ void arrive_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}\n" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // Shared-memory descriptor of a 128-byte-swizzled operand: version 1 (bits 46-47), swizzle code
@@ -275,117 +443,125 @@ struct Ring {
     }
 };
 
-// 16 bytes of a row from a source of any 2-byte alignment: the two aligned 16-byte units that hold
-// them, shifted together. Where those would pass the array's end, or for fewer than 8
-// elements, one element at a time.
-__device__ __forceinline__ uint4 load_chunk(const Side& s, int64_t row, int64_t col) {
-    uint4 out = make_uint4(0u, 0u, 0u, 0u);
-    if (row >= s.outer || col >= s.inner) return out;
-    const char* base = static_cast<const char*>(s.p);
-    const uint64_t off = (uint64_t)(row * s.ld + col) * 2, lo = off & ~15ull;
-    if (col + 8 <= s.inner && lo + 32 <= s.bytes) {
-        if (!in_bounds_role(s.role, base + lo, 32)) return out;
-        const uint4 p = __ldg(reinterpret_cast<const uint4*>(base + lo));
-        const uint32_t sh = (uint32_t)(off & 15u);
-        if (sh == 0) return p;
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(base + lo + 16));
-        uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
-        if (sh & 8u) {
-#pragma unroll
-            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+// The tiles of a block (or pair), n fastest, without a division a tile.
+struct Tiles {
+    int m, n, dm, dn, mt, nt;
+    __device__ __forceinline__ Tiles(const Gemm& g, int first, int step)
+        : m(first / g.nt), n(first % g.nt), dm(step / g.nt), dn(step % g.nt), mt(g.mt), nt(g.nt) {}
+    __device__ __forceinline__ bool more() const { return m < mt; }
+    __device__ __forceinline__ void next() {
+        m += dm;
+        n += dn;
+        if (n >= nt) {
+            n -= nt;
+            ++m;
         }
-        if (sh & 4u) {
-#pragma unroll
-            for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-        }
-        const uint32_t bits = (sh & 2u) * 8u;
-        return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
-                          __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
     }
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (col + j < s.inner && in_bounds_role(s.role, base + off + 2 * j, 2))
-            w[j >> 1] |= (uint32_t)*reinterpret_cast<const uint16_t*>(base + off + 2 * j) << (16 * (j & 1));
-    return make_uint4(w[0], w[1], w[2], w[3]);
+};
+
+__device__ __forceinline__ uint32_t cluster_address(uint32_t saddr, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float4 cluster_load(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// One stage of an operand by plain loads: i0 its first m (or n), k0 its first k.
-__device__ __forceinline__ void load_direct(const Side& s, uint8_t* dst, int64_t i0, int64_t k0, int t) {
-    const int chunks = s.box_rows * 8, total = chunks * s.boxes;
-    const int64_t row0 = s.mn ? k0 : i0, col0 = s.mn ? i0 : k0;
-#pragma unroll 4
-    for (int i = t; i < total; i += 32 * kLoadWarps) {
-        const int box = i / chunks, r = (i - box * chunks) >> 3, c = i & 7;
-        const uint4 v = load_chunk(s, row0 + r, col0 + box * 64 + c * 8);
-        *reinterpret_cast<uint4*>(dst + box * s.box_rows * 128 + r * 128 + ((c ^ (r & 7)) << 4)) = v;
-    }
-}
-
-template <typename T, bool kDirect>
-__global__ void __launch_bounds__(kDirect ? kThreadsDirect : kThreads, kDirect ? 1 : 2) gemm_kernel(const __grid_constant__ Gemm g) {
+template <typename T, bool kPair, bool kVectors>
+__global__ void __launch_bounds__(kThreads, kPair ? 1 : 2) gemm_kernel(const __grid_constant__ Gemm g) {
     extern __shared__ uint8_t raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-    uint8_t* staging = sm + (size_t)g.stages * g.stage_bytes;
+    const int kept = g.resident ? g.kblocks * g.b.bytes : 0;
+    uint8_t* staging = sm + (size_t)g.stages * g.stage_bytes + kept;
     uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kStaging);
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 5);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 6);
     __shared__ volatile int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sm0 = (uint32_t)__cvta_generic_to_shared(sm), bar0 = (uint32_t)__cvta_generic_to_shared(bars);
-    // barriers: full[stage], empty[stage], accumulator done[2], accumulator free[2], drain
-    const uint32_t full = bar0, empty = bar0 + 8 * kMaxStages, done = empty + 8 * kMaxStages, room = done + 16, drain = room + 16;
-    const bool tma_a = !kDirect || !g.a.direct, tma_b = !kDirect || !g.b.direct;
-    if (threadIdx.x == 0) {
+    const uint32_t sb0 = sm0 + g.stages * g.stage_bytes;  // B, where it stays
+    // barriers: full[stage], empty[stage], accumulator done[2], accumulator free[2], B staged, drain
+    const uint32_t full = bar0, empty = bar0 + 8 * kMaxStages, done = empty + 8 * kMaxStages, room = done + 16, bfull = room + 16,
+                   drain = bfull + 8;
+    const uint32_t rank = kPair ? blockIdx.x & 1u : 0u;
+    if (threadIdx.x == 32 * (kOutWarps + 1)) {
         abort_flag = 0;
         for (int s = 0; s < g.stages; ++s) {
-            mlp::mbar_init(full + 8 * s, (tma_a || tma_b ? 1 : 0) + (tma_a && tma_b ? 0 : kLoadWarps));
+            mlp::mbar_init(full + 8 * s, 1);
             mlp::mbar_init(empty + 8 * s, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mlp::mbar_init(done + 8 * i, 1);
-            mlp::mbar_init(room + 8 * i, kOutWarps);
+            mlp::mbar_init(room + 8 * i, kPair ? 2 * kOutWarps : kOutWarps);
         }
+        mlp::mbar_init(bfull, 1);
         mlp::mbar_init(drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"((uint32_t)__cvta_generic_to_shared(tslot)),
-                     "r"(g.tmem_columns)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        const uint32_t slot = (uint32_t)__cvta_generic_to_shared(tslot);
+        if (kPair) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(g.tmem_columns) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(g.tmem_columns) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
     }
     mlp::fence_before();
     __syncthreads();
+    if (kPair) cluster_sync();  // the other block's barriers and tensor memory are there
     mlp::fence_after();
     const uint32_t tmem = *tslot;
-    const int tiles = g.mt * g.nt, kb0 = blockIdx.y * g.kblocks_per_split;
-    const int kbs = max(0, min(g.kblocks_per_split, g.kblocks - kb0));
+    const int first = kPair ? blockIdx.x >> 1 : blockIdx.x, step = kPair ? gridDim.x >> 1 : gridDim.x;
+    const int kb0 = blockIdx.y * g.kblocks_per_split, kbs = max(0, min(g.kblocks_per_split, g.kblocks - kb0));
 
     if (warp == kOutWarps + 1) {
         // ------------------------------- TMA copies -------------------------------
-        if (lane == 0 && (tma_a || tma_b)) {
-            const uint32_t bytes = (tma_a ? g.a.box_rows * g.a.boxes * 128 : 0) + (tma_b ? g.b.box_rows * g.b.boxes * 128 : 0);
+        if (lane == 0) {
+            const uint32_t bytes = g.a.bytes + (g.resident ? 0 : g.b.bytes);
+            if (g.resident && kbs > 0) {
+                arrive_expect(bfull, kept);
+                for (int kb = 0; kb < g.kblocks; ++kb)
+                    for (int j = 0; j < g.b.boxes; ++j)
+                        tma_load(sb0 + kb * g.b.bytes + j * g.b.box_rows * 128, &g.tb, g.b.mn ? 64 * j : kb * kBk, g.b.mn ? kb * kBk : 0, bfull);
+            }
             Ring r;
             uint32_t issued = 0;  // copies so far, at most counted to the number of stages
             bool ok = true;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                const int m0 = t / g.nt * kBm, n0 = t % g.nt * g.bn;
+            for (Tiles t(g, first, step); t.more() && ok; t.next()) {
+                const int m0 = (kPair ? 2 * t.m + (int)rank : t.m) * kBm, n0 = t.n * g.bn + (kPair ? (int)rank * (g.bn / 2) : 0);
                 for (int kb = 0; kb < kbs; ++kb) {
                     if (!(ok = wait_bounded(empty + 8 * r.stage, r.phase ^ 1u, &abort_flag))) break;
-                    const uint32_t bar = full + 8 * r.stage, sa = sm0 + r.stage * g.stage_bytes, sb = sa + kStageA;
+                    const uint32_t bar = kPair ? cluster_address(full + 8 * r.stage, 0) : full + 8 * r.stage;
+                    const uint32_t sa = sm0 + r.stage * g.stage_bytes, sb = sa + g.a.bytes;
                     const int k0 = (kb0 + kb) * kBk;
-                    arrive_expect(bar, bytes);
-                    if (tma_a)
-                        for (int j = 0; j < g.a.boxes; ++j)
-                            tma_load(sa + j * g.a.box_rows * 128, &g.ta, g.a.mn ? m0 + 64 * j : k0, g.a.mn ? k0 : m0, bar);
-                    if (tma_b)
-                        for (int j = 0; j < g.b.boxes; ++j)
-                            tma_load(sb + j * g.b.box_rows * 128, &g.tb, g.b.mn ? n0 + 64 * j : k0, g.b.mn ? k0 : n0, bar);
+                    if (!kPair) arrive_expect(bar, bytes);
+                    else if (rank == 0) arrive_expect(full + 8 * r.stage, 2 * bytes);  // both blocks' copies
+                    for (int j = 0; j < g.a.boxes; ++j) {
+                        const uint32_t dst = sa + j * g.a.box_rows * 128;
+                        const int x = g.a.mn ? m0 + 64 * j : k0, y = g.a.mn ? k0 : m0;
+                        if (kPair) tma_load_pair(dst, &g.ta, x, y, bar);
+                        else tma_load(dst, &g.ta, x, y, bar);
+                    }
+                    if (!g.resident)
+                        for (int j = 0; j < g.b.boxes; ++j) {
+                            const uint32_t dst = sb + j * g.b.box_rows * 128;
+                            const int x = g.b.mn ? n0 + 64 * j : k0, y = g.b.mn ? k0 : n0;
+                            if (kPair) tma_load_pair(dst, &g.tb, x, y, bar);
+                            else tma_load(dst, &g.tb, x, y, bar);
+                        }
                     r.next(g.stages);
                     issued = min(issued + 1, (uint32_t)g.stages);
                 }
             }
             // given up: the copies in flight still write to this block's shared memory
+            if (!ok && g.resident && kbs > 0) mlp::wait_parity(bfull, 0);
             for (; !ok && issued > 0; --issued) {
                 if (r.stage == 0) {
                     r.stage = g.stages;
@@ -397,137 +573,269 @@ __global__ void __launch_bounds__(kDirect ? kThreadsDirect : kThreads, kDirect ?
         }
     } else if (warp == kOutWarps) {
         // ---------------------------------- MMAs ----------------------------------
-        if (lane == 0) {
+        if (lane == 0 && rank == 0) {
             Ring r;
             uint32_t i = 0;
-            bool ok = true;
+            bool ok = kbs == 0 || !g.resident || wait_bounded(bfull, 0, &abort_flag);
             const uint32_t step_a = g.a.mn ? 2048 : 32, step_b = g.b.mn ? 2048 : 32;
-            for (int t = blockIdx.x; t < tiles && ok && kbs > 0; t += gridDim.x, ++i) {
+            for (Tiles t(g, first, step); t.more() && ok && kbs > 0; t.next(), ++i) {
                 const uint32_t acc = tmem + (i & 1u) * g.columns;
                 if (!(ok = wait_bounded(room + 8 * (i & 1u), ((i >> 1) & 1u) ^ 1u, &abort_flag))) break;
                 mlp::fence_after();
                 for (int kb = 0; kb < kbs; ++kb) {
                     if (!(ok = wait_bounded(full + 8 * r.stage, r.phase, &abort_flag))) break;
                     mlp::fence_after();
-                    const uint32_t sa = sm0 + r.stage * g.stage_bytes, sb = sa + kStageA;
+                    const uint32_t sa = sm0 + r.stage * g.stage_bytes, sb = g.resident ? sb0 + kb * g.b.bytes : sa + g.a.bytes;
 #pragma unroll
-                    for (int k = 0; k < kBk / 16; ++k)
-                        mlp::mma(acc, swizzled_desc(sa + k * step_a, 64 * 128), swizzled_desc(sb + k * step_b, 64 * 128), g.idesc,
-                                 (kb | k) != 0 ? 1u : 0u);
-                    mlp::commit(empty + 8 * r.stage);
+                    for (int k = 0; k < kBk / 16; ++k) {
+                        const uint64_t da = swizzled_desc(sa + k * step_a, 64 * 128), db = swizzled_desc(sb + k * step_b, 64 * 128);
+                        if (kPair) mma_pair(acc, da, db, g.idesc, (kb | k) != 0 ? 1u : 0u);
+                        else mlp::mma(acc, da, db, g.idesc, (kb | k) != 0 ? 1u : 0u);
+                    }
+                    if (kPair) commit_pair(empty + 8 * r.stage);
+                    else mlp::commit(empty + 8 * r.stage);
                     r.next(g.stages);
                 }
-                if (ok) mlp::commit(done + 8 * (i & 1u));
+                if (ok && kPair) commit_pair(done + 8 * (i & 1u));
+                else if (ok) mlp::commit(done + 8 * (i & 1u));
             }
             if (!ok) {
-                mlp::commit(drain);
+                if (kPair) commit_pair(drain);
+                else mlp::commit(drain);
                 mlp::wait_parity(drain, 0);
-            }
-        }
-    } else if (kDirect && warp > kOutWarps + 1) {
-        // ------------------------------- plain loads -------------------------------
-        const int lt = threadIdx.x - kThreads;
-        Ring r;
-        bool ok = true;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const int64_t m0 = (int64_t)(t / g.nt) * kBm, n0 = (int64_t)(t % g.nt) * g.bn;
-            for (int kb = 0; kb < kbs; ++kb) {
-                ok = wait_bounded(empty + 8 * r.stage, r.phase ^ 1u, &abort_flag);
-                if (__any_sync(0xffffffffu, !ok)) {
-                    ok = false;
-                    break;
-                }
-                uint8_t* sa = sm + r.stage * g.stage_bytes;
-                const int64_t k0 = (int64_t)(kb0 + kb) * kBk;
-                if (g.a.direct) load_direct(g.a, sa, m0, k0, lt);
-                if (g.b.direct) load_direct(g.b, sa + kStageA, n0, k0, lt);
-                mlp::fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mlp::mbar_arrive(full + 8 * r.stage);
-                r.next(g.stages);
             }
         }
     } else {
         // -------------------------------- way out ---------------------------------
         const int quarter = warp & 3, chunks = (g.bn + 31) / 32;
         float4* st = reinterpret_cast<float4*>(staging + warp * 4096);
-        Epilogue e = g.e;
-        if (g.split_stride != 0) e.out = static_cast<float*>(e.out) + blockIdx.y * g.split_stride;
+        const Epilogue& e = g.e;
+        void* out = g.split_stride != 0 ? static_cast<float*>(e.out) + blockIdx.y * g.split_stride : e.out;
         uint32_t i = 0;
-        bool ok = true;
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++i) {
-            const int64_t m0 = (int64_t)(t / g.nt) * kBm + 32 * quarter, n0 = (int64_t)(t % g.nt) * g.bn;
+        for (Tiles t(g, first, step); t.more(); t.next(), ++i) {
+            const int64_t m0 = (int64_t)(kPair ? 2 * t.m + (int)rank : t.m) * kBm + 32 * quarter;
+            const int n0 = t.n * g.bn, cols = (int)min(g.N, (int64_t)n0 + g.bn);
             const int rows = (int)min((int64_t)32, g.M - m0);
-            const int64_t cols = min(g.N, n0 + g.bn);
-            if (kbs > 0) {
-                ok = wait_bounded(done + 8 * (i & 1u), (i >> 1) & 1u, &abort_flag);
-                if (__any_sync(0xffffffffu, !ok)) break;
-                mlp::fence_after();
-            }
-            for (int c = warp >> 2; c < chunks; c += 2) {
-                uint32_t v[32];
+            bool waited = kbs == 0;
+            for (int c = warp >> 2; c < chunks && rows > 0; c += 2) {
                 __syncwarp();
+                const int c0 = n0 + 32 * c, col = c0 + 8 * (lane & 3);
+                // bias and residual are on their way while the accumulator is waited for and read
+                const bool whole = kVectors && col < cols;  // cols is a multiple of 8 then
+                uint4 q[4] = {};
+                float b[8];
+                if (whole && g.cluster == 1) {
+                    bias8(e, col, b);
+                    if (e.residual != nullptr && !e.out_f32) load_residuals<T, 4>(e, m0 + (lane >> 2), g.M, col, q);
+                }
+                __syncwarp();
+                if (!waited) {
+                    const bool ok = wait_bounded(done + 8 * (i & 1u), (i >> 1) & 1u, &abort_flag);
+                    if (__any_sync(0xffffffffu, !ok)) goto out_of_time;
+                    mlp::fence_after();
+                    waited = true;
+                }
+                uint32_t v[32];
                 if (kbs > 0) {
                     tmem_ld32(tmem + ((uint32_t)(32 * quarter) << 16) + (i & 1u) * g.columns + 32 * c, v);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = 0u;
                 }
+                // a split product leaves its share in the stages' memory, where the cluster's other blocks read it
+                if (g.cluster > 1) st = reinterpret_cast<float4*>(sm + (quarter * chunks + c) * 4096);
                 __syncwarp();
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
-                    st[lane * 8 + (u ^ (lane & 7))] = make_float4(__uint_as_float(v[4 * u]), __uint_as_float(v[4 * u + 1]),
-                                                                  __uint_as_float(v[4 * u + 2]), __uint_as_float(v[4 * u + 3]));
+                    st[unit_of(lane, u)] = make_float4(__uint_as_float(v[4 * u]), __uint_as_float(v[4 * u + 1]),
+                                                       __uint_as_float(v[4 * u + 2]), __uint_as_float(v[4 * u + 3]));
+                if (g.cluster > 1) continue;
                 __syncwarp();
-                const int64_t c0 = n0 + 32 * c;
-                if (e.vectors) {
-                    const int64_t col = c0 + 8 * (lane & 3);
-                    if (col + 8 <= cols) {
-                        float b[8] = {};
-                        if (e.bias != nullptr && in_bounds<kChkBias>(e.bias + col, 32)) {
-                            const float4 lo = __ldg(reinterpret_cast<const float4*>(e.bias + col)),
-                                         hi = __ldg(reinterpret_cast<const float4*>(e.bias + col + 4));
-                            b[0] = lo.x; b[1] = lo.y; b[2] = lo.z; b[3] = lo.w;
-                            b[4] = hi.x; b[5] = hi.y; b[6] = hi.z; b[7] = hi.w;
-                        }
+                if (whole) {
+                    float y[4][8];
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) {
-                            const int r = 8 * p + (lane >> 2);
-                            if (r >= rows) break;
-                            const float4 lo = st[r * 8 + ((2 * (lane & 3)) ^ (r & 7))], hi = st[r * 8 + ((2 * (lane & 3) + 1) ^ (r & 7))];
-                            float y[8] = {lo.x + b[0], lo.y + b[1], lo.z + b[2], lo.w + b[3],
-                                          hi.x + b[4], hi.y + b[5], hi.z + b[6], hi.w + b[7]};
-                            emit8<T>(e, m0 + r, col, y);
-                        }
-                    } else {
-                        const float* sf = reinterpret_cast<const float*>(st);
-                        for (int p = 0; p < 4; ++p) {
-                            const int r = 8 * p + (lane >> 2);
-                            if (r >= rows) break;
-                            for (int j = 0; j < 8; ++j)
-                                if (col + j < cols)
-                                    emit<T>(e, m0 + r, col + j, sf[r * 32 + (((2 * (lane & 3) + (j >> 2)) ^ (r & 7)) << 2) + (j & 3)]);
-                        }
+                    for (int p = 0; p < 4; ++p) {
+                        const int r = 8 * p + (lane >> 2);
+                        const float4 lo = st[unit_of(r, 2 * (lane & 3))], hi = st[unit_of(r, 2 * (lane & 3) + 1)];
+                        y[p][0] = lo.x + b[0]; y[p][1] = lo.y + b[1]; y[p][2] = lo.z + b[2]; y[p][3] = lo.w + b[3];
+                        y[p][4] = hi.x + b[4]; y[p][5] = hi.y + b[5]; y[p][6] = hi.z + b[6]; y[p][7] = hi.w + b[7];
                     }
-                } else if (c0 + lane < cols) {
+                    emit_vectors<T, 4>(e, out, m0 + (lane >> 2), g.M, col, y, q);
+                } else if (!kVectors && c0 + lane < cols) {
+                    // a lane holds a column, so that a warp writes 32 neighbours whatever their alignment
                     const float* sf = reinterpret_cast<const float*>(st);
-                    for (int r = 0; r < rows; ++r) emit<T>(e, m0 + r, c0 + lane, sf[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)]);
+                    const float bias = bias1(e, c0 + lane);
+#pragma unroll 1
+                    for (int r0 = 0; r0 < rows; r0 += 8) {
+                        float y[8];
+#pragma unroll
+                        for (int p = 0; p < 8; ++p) y[p] = sf[unit_of(r0 + p, lane >> 2) * 4 + (lane & 3)] + bias;
+                        emit_column8<T>(e, out, m0 + r0, rows - r0, c0 + lane, y);
+                    }
                 }
             }
             if (kbs > 0) {
+                if (!waited) {  // a warp without a chunk of this tile keeps in step all the same
+                    const bool ok = wait_bounded(done + 8 * (i & 1u), (i >> 1) & 1u, &abort_flag);
+                    if (__any_sync(0xffffffffu, !ok)) goto out_of_time;
+                }
                 mlp::fence_before();
                 __syncwarp();
-                if (lane == 0) mlp::mbar_arrive(room + 8 * (i & 1u));
+                if (lane == 0) {
+                    if (kPair) arrive_cluster(cluster_address(room + 8 * (i & 1u), 0));
+                    else mlp::mbar_arrive(room + 8 * (i & 1u));
+                }
             }
         }
+    out_of_time:;
     }
     __syncwarp();
+    if (!kPair && g.cluster > 1) {
+        // K is split over the cluster's blocks: their shares of the tile are added in rank order, every block
+        // writing out the rows of its turn.
+        cluster_sync();
+        const int chunks = (g.bn + 31) / 32, quarters = (int)min((int64_t)4, (g.M - (int64_t)(blockIdx.x / g.nt) * kBm + 31) / 32);
+        const int64_t tm = (int64_t)(blockIdx.x / g.nt) * kBm;
+        const int tn = (int)(blockIdx.x % g.nt) * g.bn, cols = (int)min(g.N, (int64_t)tn + g.bn);
+        if (warp < kOutWarps && abort_flag == 0)
+            for (int u = warp * g.cluster + blockIdx.y; u < quarters * chunks * 4; u += kOutWarps * g.cluster) {
+                const int chunk = u >> 2, r = 8 * (u & 3) + (lane >> 2);  // chunk = quarter * chunks + column chunk
+                const int64_t row = tm + 32 * (chunk / chunks) + r;
+                const int col = tn + 32 * (chunk % chunks) + 8 * (lane & 3);
+                if (row >= g.M || col >= cols) continue;
+                const uint32_t lo = sm0 + chunk * 4096 + unit_of(r, 2 * (lane & 3)) * 16, hi = sm0 + chunk * 4096 + unit_of(r, 2 * (lane & 3) + 1) * 16;
+                float y[1][8] = {};
+#pragma unroll 4
+                for (int k = 0; k < g.cluster; ++k) {
+                    const float4 a = cluster_load(cluster_address(lo, k)), b = cluster_load(cluster_address(hi, k));
+                    y[0][0] += a.x; y[0][1] += a.y; y[0][2] += a.z; y[0][3] += a.w;
+                    y[0][4] += b.x; y[0][5] += b.y; y[0][6] += b.z; y[0][7] += b.w;
+                }
+                if (kVectors) {
+                    float b[8];
+                    uint4 q[1] = {};
+                    if (g.e.residual != nullptr && !g.e.out_f32) load_residuals<T, 1>(g.e, row, row + 1, col, q);
+                    bias8(g.e, col, b);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[0][j] += b[j];
+                    emit_vectors<T, 1>(g.e, g.e.out, row, row + 1, col, y, q);
+                } else {
+                    float res[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        res[j] = col + j < cols ? residual1<T>(g.e, row, col + j) : 0.f;
+                        if (col + j < cols) y[0][j] += bias1(g.e, col + j);
+                    }
+                    if (g.e.z != nullptr)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (col + j < cols) store_z1<T>(g.e, row, col + j, y[0][j]);
+                    activate(y[0], g.e.act);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (col + j < cols) store_y1<T>(g.e, g.e.out, row, col + j, y[0][j] + res[j]);
+                }
+            }
+        __syncwarp();
+        cluster_sync();  // nobody leaves while its shares are read
+    }
     mlp::fence_before();
     __syncthreads();
+    if (kPair) cluster_sync();  // nor while the pair's MMAs read its memory
     mlp::fence_after();
     if (threadIdx.x == 0 && abort_flag != 0 && g.status != nullptr) atomicExch(g.status, 1);
-    if (warp == 0)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(g.tmem_columns) : "memory");
+    if (warp == 0) {
+        if (kPair) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(g.tmem_columns) : "memory");
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(g.tmem_columns) : "memory");
+    }
+}
+
+// Copies of arrays whose rows do not begin on 16-byte boundaries into rows that do (TMA copies no
+// others): 16 bytes out a thread at a time, from the two aligned 16-byte units that hold them,
+// shifted together; four such at once keep loads in flight.
+struct Realign {
+    const void* p;
+    uint16_t* to;
+    uint64_t bytes;        // extent of the source
+    int64_t outer, ld, chunks;  // chunks of 8 elements of a row, rounded up
+    int inner, role;
+};
+struct RealignList {
+    Realign a[2];
+    int64_t first;  // chunks of a[0]
+    int64_t total;
+};
+
+// Eight elements of a row (zeros beyond its end).
+struct Chunk {
+    uint4 p, q;
+    uint32_t shift;  // bytes
+    int n;           // elements that are there
+};
+
+__device__ __forceinline__ void begin_chunk(const Realign& s, int64_t row, int col, Chunk& c) {
+    c.p = c.q = make_uint4(0u, 0u, 0u, 0u);
+    c.shift = 0;
+    c.n = min(8, s.inner - col);
+    const char* base = static_cast<const char*>(s.p);
+    const uint64_t off = (uint64_t)(row * s.ld + col) * 2, lo = off & ~15ull;
+    const uint32_t sh = (uint32_t)(off & 15u);
+    const bool two = sh + 2 * c.n > 16;
+    if (lo + (two ? 32 : 16) <= s.bytes) {
+        c.shift = sh;
+        if (in_bounds_role(s.role, base + lo, 16)) c.p = __ldg(reinterpret_cast<const uint4*>(base + lo));
+        if (two && in_bounds_role(s.role, base + lo + 16, 16)) c.q = __ldg(reinterpret_cast<const uint4*>(base + lo + 16));
+        return;
+    }
+    // the array's last bytes: one element at a time
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j < c.n && in_bounds_role(s.role, base + off + 2 * j, 2))
+            w[j >> 1] |= (uint32_t)*reinterpret_cast<const uint16_t*>(base + off + 2 * j) << (16 * (j & 1));
+    c.p = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ uint4 finish_chunk(const Chunk& c) {
+    uint32_t w[8] = {c.p.x, c.p.y, c.p.z, c.p.w, c.q.x, c.q.y, c.q.z, c.q.w};
+    if (c.shift & 8u) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (c.shift & 4u) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    const uint32_t bits = (c.shift & 2u) * 8u;
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = __funnelshift_r(w[i], w[i + 1], bits);
+        if (2 * i + 1 >= c.n) v[i] = 2 * i < c.n ? v[i] & 0xffffu : 0u;
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+__global__ void __launch_bounds__(256) realign_kernel(const __grid_constant__ RealignList l) {
+    constexpr int kAtOnce = 4;
+    const int64_t i0 = (int64_t)blockIdx.x * (256 * kAtOnce) + threadIdx.x;
+    Chunk c[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+        const int64_t i = i0 + 256 * u;
+        if (i >= l.total) continue;
+        const Realign& s = l.a[i >= l.first];
+        const int64_t j = i >= l.first ? i - l.first : i, row = j / s.chunks;
+        begin_chunk(s, row, (int)(j - row * s.chunks) * 8, c[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+        const int64_t i = i0 + 256 * u;
+        if (i >= l.total) continue;
+        const Realign& s = l.a[i >= l.first];
+        uint16_t* to = s.to + 8 * (i >= l.first ? i - l.first : i);
+        if (in_bounds<kChkWork>(to, 16)) *reinterpret_cast<uint4*>(to) = finish_chunk(c[u]);
+    }
 }
 
 // dz = dy act'(z), rounded to T, into dz (NULL: not wanted), and the sums of the unrounded dz
@@ -544,7 +852,11 @@ __global__ void __launch_bounds__(256) slope_kernel(const T* __restrict__ dy, in
     if (col < cols)
         for (int64_t r = r0 + warp; r < r1; r += 8) {
             float d = in_bounds<kChkDout>(dy + r * lddy + col, 2) ? to_float(dy[r * lddy + col]) : 0.f;
-            if (act != kNoAct && in_bounds<kChkZ>(z + r * cols + col, 2)) d *= slope(to_float(z[r * cols + col]), act);
+            if (act != kNoAct && in_bounds<kChkZ>(z + r * cols + col, 2)) {
+                float d2[2] = {d, 0.f}, z2[2] = {to_float(z[r * cols + col]), 0.f};
+                times_slope(d2, z2, act);
+                d = d2[0];
+            }
             if (dz != nullptr && in_bounds<kChkWork>(dz + r * lddz + col, 2)) dz[r * lddz + col] = from_float<T>(d);
             s += d;
         }

@@ -78,9 +78,12 @@ def check_forward(N, K, M, dtype, act, bias=True, residual=True, keep=True, y32=
     z = zbuf[:N * M].view(N, M) if keep else None
     layer = hg.Linear(K, M, dtype, act)
     status = torch.zeros(4, dtype=torch.int32, device="cuda")
-    layer.forward(x, w, b, residual=r, y=ybuf[:, :M], z=z, device_status=status)
+    need = hg.hashgrid_linear_forward_workspace(layer.handle, N, K + pad if N > 1 else K)
+    work = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")   # NaN, whatever is read from it
+    layer.forward(x, w, b, residual=r, y=ybuf[:, :M], z=z, workspace=work[:max(16, need)], device_status=status)
     torch.cuda.synchronize()
     assert int(status[0]) == 0
+    assert bool((work[need:] == 0xFF).all())
     assert bool((ybuf[:, M:] == 7.0).all()) and bool((zbuf[N * M:] == 7.0).all())
     X, W = x.double(), w.double()
     z64 = X @ W.t() + (b.double() if bias else 0)
@@ -108,7 +111,7 @@ def check_backward(N, K, M, dtype, act, dx32=False, dw32=True, pad=0, seed=0, wa
     db = torch.full((M,), 7.0, device="cuda")
     layer = hg.Linear(K, M, dtype, act)
     status = torch.zeros(4, dtype=torch.int32, device="cuda")
-    need = hg.hashgrid_linear_workspace(layer.handle, N)
+    need = hg.hashgrid_linear_backward_workspace(layer.handle, N, M + pad if N > 1 else M, K + pad if N > 1 else K)
     work = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")   # NaN, whatever is read from it
     layer.backward(dy, x, w, z=None if act == hg.HASHGRID_ACT_NONE else z, dL_dx=dxbuf[:, :K] if want[0] else None,
                    dL_dw=dw if want[1] else None, dL_db=db if want[2] else None, workspace=work[:max(16, need)],
@@ -366,9 +369,9 @@ def test_refusals():
     h, p = layer.handle, 0x1000
 
     def forward(x=p, ldx=8, N=2, w=p, b=p, r=None, ldr=4, y=p, ldy=4, yt=1, z=None):
-        return lib.hashgrid_linear_forward(h, x, ldx, N, w, b, r, ldr, y, ldy, yt, z, None, None)
+        return lib.hashgrid_linear_forward(h, x, ldx, N, w, b, r, ldr, y, ldy, yt, z, None, 0, None, None)
     A, L = hg.HASHGRID_ERR_ARG, hg.HASHGRID_ERR_ALIGN
-    assert lib.hashgrid_linear_forward(None, p, 8, 2, p, p, None, 4, p, 4, 1, None, None, None) == A
+    assert lib.hashgrid_linear_forward(None, p, 8, 2, p, p, None, 4, p, 4, 1, None, None, 0, None, None) == A
     assert forward(N=0, x=None, w=None, y=None) == hg.HASHGRID_OK
     assert forward(N=-1) == A and forward(N=2 ** 31) == A
     assert forward(yt=2) == A and forward(yt=3) == A            # fp16 layer: y is fp16 or fp32
@@ -382,8 +385,12 @@ def test_refusals():
     assert backward(dx=None) == hg.HASHGRID_OK                   # nothing is asked for
     assert backward(N=-1) == A and backward(xt=2) == A and backward(wt=2) == A and backward(lddy=3) == A
     assert backward(dy=p + 4) == L and backward(dy=None) == A
-    assert hg.hashgrid_linear_workspace(None, 5) == 0 and hg.hashgrid_linear_workspace(h, -1) == 0
-    assert hg.hashgrid_linear_workspace(h, 100) > 0
+    size = hg.hashgrid_linear_backward_workspace
+    assert size(None, 5, 4, 8) == 0 and size(h, -1, 4, 8) == 0 and 0 < size(h, 100, 8, 8) < size(h, 100, 8, 9)
+    assert hg.hashgrid_linear_forward_workspace(h, 100, 8) == 0 < hg.hashgrid_linear_forward_workspace(h, 100, 9)
+    for f in (lambda n: size(h, n, 5, 9), lambda n: hg.hashgrid_linear_forward_workspace(h, n, 9)):
+        sizes = [f(n) for n in list(range(1, 200)) + [10 ** k for k in range(3, 9)] + [16383, 16384, 16385]]
+        assert [f(n) for n in range(1, 200)] == sorted(f(n) for n in range(1, 200)) and f(16384) <= f(16385) and min(sizes) >= 0
 
 
 def test_binding_refuses_wrong_tensors():
@@ -406,12 +413,14 @@ def test_gpu_refusals():
     big = torch.zeros(1 << 22, dtype=torch.uint8, device="cuda")
     p = big.data_ptr()
     lib, h = hg.lib, layer.handle
-    assert lib.hashgrid_linear_forward(h, p, 1 << 30, 100, p, None, None, 4, p, 4, 2, None, None, None) == hg.HASHGRID_ERR_ARG
+    assert lib.hashgrid_linear_forward(h, p, 1 << 30, 100, p, None, None, 4, p, 4, 2, None, None, 0, None, None) == hg.HASHGRID_ERR_ARG
     assert "allocation ends" in hg.hashgrid_last_error()
     args = [h, p, 4, p, 8, 100, p, None, p, 8, 0, None, 0, None, p, 1 << 20, None, None]
     assert lib.hashgrid_linear_backward(*args) == hg.HASHGRID_ERR_ARG and "z is NULL" in hg.hashgrid_last_error()
-    args[7], args[15] = p, hg.hashgrid_linear_workspace(h, 100) - 1
+    args[7], args[15] = p, hg.hashgrid_linear_backward_workspace(h, 100, 4, 8) - 1
     assert lib.hashgrid_linear_backward(*args) == hg.HASHGRID_ERR_ARG and "workspace" in hg.hashgrid_last_error()
+    args = [h, p, 9, 100, p, None, None, 4, p, 4, 2, None, None, 0, None, None]
+    assert lib.hashgrid_linear_forward(*args) == hg.HASHGRID_ERR_ARG and "workspace" in hg.hashgrid_last_error()
     with pytest.raises(hg.HashGridError):
         layer.forward(torch.zeros(5, 8, dtype=torch.bfloat16), torch.zeros(4, 8, dtype=torch.bfloat16, device="cuda"),
                       y=torch.zeros(5, 4, dtype=torch.bfloat16, device="cuda"))
