@@ -431,6 +431,12 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
     return false;
 }
 
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+    return p != 0;
+}
+
 // Position in a ring of stages.
 struct Ring {
     int stage = 0;
@@ -482,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, kPair ? 1 : 2) gemm_kernel(const __g
     uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kStaging);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 6);
     __shared__ volatile int abort_flag;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // the shuffle tells the compiler that it is uniform
     const uint32_t sm0 = (uint32_t)__cvta_generic_to_shared(sm), bar0 = (uint32_t)__cvta_generic_to_shared(bars);
     const uint32_t sb0 = sm0 + g.stages * g.stage_bytes;  // B, where it stays
     // barriers: full[stage], empty[stage], accumulator done[2], accumulator free[2], B staged, drain
@@ -573,11 +579,18 @@ __global__ void __launch_bounds__(kThreads, kPair ? 1 : 2) gemm_kernel(const __g
         }
     } else if (warp == kOutWarps) {
         // ---------------------------------- MMAs ----------------------------------
-        if (lane == 0 && rank == 0) {
+        // The whole warp walks through the loop and one lane issues: with everything uniform the descriptors stay
+        // in uniform registers, which the instruction wants (from a branch of lane 0 alone it took 385 instead of 332
+        // thousand cycles for 8192 x 4096 x 4096).
+        if (rank == 0) {
+            const bool issues = elect_one();
             Ring r;
             uint32_t i = 0;
             bool ok = kbs == 0 || !g.resident || wait_bounded(bfull, 0, &abort_flag);
-            const uint32_t step_a = g.a.mn ? 2048 : 32, step_b = g.b.mn ? 2048 : 32;
+            // Descriptors count addresses in units of 16 bytes: a stage and a step of 16 k are additions to them.
+            const uint32_t step_a = g.a.mn ? 128 : 2, step_b = g.b.mn ? 128 : 2, stage = g.stage_bytes >> 4;
+            const uint32_t next_b = g.resident ? g.b.bytes >> 4 : 0;
+            const uint64_t a0 = swizzled_desc(sm0, 64 * 128), b0 = swizzled_desc(g.resident ? sb0 : sm0 + g.a.bytes, 64 * 128);
             for (Tiles t(g, first, step); t.more() && ok && kbs > 0; t.next(), ++i) {
                 const uint32_t acc = tmem + (i & 1u) * g.columns;
                 if (!(ok = wait_bounded(room + 8 * (i & 1u), ((i >> 1) & 1u) ^ 1u, &abort_flag))) break;
@@ -585,21 +598,20 @@ __global__ void __launch_bounds__(kThreads, kPair ? 1 : 2) gemm_kernel(const __g
                 for (int kb = 0; kb < kbs; ++kb) {
                     if (!(ok = wait_bounded(full + 8 * r.stage, r.phase, &abort_flag))) break;
                     mlp::fence_after();
-                    const uint32_t sa = sm0 + r.stage * g.stage_bytes, sb = g.resident ? sb0 + kb * g.b.bytes : sa + g.a.bytes;
+                    const uint64_t da = a0 + (uint32_t)r.stage * stage, db = b0 + (g.resident ? (uint32_t)kb * next_b : (uint32_t)r.stage * stage);
 #pragma unroll
                     for (int k = 0; k < kBk / 16; ++k) {
-                        const uint64_t da = swizzled_desc(sa + k * step_a, 64 * 128), db = swizzled_desc(sb + k * step_b, 64 * 128);
-                        if (kPair) mma_pair(acc, da, db, g.idesc, (kb | k) != 0 ? 1u : 0u);
-                        else mlp::mma(acc, da, db, g.idesc, (kb | k) != 0 ? 1u : 0u);
+                        if (kPair && issues) mma_pair(acc, da + k * step_a, db + k * step_b, g.idesc, (kb | k) != 0 ? 1u : 0u);
+                        if (!kPair && issues) mlp::mma(acc, da + k * step_a, db + k * step_b, g.idesc, (kb | k) != 0 ? 1u : 0u);
                     }
-                    if (kPair) commit_pair(empty + 8 * r.stage);
-                    else mlp::commit(empty + 8 * r.stage);
+                    if (kPair && issues) commit_pair(empty + 8 * r.stage);
+                    if (!kPair && issues) mlp::commit(empty + 8 * r.stage);
                     r.next(g.stages);
                 }
-                if (ok && kPair) commit_pair(done + 8 * (i & 1u));
-                else if (ok) mlp::commit(done + 8 * (i & 1u));
+                if (kPair && ok && issues) commit_pair(done + 8 * (i & 1u));
+                if (!kPair && ok && issues) mlp::commit(done + 8 * (i & 1u));
             }
-            if (!ok) {
+            if (!ok && issues) {
                 if (kPair) commit_pair(drain);
                 else mlp::commit(drain);
                 mlp::wait_parity(drain, 0);
