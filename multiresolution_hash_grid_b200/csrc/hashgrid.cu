@@ -687,6 +687,20 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int sms) {
     return p;
 }
 
+// The map of an array that is copied in boxes of box_rows x 64 elements, 128-byte-swizzled.
+int set_map(CUtensorMap& map, const Array& a, int box_rows, const char* what) {
+    const cuuint64_t dims[2] = {(cuuint64_t)a.inner, (cuuint64_t)a.outer};
+    const cuuint64_t strides[1] = {(cuuint64_t)(a.outer > 1 ? a.ld : (a.inner + 7) / 8 * 8) * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, ones[2] = {1, 1};
+    PFN_tensorMapEncodeTiled encode = tensor_map_fn();
+    const CUresult r = encode == nullptr ? CUDA_ERROR_NOT_SUPPORTED
+                                         : encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(a.p), dims, strides, box, ones,
+                                                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(HASHGRID_ERR_CUDA, "%s: encoding a tensor map failed (%d)", what, (int)r);
+    return ok();
+}
+
 // One operand's share of a stage, and its tensor map. `wanted` rows (or columns) of it are staged at a
 // time; those that the array does not have are left out.
 int set_side(hg::linear::Side& s, CUtensorMap& map, const Array& a, int wanted, const char* what) {
@@ -700,16 +714,7 @@ int set_side(hg::linear::Side& s, CUtensorMap& map, const Array& a, int wanted, 
         s.boxes = 1;
     }
     s.bytes = s.box_rows * s.boxes * 128;
-    const cuuint64_t dims[2] = {(cuuint64_t)a.inner, (cuuint64_t)a.outer};
-    const cuuint64_t strides[1] = {(cuuint64_t)(a.outer > 1 ? a.ld : (a.inner + 7) / 8 * 8) * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)s.box_rows}, ones[2] = {1, 1};
-    PFN_tensorMapEncodeTiled encode = tensor_map_fn();
-    const CUresult r = encode == nullptr ? CUDA_ERROR_NOT_SUPPORTED
-                                         : encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(a.p), dims, strides, box, ones,
-                                                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return fail(HASHGRID_ERR_CUDA, "%s: encoding a tensor map failed (%d)", what, (int)r);
-    return ok();
+    return set_map(map, a, s.box_rows, what);
 }
 
 bool vector_rows(const void* p, int64_t ld, size_t elem) { return p == nullptr || ((size_t)ld * elem) % 16 == 0; }
@@ -815,7 +820,7 @@ int realign(Array* const* arrays, int count, char* work, const char* what, cudaS
 }
 
 // The backward pass's workspace: the copies of x and w (or dy) with aligned rows, dz (where it has to be
-// computed), the parts of db, the parts of dw.
+// computed), the parts of db, the parts of dw; or, for a narrow layer, the blocks' sums.
 struct LinearWork {
     int64_t lddz;   // elements
     int parts;      // row shares of the db sums
@@ -823,15 +828,25 @@ struct LinearWork {
     size_t copies, dy, dz, sums, dw, bytes;  // offsets, total
 };
 
+constexpr int kWorkSms = 148;  // the workspace's size may not depend on the device
+
+// Whether the one-pass kernel takes a layer: its tile of dy, z and x (x 2 stages) and W fit into shared
+// memory, and there are tiles enough for every SM.
+bool narrow_layer(const hashgrid_linear_s* l, int64_t N) {
+    if (l->in > 128 || l->out > 128 || l->in % 8 != 0 || l->out % 8 != 0 || N < 4 * kWorkSms * hg::linear::kBm) return false;
+    const int boxes_out = ceil_div(l->out, 64), boxes_in = ceil_div(l->in, 64);
+    const int stage = (boxes_out * (l->act == HASHGRID_ACT_NONE ? 1 : 2) + boxes_in) * hg::linear::kBox;
+    return hg::linear::narrow_smem(2 * stage, ceil_div(l->out, 16) * 16 * boxes_in * 128) <= 226 * 1024;
+}
+
 // dw sums over the rows: beyond what a cluster's 8 blocks can share, so many shares of them that
 // every SM has a tile of one.
 LinearWork linear_work(const hashgrid_linear_s* l, int64_t N, int64_t lddy, int64_t ldx) {
     LinearWork w;
-    constexpr int kSms = 148;  // the workspace's size may not depend on the device
     w.lddz = (l->out + 7) / 8 * 8;
     w.parts = (int)std::min<int64_t>(256, (N + 63) / 64);
     const int64_t tiles = (int64_t)ceil_div(l->out, hg::linear::kBm) * ceil_div(l->in, 256);
-    w.splits = N <= 16384 ? 1 : (int)std::max<int64_t>(1, kSms / tiles);
+    w.splits = N <= 16384 ? 1 : (int)std::max<int64_t>(1, kWorkSms / tiles);
     const bool plain = l->act == HASHGRID_ACT_NONE;
     w.copies = 0;
     w.dy = (l->in % 8 != 0 ? realigned_bytes(l->out, l->in) : 0) + (ldx % 8 != 0 ? realigned_bytes(N, l->in) : 0);
@@ -839,7 +854,72 @@ LinearWork linear_work(const hashgrid_linear_s* l, int64_t N, int64_t lddy, int6
     w.sums = w.dz + (plain ? 0 : align256((size_t)N * w.lddz * 2));
     w.dw = w.sums + align256((size_t)w.parts * l->out * sizeof(float));
     w.bytes = w.dw + (w.splits > 1 ? align256((size_t)w.splits * l->in * l->out * sizeof(float)) : 0);
+    if (narrow_layer(l, N)) w.bytes = std::max(w.bytes, align256((size_t)kWorkSms * (l->in + 1) * l->out * sizeof(float)));
     return w;
+}
+
+// The sums of up to two arrays' parts.
+template <typename T>
+int launch_sums(const hg::linear::Sums* list, int count, const char* what, cudaStream_t s) {
+    hg::linear::SumsList l;
+    std::memset(&l, 0, sizeof l);
+    int64_t blocks = 0;
+    for (int i = 0; i < count; ++i) {
+        l.a[i] = list[i];
+        blocks += (list[i].n + 31) / 32;
+        if (i == 0) l.blocks0 = (int)blocks;
+    }
+    if (count == 0) return ok();
+    if (blocks > 0x7fffffffLL) return fail(HASHGRID_ERR_ARG, "%s: too many weights", what);
+    hg::linear::sum_parts_kernel<T><<<(unsigned)blocks, 256, 0, s>>>(l);
+    return launch_status(what);
+}
+
+template <typename T>
+int launch_narrow_backward(const hashgrid_linear_s* l, const Array& dy, const Array& x, int64_t N, const void* w, const void* z, void* dx,
+                           int64_t lddx, int dx_dtype, void* dw, int dw_dtype, float* db, char* work, int* status, const char* what,
+                           cudaStream_t s) {
+    namespace hl = hg::linear;
+    hl::Narrow g;
+    std::memset(&g, 0, sizeof g);
+    g.rows = N;
+    g.in = l->in;
+    g.out = l->out;
+    g.act = l->act;
+    g.boxes_in = ceil_div(l->in, 64);
+    g.boxes_out = ceil_div(l->out, 64);
+    g.columns = ceil_div(l->in, 32) * 32;
+    g.tmem_columns = 128;
+    while ((int)g.tmem_columns < 4 * g.columns) g.tmem_columns *= 2;
+    g.k_out = ceil_div(l->out, 16) * 16;
+    if (int rc = set_map(g.tdy, dy, hl::kBm, what)) return rc;
+    if (int rc = set_map(g.tx, x, hl::kBm, what)) return rc;
+    if (z != nullptr)
+        if (int rc = set_map(g.tz, {z, N, l->out, l->out, false, hg::kChkZ}, hl::kBm, what)) return rc;
+    if (int rc = set_map(g.tw, {dx != nullptr ? w : dy.p, l->out, l->in, l->in, true, hg::kChkWeights}, g.k_out, what)) return rc;
+    g.stage_bytes = (g.boxes_out * (l->act == HASHGRID_ACT_NONE ? 1 : 2) + g.boxes_in) * hl::kBox;
+    g.w_bytes = g.k_out * g.boxes_in * 128;
+    g.stages = hl::kNarrowStages;
+    while (g.stages > 2 && hl::narrow_smem(g.stages * g.stage_bytes, g.w_bytes) > 226 * 1024) --g.stages;
+    const uint32_t type = std::is_same<T, __half>::value ? 0u : 1u;
+    const uint32_t id = (1u << 4) | (type << 7) | (type << 10) | (1u << 16) | ((uint32_t)(ceil_div(l->in, 16) * 16 >> 3) << 17) |
+                        ((uint32_t)(hl::kBm >> 4) << 24);
+    g.id_dx = id;
+    g.id_dw = id | (1u << 15);
+    g.e = hl::Epilogue{nullptr, nullptr, dx, nullptr, 0, lddx, 0, dx_dtype == HASHGRID_F32, hl::kNoAct, hg::kChkOut};
+    g.parts = reinterpret_cast<float*>(work);
+    g.want_db = db != nullptr;
+    g.status = status;
+    const int blocks = std::min(kWorkSms, device_sms());
+    const size_t smem = hl::narrow_smem(g.stages * g.stage_bytes, g.w_bytes);
+    auto k = l->in <= 64 ? hl::narrow_backward_kernel<T, 1> : hl::narrow_backward_kernel<T, 2>;
+    if (int rc = prepare_smem(k, smem)) return rc;
+    k<<<(unsigned)std::min<int64_t>(blocks, ceil_div(N, hl::kBm)), hl::kNarrowThreads, smem, s>>>(g);
+    if (int rc = launch_status(what)) return rc;
+    const int64_t nw = (int64_t)l->in * l->out, stride = nw + l->out;
+    hl::Sums sums[2] = {{g.parts, stride, nw, blocks, dw_dtype == HASHGRID_F32 ? 0 : 1, dw, hg::kChkGrad},
+                        {g.parts + nw, stride, l->out, blocks, 0, db, hg::kChkBias}};
+    return launch_sums<T>(sums, db != nullptr ? 2 : 1, what, s);
 }
 
 size_t forward_work(const hashgrid_linear_s* l, int64_t N, int64_t ldx) {
@@ -861,56 +941,53 @@ int launch_linear_backward(const hashgrid_linear_s* l, const void* dy, int64_t l
                            int64_t N, const void* w, const void* z, void* dx, int64_t lddx, int dx_dtype, void* dw,
                            int dw_dtype, float* db, char* work, int* status, cudaStream_t s) {
     static const char* what = "linear_backward";
+    namespace hl = hg::linear;
     const LinearWork lw = linear_work(l, N, lddy, ldx);
     Array dz{dy, N, l->out, lddy, false, hg::kChkDout};
     Array W{w, l->out, l->in, l->in, true, hg::kChkWeights}, X{x, N, l->in, ldx, true, hg::kChkX};
+    const bool plain = l->act == HASHGRID_ACT_NONE;
+    if (dw != nullptr && narrow_layer(l, N) && aligned_rows(dz) && aligned_rows(X) &&
+        (dx == nullptr || vector_rows(dx, lddx, dx_dtype == HASHGRID_F32 ? 4 : 2)))
+        return launch_narrow_backward<T>(l, dz, X, N, w, plain ? nullptr : z, dx, lddx, dx_dtype, dw, dw_dtype, db, work, status, what, s);
     Array* list[2];
     int n = 0;
     if (dx != nullptr) list[n++] = &W;
     if (dw != nullptr) list[n++] = &X;
     if (int rc = realign(list, n, work + lw.copies, what, s)) return rc;
-    const bool convert = l->act != HASHGRID_ACT_NONE && (dx != nullptr || dw != nullptr);
+    const bool convert = !plain && (dx != nullptr || dw != nullptr);
+    hl::Sums sums[2];
+    int nsums = 0;
     if (convert || db != nullptr) {
         T* to = convert ? reinterpret_cast<T*>(work + lw.dz) : nullptr;
-        float* sums = db != nullptr ? reinterpret_cast<float*>(work + lw.sums) : nullptr;
-        const dim3 grid((unsigned)((l->out + 31) / 32), (unsigned)lw.parts);
-        hg::linear::slope_kernel<T><<<grid, 256, 0, s>>>(static_cast<const T*>(dy), lddy, static_cast<const T*>(z), N,
-                                                        l->out, l->act, to, lw.lddz, sums);
+        float* parts = db != nullptr ? reinterpret_cast<float*>(work + lw.sums) : nullptr;
+        const dim3 grid((unsigned)((l->out + 63) / 64), (unsigned)lw.parts);
+        auto k = aligned_rows(dz) && l->out % 8 == 0 ? hl::slope_kernel<T, true> : hl::slope_kernel<T, false>;
+        k<<<grid, 256, 0, s>>>(static_cast<const T*>(dy), lddy, static_cast<const T*>(z), N, l->out, l->act, to, lw.lddz, parts);
         if (int rc = launch_status(what)) return rc;
         if (convert) dz = Array{to, N, l->out, lw.lddz, false, hg::kChkWork};
-        if (db != nullptr) {
-            hg::linear::sum_parts_kernel<float><<<(unsigned)((l->out + 255) / 256), 256, 0, s>>>(sums, lw.parts, l->out, db, hg::kChkBias);
-            if (int rc = launch_status(what)) return rc;
-        }
+        if (db != nullptr) sums[nsums++] = hl::Sums{parts, l->out, l->out, lw.parts, 0, db, hg::kChkBias};
     }
     if (!convert && n > 0) {
         Array* d = &dz;
         if (int rc = realign(&d, 1, work + lw.dy, what, s)) return rc;
     }
     if (dx != nullptr) {
-        const hg::linear::Epilogue e{nullptr, nullptr, dx, nullptr, 0, lddx, 0, dx_dtype == HASHGRID_F32, hg::linear::kNoAct, hg::kChkOut};
+        const hl::Epilogue e{nullptr, nullptr, dx, nullptr, 0, lddx, 0, dx_dtype == HASHGRID_F32, hl::kNoAct, hg::kChkOut};
         if (int rc = launch_gemm<T>(dz, W, N, l->in, l->out, e, make_plan(N, l->in, l->out, device_sms()), status, what, s)) return rc;
     }
     if (dw != nullptr) {
         const bool parts = lw.splits > 1;
         float* out = reinterpret_cast<float*>(work + lw.dw);
-        const hg::linear::Epilogue e{nullptr, nullptr, parts ? out : dw, nullptr, 0, l->in, 0, parts || dw_dtype == HASHGRID_F32,
-                                     hg::linear::kNoAct, parts ? hg::kChkWork : hg::kChkGrad};
+        const hl::Epilogue e{nullptr, nullptr, parts ? out : dw, nullptr, 0, l->in, 0, parts || dw_dtype == HASHGRID_F32,
+                             hl::kNoAct, parts ? hg::kChkWork : hg::kChkGrad};
         const Plan plan = parts ? Plan{ceil_div(ceil_div(l->in, ceil_div(l->in, 256)), 16) * 16, 1, lw.splits, false}
                                 : make_plan(l->out, l->in, N, device_sms());
         dz.mn = true;
         if (int rc = launch_gemm<T>(dz, X, l->out, l->in, N, e, plan, status, what, s)) return rc;
-        if (parts) {
-            const int64_t n = (int64_t)l->in * l->out;
-            const unsigned blocks = (unsigned)((n + 255) / 256);
-            if (dw_dtype == HASHGRID_F32)
-                hg::linear::sum_parts_kernel<float><<<blocks, 256, 0, s>>>(out, lw.splits, n, static_cast<float*>(dw), hg::kChkGrad);
-            else
-                hg::linear::sum_parts_kernel<T><<<blocks, 256, 0, s>>>(out, lw.splits, n, static_cast<T*>(dw), hg::kChkGrad);
-            return launch_status(what);
-        }
+        const int64_t nw = (int64_t)l->in * l->out;
+        if (parts) sums[nsums++] = hl::Sums{out, nw, nw, lw.splits, dw_dtype == HASHGRID_F32 ? 0 : 1, dw, hg::kChkGrad};
     }
-    return ok();
+    return launch_sums<T>(sums, nsums, what, s);
 }
 
 int adamw_bytes(int dtype) { return dtype == HASHGRID_F32 ? 4 : dtype == HASHGRID_E4M3 ? 1 : 2; }

@@ -850,46 +850,392 @@ __global__ void __launch_bounds__(256) realign_kernel(const __grid_constant__ Re
     }
 }
 
+// ---------------------------------------------------------------------------------------
+// The whole backward pass of a narrow layer in one pass over its rows (in, out up to 128, many
+// rows: the layers of a head over a batch of points). Such a layer is bound by memory: dy, z and
+// x are read once and dx is written once, 2 (2 out + 2 in) bytes a row, where separate products
+// would move dz three more times and x once.
+//
+// Persistent blocks, one an SM, over tiles of 128 rows. TMA brings a tile of dy, z and x into a stage in
+// the 128-byte-swizzled layout. Eight warps turn dy into dz in place (and keep db's sums in
+// registers). That one copy of dz then serves both products: with rows of 64 outputs it is a k-major
+// A operand of dx = dz W and, read the other way, an mn-major A operand of dW = dz^T x, as the tile of x
+// is its mn-major B operand. W stays in shared memory. dx goes out as in the kernel above; dW
+// gathers in tensor memory over kFlush tiles, and is then added to fp32 registers: the tensor
+// cores' sums lose up to a unit in the last place at each addition, registers only half of one, and only
+// one in kFlush * 8 (measured for 2^20 rows: see the error bounds in the tests). Each block writes its sums
+// to the workspace, where sum_parts_kernel adds them in order.
+//
+// Warps: 0-7 write dx, 8 issues MMAs, 9 copies, 10-17 make dz and keep dW's and db's sums.
+// ---------------------------------------------------------------------------------------
+constexpr int kFlush = 8;
+constexpr int kNarrowThreads = 32 * 18;
+constexpr int kNarrowStages = 4;
+constexpr int kBox = kBm * 128;  // bytes of a box of 128 rows x 64 columns
+
+struct Narrow {
+    CUtensorMap tdy, tz, tx, tw;
+    int64_t rows;
+    int in, out, act;
+    int boxes_in, boxes_out, columns;  // 64-wide boxes of x and of dy (and z); columns from one accumulator to the next
+    int stages, stage_bytes, w_bytes, k_out;  // k_out: out, rounded up to 16
+    uint32_t id_dx, id_dw, tmem_columns;
+    Epilogue e;                        // of dx; out NULL: not wanted
+    float* parts;                      // [blocks][out * in + out]
+    int want_db;
+    int* status;
+};
+
+__host__ __device__ constexpr size_t narrow_smem(int stage_bytes_in_all, int w_bytes) {
+    return 1024 + (size_t)stage_bytes_in_all + w_bytes + kStaging + 256 + 16;
+}
+
+template <typename T, int kChunks>  // kChunks * 64 >= in
+__global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(const __grid_constant__ Narrow g) {
+    extern __shared__ uint8_t raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    uint8_t* ws = sm + (size_t)g.stages * g.stage_bytes;
+    uint8_t* staging = ws + g.w_bytes;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kStaging);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 32);
+    __shared__ volatile int abort_flag;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t sm0 = (uint32_t)__cvta_generic_to_shared(sm), w0 = (uint32_t)__cvta_generic_to_shared(ws);
+    const uint32_t bar0 = (uint32_t)__cvta_generic_to_shared(bars);
+    // barriers: stage copied [4], dz ready [4], stage free [4], dx done [2], dx room [2], dw done [2], dw room [2], W copied, drain
+    const uint32_t full = bar0, ready = full + 32, empty = ready + 32, done = empty + 32, room = done + 16, wdone = room + 16, wroom = wdone + 16,
+                   wfull = wroom + 16, drain = wfull + 8;
+    const bool dx = g.e.out != nullptr;
+    if (threadIdx.x == 32 * 9) {
+        abort_flag = 0;
+        for (int s = 0; s < g.stages; ++s) {
+            mlp::mbar_init(full + 8 * s, 1);
+            mlp::mbar_init(ready + 8 * s, 8);
+            mlp::mbar_init(empty + 8 * s, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mlp::mbar_init(done + 8 * i, 1);
+            mlp::mbar_init(room + 8 * i, 8);
+            mlp::mbar_init(wdone + 8 * i, 1);
+            mlp::mbar_init(wroom + 8 * i, 8);
+        }
+        mlp::mbar_init(wfull, 1);
+        mlp::mbar_init(drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"((uint32_t)__cvta_generic_to_shared(tslot)),
+                     "r"(g.tmem_columns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    mlp::fence_before();
+    __syncthreads();
+    mlp::fence_after();
+    const uint32_t tmem = *tslot;
+    const int tiles = (int)((g.rows + kBm - 1) / kBm);
+    const int mine = (tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1;  // at least one: the grid has no more blocks than tiles
+    const int dy_bytes = g.boxes_out * kBox, z_at = dy_bytes, x_at = g.act == kNoAct ? dy_bytes : 2 * dy_bytes;
+
+    if (warp == 9) {
+        // ------------------------------- TMA copies -------------------------------
+        if (lane == 0) {
+            bool ok = true;
+            if (dx) {
+                arrive_expect(wfull, g.w_bytes);
+                for (int j = 0; j < g.boxes_in; ++j) tma_load(w0 + j * g.k_out * 128, &g.tw, 64 * j, 0, wfull);
+            }
+            Ring r;
+            int issued = 0;
+            for (int i = 0; i < mine; ++i) {
+                if (!(ok = wait_bounded(empty + 8 * r.stage, r.phase ^ 1u, &abort_flag))) break;
+                const uint32_t bar = full + 8 * r.stage, s = sm0 + r.stage * g.stage_bytes;
+                const int m0 = (int)(blockIdx.x + (int64_t)i * gridDim.x) * kBm;
+                arrive_expect(bar, g.stage_bytes);
+                for (int j = 0; j < g.boxes_out; ++j) tma_load(s + j * kBox, &g.tdy, 64 * j, m0, bar);
+                if (g.act != kNoAct)
+                    for (int j = 0; j < g.boxes_out; ++j) tma_load(s + z_at + j * kBox, &g.tz, 64 * j, m0, bar);
+                for (int j = 0; j < g.boxes_in; ++j) tma_load(s + x_at + j * kBox, &g.tx, 64 * j, m0, bar);
+                r.next(g.stages);
+                issued = min(issued + 1, g.stages);
+            }
+            if (!ok && dx) mlp::wait_parity(wfull, 0);
+            for (; !ok && issued > 0; --issued) {  // copies in flight still write to this block's memory
+                if (r.stage == 0) {
+                    r.stage = g.stages;
+                    r.phase ^= 1u;
+                }
+                --r.stage;
+                mlp::wait_parity(full + 8 * r.stage, r.phase);
+            }
+        }
+    } else if (warp == 8) {
+        // ---------------------------------- MMAs ----------------------------------
+        const bool issues = elect_one();
+        Ring r;
+        bool ok = !dx || wait_bounded(wfull, 0, &abort_flag);
+        const uint32_t dw0 = tmem + 2 * g.columns, stage = g.stage_bytes >> 4;
+        const uint64_t dz_k = swizzled_desc(sm0, 0), dz_mn = swizzled_desc(sm0, kBox), x_mn = swizzled_desc(sm0 + x_at, kBox),
+                       w_mn = swizzled_desc(w0, g.k_out * 128);
+        for (int i = 0; i < mine && ok; ++i) {
+            const int b = i & 1, group = i / kFlush, f = group & 1;
+            if (!(ok = wait_bounded(full + 8 * r.stage, r.phase, &abort_flag))) break;
+            if (!(ok = wait_bounded(ready + 8 * r.stage, r.phase, &abort_flag))) break;
+            if (dx && !(ok = wait_bounded(room + 8 * b, ((i >> 1) & 1u) ^ 1u, &abort_flag))) break;
+            if (i % kFlush == 0 && !(ok = wait_bounded(wroom + 8 * f, ((group >> 1) & 1u) ^ 1u, &abort_flag))) break;
+            mlp::fence_after();
+            const uint32_t off = (uint32_t)r.stage * stage;
+            if (dx) {
+                for (int k = 0; k < g.k_out / 16; ++k) {
+                    const uint32_t ak = (k >> 2) * (kBox >> 4) + (k & 3) * 2, bk = k * 128;
+                    if (issues) mlp::mma(tmem + b * g.columns, dz_k + off + ak, w_mn + bk, g.id_dx, k != 0 ? 1u : 0u);
+                }
+                if (issues) mlp::commit(done + 8 * b);
+            }
+#pragma unroll
+            for (int k = 0; k < kBm / 16; ++k)
+                if (issues) mlp::mma(dw0 + f * g.columns, dz_mn + off + k * 128, x_mn + off + k * 128, g.id_dw, (i % kFlush != 0 || k != 0) ? 1u : 0u);
+            if (issues) mlp::commit(empty + 8 * r.stage);
+            if (issues && (i % kFlush == kFlush - 1 || i == mine - 1)) mlp::commit(wdone + 8 * f);
+            r.next(g.stages);
+        }
+        if (!ok && issues) {
+            mlp::commit(drain);
+            mlp::wait_parity(drain, 0);
+        }
+    } else if (warp < 8) {
+        // ---------------------------------- dx -----------------------------------
+        const int quarter = warp & 3, chunks = (g.in + 31) / 32;
+        float4* st = reinterpret_cast<float4*>(staging + warp * 4096);
+        for (int i = 0; i < mine && dx; ++i) {
+            const int b = i & 1;
+            const int64_t m0 = (blockIdx.x + (int64_t)i * gridDim.x) * kBm + 32 * quarter;
+            const bool ok = wait_bounded(done + 8 * b, (i >> 1) & 1u, &abort_flag);
+            if (__any_sync(0xffffffffu, !ok)) break;
+            mlp::fence_after();
+            for (int c = warp >> 2; c < chunks; c += 2) {
+                const int col = 32 * c + 8 * (lane & 3);
+                uint32_t v[32];
+                __syncwarp();
+                tmem_ld32(tmem + ((uint32_t)(32 * quarter) << 16) + b * g.columns + 32 * c, v);
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    st[unit_of(lane, u)] = make_float4(__uint_as_float(v[4 * u]), __uint_as_float(v[4 * u + 1]),
+                                                       __uint_as_float(v[4 * u + 2]), __uint_as_float(v[4 * u + 3]));
+                __syncwarp();
+                if (col < g.in) {
+                    float y[4][8];
+                    const uint4 q[4] = {};
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const int r = 8 * p + (lane >> 2);
+                        const float4 lo = st[unit_of(r, 2 * (lane & 3))], hi = st[unit_of(r, 2 * (lane & 3) + 1)];
+                        y[p][0] = lo.x; y[p][1] = lo.y; y[p][2] = lo.z; y[p][3] = lo.w;
+                        y[p][4] = hi.x; y[p][5] = hi.y; y[p][6] = hi.z; y[p][7] = hi.w;
+                    }
+                    emit_vectors<T, 4>(g.e, g.e.out, m0 + (lane >> 2), g.rows, col, y, q);
+                }
+            }
+            mlp::fence_before();
+            __syncwarp();
+            if (lane == 0) mlp::mbar_arrive(room + 8 * b);
+        }
+    } else {
+        // --------------------------- dz, and dW's and db's sums ---------------------------
+        const int tt = threadIdx.x - 32 * 10, quarter = warp & 3, half = (warp - 10) >> 2;
+        // a thread keeps one 16-byte column chunk and takes every 256 / (8 boxes_out)-th row
+        const int per_row = 8 * g.boxes_out, chunk = tt % per_row, row_step = 256 / per_row, row0 = tt / per_row;
+        const int box_at = (chunk >> 3) * kBox, cc = chunk & 7;
+        float sum[8] = {}, acc[kChunks][32];
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[c][j] = 0.f;
+        bool ok = true;
+        auto flush = [&](int group) {  // adds what a group of tiles gathered in tensor memory
+            const int f = group & 1;
+            const bool fine = wait_bounded(wdone + 8 * f, (group >> 1) & 1u, &abort_flag);
+            if (__any_sync(0xffffffffu, !fine)) return false;
+            mlp::fence_after();
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                if (32 * quarter >= g.out || 32 * (2 * c + half) >= g.in) continue;
+                uint32_t v[32];
+                __syncwarp();
+                tmem_ld32(tmem + ((uint32_t)(32 * quarter) << 16) + (2 + f) * g.columns + 32 * (2 * c + half), v);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) acc[c][j] += __uint_as_float(v[j]);
+            }
+            mlp::fence_before();
+            __syncwarp();
+            if (lane == 0) mlp::mbar_arrive(wroom + 8 * f);
+            return true;
+        };
+        Ring r;
+        for (int i = 0; i < mine && ok; ++i) {
+            ok = wait_bounded(full + 8 * r.stage, r.phase, &abort_flag);
+            if (__any_sync(0xffffffffu, !ok)) {
+                ok = false;
+                break;
+            }
+            uint8_t* s = sm + r.stage * g.stage_bytes + box_at;
+            if (g.act != kNoAct || g.want_db) {
+#pragma unroll 2
+                for (int row = row0; row < kBm; row += row_step) {
+                    uint4* at = reinterpret_cast<uint4*>(s + row * 128 + ((cc ^ (row & 7)) << 4));
+                    const uint4 q = *at;
+                    float d[8];
+                    const float2 d0 = unpack2<T>(q.x), d1 = unpack2<T>(q.y), d2 = unpack2<T>(q.z), d3 = unpack2<T>(q.w);
+                    d[0] = d0.x; d[1] = d0.y; d[2] = d1.x; d[3] = d1.y; d[4] = d2.x; d[5] = d2.y; d[6] = d3.x; d[7] = d3.y;
+                    if (g.act != kNoAct) {
+                        const uint4 zq = *reinterpret_cast<const uint4*>(reinterpret_cast<uint8_t*>(at) + z_at);
+                        const float2 z0 = unpack2<T>(zq.x), z1 = unpack2<T>(zq.y), z2 = unpack2<T>(zq.z), z3 = unpack2<T>(zq.w);
+                        const float z[8] = {z0.x, z0.y, z1.x, z1.y, z2.x, z2.y, z3.x, z3.y};
+                        times_slope(d, z, g.act);
+                        *at = pack8<T>(d);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[j] += d[j];
+                }
+                mlp::fence_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mlp::mbar_arrive(ready + 8 * r.stage);
+            r.next(g.stages);
+            // a group's sums are collected one tile after its last MMAs became ready: by then they are done, and nothing waits
+            if (i % kFlush == 1 && i > kFlush) ok = flush(i / kFlush - 1);
+        }
+        if (ok && mine > kFlush && (mine - 1) % kFlush == 0) ok = flush((mine - 1) / kFlush - 1);
+        if (ok) ok = flush((mine - 1) / kFlush);
+        float* part = g.parts + (int64_t)blockIdx.x * ((int64_t)g.out * g.in + g.out);
+        const int o = 32 * quarter + lane;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                const int col = 32 * (2 * c + half) + j;
+                float* p = part + (int64_t)o * g.in + col;
+                if (o < g.out && col < g.in && in_bounds<kChkWork>(p, 16))
+                    *reinterpret_cast<float4*>(p) = make_float4(acc[c][j], acc[c][j + 1], acc[c][j + 2], acc[c][j + 3]);
+            }
+        // db: the threads of a column chunk in order, through the first stage (every MMA that read it is done)
+        if (g.want_db) {
+            float* shared = reinterpret_cast<float*>(sm);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) shared[(row0 * per_row + chunk) * 8 + j] = sum[j];
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (tt < g.out) {
+                float s = 0.f;
+                for (int k = 0; k < row_step; ++k) s += shared[(k * per_row) * 8 + tt];
+                float* p = part + (int64_t)g.out * g.in + tt;
+                if (in_bounds<kChkWork>(p, 4)) *p = s;
+            }
+        }
+    }
+    __syncwarp();
+    mlp::fence_before();
+    __syncthreads();
+    mlp::fence_after();
+    if (threadIdx.x == 0 && abort_flag != 0 && g.status != nullptr) atomicExch(g.status, 1);
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(g.tmem_columns) : "memory");
+}
+
 // dz = dy act'(z), rounded to T, into dz (NULL: not wanted), and the sums of the unrounded dz
-// over this block's rows into sums[blockIdx.y][col] (NULL: not wanted). A block takes 32
-// columns, its 8 warps every eighth row of its share.
-template <typename T>
+// over this block's rows into sums[blockIdx.y][col] (NULL: not wanted). A block takes 64 columns, eight
+// neighbouring ones a thread, and every 32nd row of its share. kVectors: the rows of dy and z
+// begin on 16-byte boundaries and cols is a multiple of 8.
+template <typename T, bool kVectors>
 __global__ void __launch_bounds__(256) slope_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ z,
                                                     int64_t rows, int cols, int act, T* __restrict__ dz, int64_t lddz,
                                                     float* __restrict__ sums) {
-    __shared__ float part[8][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+    __shared__ float part[32][65];
+    const int col = blockIdx.x * 64 + 8 * (threadIdx.x & 7), r = threadIdx.x >> 3;
     const int64_t share = (rows + gridDim.y - 1) / gridDim.y, r0 = blockIdx.y * share, r1 = min(rows, r0 + share);
-    float s = 0.f;
-    if (col < cols)
-        for (int64_t r = r0 + warp; r < r1; r += 8) {
-            float d = in_bounds<kChkDout>(dy + r * lddy + col, 2) ? to_float(dy[r * lddy + col]) : 0.f;
-            if (act != kNoAct && in_bounds<kChkZ>(z + r * cols + col, 2)) {
-                float d2[2] = {d, 0.f}, z2[2] = {to_float(z[r * cols + col]), 0.f};
-                times_slope(d2, z2, act);
-                d = d2[0];
-            }
-            if (dz != nullptr && in_bounds<kChkWork>(dz + r * lddz + col, 2)) dz[r * lddz + col] = from_float<T>(d);
-            s += d;
-        }
-    part[warp][lane] = s;
-    __syncthreads();
-    if (warp == 0 && col < cols && sums != nullptr) {
+    const int n = min(8, cols - col);
+    float s[8] = {};
+    if (n > 0) {
+#pragma unroll 2
+        for (int64_t row = r0 + r; row < r1; row += 32) {
+            float d[8], v[8];
+            if (kVectors) {
+                const T* p = dy + row * lddy + col;
+                const uint4 q = in_bounds<kChkDout>(p, 16) ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
+                const float2 d0 = unpack2<T>(q.x), d1 = unpack2<T>(q.y), d2 = unpack2<T>(q.z), d3 = unpack2<T>(q.w);
+                d[0] = d0.x; d[1] = d0.y; d[2] = d1.x; d[3] = d1.y; d[4] = d2.x; d[5] = d2.y; d[6] = d3.x; d[7] = d3.y;
+                if (act != kNoAct) {
+                    const T* pz = z + row * cols + col;
+                    const uint4 zq = in_bounds<kChkZ>(pz, 16) ? __ldg(reinterpret_cast<const uint4*>(pz)) : make_uint4(0u, 0u, 0u, 0u);
+                    const float2 z0 = unpack2<T>(zq.x), z1 = unpack2<T>(zq.y), z2 = unpack2<T>(zq.z), z3 = unpack2<T>(zq.w);
+                    v[0] = z0.x; v[1] = z0.y; v[2] = z1.x; v[3] = z1.y; v[4] = z2.x; v[5] = z2.y; v[6] = z3.x; v[7] = z3.y;
+                }
+            } else {
 #pragma unroll
-        for (int w = 1; w < 8; ++w) s += part[w][lane];
-        if (in_bounds<kChkWork>(sums + (int64_t)blockIdx.y * cols + col, 4)) sums[(int64_t)blockIdx.y * cols + col] = s;
+                for (int j = 0; j < 8; ++j) {
+                    d[j] = j < n && in_bounds<kChkDout>(dy + row * lddy + col + j, 2) ? to_float(dy[row * lddy + col + j]) : 0.f;
+                    v[j] = act != kNoAct && j < n && in_bounds<kChkZ>(z + row * cols + col + j, 2) ? to_float(z[row * cols + col + j]) : 0.f;
+                }
+            }
+            if (act != kNoAct) times_slope(d, v, act);
+            // rows of dz are multiples of 8 wide: what lies between `cols` and that is zero
+            if (dz != nullptr && in_bounds<kChkWork>(dz + row * lddz + col, 16)) *reinterpret_cast<uint4*>(dz + row * lddz + col) = pack8<T>(d);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] += d[j];
+        }
+    }
+    if (sums == nullptr) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part[r][8 * (threadIdx.x & 7) + j] = s[j];
+    __syncthreads();
+    const int c = blockIdx.x * 64 + threadIdx.x;
+    if (threadIdx.x < 64 && c < cols) {
+        float t = 0.f;
+        for (int k = 0; k < 32; ++k) t += part[k][threadIdx.x];
+        if (in_bounds<kChkWork>(sums + (int64_t)blockIdx.y * cols + c, 4)) sums[(int64_t)blockIdx.y * cols + c] = t;
     }
 }
 
-// out[i] = sum over parts of sums[part][i], in order.
+// Sums of parts in order, of one or two arrays: out[i] = sum over p of parts[p * stride + i]. A block takes
+// 32 neighbours of an array, each of its 8 warps every eighth part.
+struct Sums {
+    const float* parts;
+    int64_t stride, n;
+    int count, out_type;  // parts; 0 fp32, 1 T
+    void* out;
+    int role;
+};
+struct SumsList {
+    Sums a[2];
+    int blocks0;  // blocks of a[0]
+};
+
 template <typename T>
-__global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict__ sums, int parts, int64_t n, T* __restrict__ out, int role) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
-    float s = 0.f;
-    for (int p = 0; p < parts; ++p)
-        if (in_bounds<kChkWork>(sums + p * n + i, 4)) s += sums[p * n + i];
-    if (in_bounds_role(role, out + i, sizeof(T))) out[i] = from_float<T>(s);
+__global__ void __launch_bounds__(256) sum_parts_kernel(const __grid_constant__ SumsList l) {
+    __shared__ float part[8][32];
+    const bool second = (int)blockIdx.x >= l.blocks0;
+    const Sums& s = l.a[second];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t i = (int64_t)(second ? blockIdx.x - l.blocks0 : blockIdx.x) * 32 + lane;
+    float v = 0.f;
+    if (i < s.n) {
+#pragma unroll 8
+        for (int p = warp; p < s.count; p += 8) {
+            const float* at = s.parts + p * s.stride + i;
+            if (in_bounds<kChkWork>(at, 4)) v += __ldg(at);
+        }
+    }
+    part[warp][lane] = v;
+    __syncthreads();
+    if (warp != 0 || i >= s.n) return;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) v += part[w][lane];
+    if (s.out_type == 0) {
+        float* p = static_cast<float*>(s.out) + i;
+        if (in_bounds_role(s.role, p, 4)) *p = v;
+    } else {
+        T* p = static_cast<T*>(s.out) + i;
+        if (in_bounds_role(s.role, p, sizeof(T))) *p = from_float<T>(v);
+    }
 }
 
 }  // namespace linear
