@@ -137,20 +137,28 @@ def _check(rc: int) -> None:
 
 
 def _ptr(a) -> int | None:
-    if a is None:
-        return None
-    if isinstance(a, int):
+    if a is None or isinstance(a, int):
         return a
     return a.data_ptr()
 
 
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _current_stream() -> int:
+    """Torch's current stream on the current device."""
+    global _current_stream
+    import torch
+    device, raw = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+
+    def _current_stream():
+        return raw(device())
+    return _current_stream()
 
 
 def hashgrid_version() -> str:
@@ -382,20 +390,21 @@ def _dtype_code(t, name: str) -> int:
 
 def _rows(t, n, width: int, dtypes, name: str) -> int:
     """Checks a [n, width] tensor with contiguous rows and returns its row stride."""
-    if t.dim() != 2 or t.shape[1] != width or (n is not None and t.shape[0] != n):
-        raise HashGridError(HASHGRID_ERR_ARG, f"{name} has shape {tuple(t.shape)}, [{'N' if n is None else n}, {width}] is wanted")
-    if _dtype_code(t, name) not in dtypes:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[1] != width or (n is not None and shape[0] != n):
+        raise HashGridError(HASHGRID_ERR_ARG, f"{name} has shape {tuple(shape)}, [{'N' if n is None else n}, {width}] is wanted")
+    if t.dtype not in dtypes:
         raise HashGridError(HASHGRID_ERR_ARG, f"{name} has type {t.dtype}")
-    if width > 1 and t.stride(1) != 1:
-        raise HashGridError(HASHGRID_ERR_ARG, f"{name}: the elements of a row must be contiguous (strides {t.stride()})")
-    return t.stride(0) if t.shape[0] > 1 else width
+    if width > 1 and stride[1] != 1:
+        raise HashGridError(HASHGRID_ERR_ARG, f"{name}: the elements of a row must be contiguous (strides {stride})")
+    return stride[0] if shape[0] > 1 else width
 
 
 def _flat(t, shape, dtypes, name: str) -> None:
     """Checks a contiguous tensor of the given shape."""
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise HashGridError(HASHGRID_ERR_ARG, f"{name} has shape {tuple(t.shape)}, strides {t.stride()}: contiguous {tuple(shape)} is wanted")
-    if _dtype_code(t, name) not in dtypes:
+    if t.dtype not in dtypes:
         raise HashGridError(HASHGRID_ERR_ARG, f"{name} has type {t.dtype}")
 
 
@@ -408,7 +417,10 @@ class Linear:
     def __init__(self, in_features: int, out_features: int, dtype: int = HASHGRID_BF16,
                  activation: int = HASHGRID_ACT_NONE):
         self.in_features, self.out_features, self.dtype, self.activation = in_features, out_features, dtype, activation
-        self._shape = (out_features, in_features)
+        import torch
+        own = torch.float16 if dtype == HASHGRID_F16 else torch.bfloat16
+        self._shape, self._bias_shape = (out_features, in_features), (out_features,)
+        self._own, self._either, self._f32 = (own,), (own, torch.float32), (torch.float32,)
         self.handle = hashgrid_linear_create(in_features, out_features, dtype, activation)
 
     def __del__(self):
@@ -417,28 +429,24 @@ class Linear:
             lib.hashgrid_linear_destroy(h)
             self.handle = None
 
-    def _torch_dtype(self):
-        import torch
-        return torch.float16 if self.dtype == HASHGRID_F16 else torch.bfloat16
-
     def forward(self, x, w, b=None, residual=None, y=None, z=None, workspace=None, device_status=None, stream=None):
         """Returns y. ``w`` [out, in] contiguous; ``b`` [out] fp32; ``y`` (allocated if None, of ``residual``'s
         type or else the layer's) and ``residual`` of the layer's type or fp32; ``z``: a contiguous [N, out] tensor
         that receives the pre-activation, for ``backward``; ``workspace``: bytes from ``workspace()`` (allocated if
         None; only rows that do not begin on 16-byte boundaries need any)."""
-        N, own = x.shape[0], (self.dtype,)
+        N, own = x.shape[0], self._own
         ldx = _rows(x, None, self.in_features, own, "x")
         _flat(w, self._shape, own, "w")
         if b is not None:
-            _flat(b, self._shape[:1], (HASHGRID_F32,), "b")
+            _flat(b, self._bias_shape, self._f32, "b")
         if y is None:
             import torch
             y = torch.empty((N, self.out_features), device=x.device,
-                            dtype=self._torch_dtype() if residual is None else residual.dtype)
+                            dtype=self._own[0] if residual is None else residual.dtype)
             _record(y, stream)
-        ldy = _rows(y, N, self.out_features, (self.dtype, HASHGRID_F32), "y")
-        y_dtype = _dtype_code(y, "y")
-        ldr = 0 if residual is None else _rows(residual, N, self.out_features, (y_dtype,), "residual")
+        ldy = _rows(y, N, self.out_features, self._either, "y")
+        y_dtype = self.dtype if y.dtype is own[0] else HASHGRID_F32
+        ldr = 0 if residual is None else _rows(residual, N, self.out_features, (y.dtype,), "residual")
         if z is not None:
             _flat(z, (N, self.out_features), own, "z")
         size = 0
@@ -447,8 +455,8 @@ class Linear:
         elif ldx % 8 or self.in_features % 8:
             size = lib.hashgrid_linear_forward_workspace(self.handle, N, ldx)
             workspace = self._scratch(size, x.device, stream)
-        hashgrid_linear_forward(self.handle, x, ldx, N, w, b, residual, ldr, y, ldy, y_dtype, z, workspace, size,
-                                device_status, stream)
+        hashgrid_linear_forward(self.handle, x.data_ptr(), ldx, N, w.data_ptr(), b, residual, ldr, y.data_ptr(), ldy,
+                                y_dtype, z, workspace, size, device_status, stream)
         return y
 
     def workspace(self, N: int, device, lddy: int | None = None, ldx: int | None = None):
@@ -470,14 +478,14 @@ class Linear:
         fp32), True to allocate it (the layer's type, fp32, fp32), or None to leave it out. ``z``: what ``forward``
         wrote (not needed without an activation)."""
         import torch
-        N, own, either = dL_dy.shape[0], (self.dtype,), (self.dtype, HASHGRID_F32)
+        N, own, either = dL_dy.shape[0], self._own, self._either
         lddy = _rows(dL_dy, None, self.out_features, own, "dL_dy")
         ldx = _rows(x, N, self.in_features, own, "x")
         _flat(w, self._shape, own, "w")
         if z is not None:
             _flat(z, (N, self.out_features), own, "z")
         if dL_dx is True:
-            dL_dx = torch.empty((N, self.in_features), device=x.device, dtype=self._torch_dtype())
+            dL_dx = torch.empty((N, self.in_features), device=x.device, dtype=self._own[0])
             _record(dL_dx, stream)
         if dL_dw is True:
             dL_dw = torch.empty((self.out_features, self.in_features), device=x.device, dtype=torch.float32)
@@ -489,7 +497,7 @@ class Linear:
         if dL_dw is not None:
             _flat(dL_dw, self._shape, either, "dL_dw")
         if dL_db is not None:
-            _flat(dL_db, (self.out_features,), (HASHGRID_F32,), "dL_db")
+            _flat(dL_db, self._bias_shape, self._f32, "dL_db")
         if workspace is None:
             workspace = self._scratch(lib.hashgrid_linear_backward_workspace(self.handle, N, lddy, ldx), x.device, stream)
         hashgrid_linear_backward(self.handle, dL_dy, lddy, x, ldx, N, w, z, dL_dx, lddx,

@@ -17,6 +17,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <initializer_list>
+#include <mutex>
 #include <new>
 #include <string>
 #include <type_traits>
@@ -627,6 +628,33 @@ int check_out_type(const hashgrid_linear_s* layer, int dtype, const char* name) 
     return ok();
 }
 
+// prepare_smem once for each kernel, size and device: the attribute call costs as much as a small launch's checks.
+template <typename K>
+int prepare_smem_once(K kernel, size_t smem) {
+    struct Entry {
+        const void* kernel;
+        int device;
+        size_t smem;
+    };
+    static std::mutex lock;
+    static Entry table[64];
+    static int used = 0;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const void* key = reinterpret_cast<const void*>(kernel);
+    std::lock_guard<std::mutex> hold(lock);
+    for (int i = 0; i < used; ++i)
+        if (table[i].kernel == key && table[i].device == dev) {
+            if (table[i].smem >= smem) return ok();
+            if (int rc = prepare_smem(kernel, smem)) return rc;
+            table[i].smem = smem;
+            return ok();
+        }
+    if (int rc = prepare_smem(kernel, smem)) return rc;
+    if (used < 64) table[used++] = Entry{key, dev, smem};
+    return ok();
+}
+
 typedef CUresult (*PFN_tensorMapEncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -671,15 +699,17 @@ struct Plan {
     bool pair;    // 256-row tiles by pairs of SMs
 };
 
-// Where 256 x 256 tiles by pairs of SMs occupy the device: those. Else 128-row tiles: as few column tiles
-// as there can be while every SM has one, then narrower ones, down to 64 columns, and if
-// those are still too few, a split of K over up to 8 blocks of a cluster, each with two
-// 64-wide steps at least.
+// Where 256 x 256 tiles by pairs of SMs occupy the device and K is long: those. Else 128-row tiles of up to
+// 128 columns, two blocks a SM, since with few steps of K what counts is how many warps write out: as few
+// column tiles as there can be while every SM has one, then narrower ones, down to 64 columns, and
+// if those are still too few, a split of K over up to 8 blocks of a cluster, each with two 64-wide
+// steps at least.
 Plan make_plan(int64_t M, int64_t N, int64_t K, int sms) {
     const int64_t mt = ceil_div(M, hg::linear::kBm);
     int64_t nt = ceil_div(N, 256);
     const int wide = ceil_div(ceil_div(N, nt), 32) * 32;
-    if (N >= 160 && (int64_t)ceil_div(M, 256) * nt >= sms / 2 && K >= 256) return Plan{wide, 1, 1, true};
+    if (N >= 160 && (int64_t)ceil_div(M, 256) * nt >= sms / 2 && K >= 512) return Plan{wide, 1, 1, true};
+    nt = ceil_div(N, 128);
     while (mt * nt < sms && ceil_div(N, nt) > 64) ++nt;
     Plan p{ceil_div(ceil_div(N, nt), 16) * 16, 1, 1, false};
     const int64_t tiles = mt * ceil_div(N, p.bn);
@@ -779,7 +809,7 @@ int launch_gemm(const Array& A, const Array& B, int64_t M, int64_t N, int64_t K,
     cfg.numAttrs = plan.cluster > 1 || plan.pair ? 1 : 0;
     auto k = plan.pair ? (vectors ? hl::gemm_kernel<T, true, true> : hl::gemm_kernel<T, true, false>)
                        : (vectors ? hl::gemm_kernel<T, false, true> : hl::gemm_kernel<T, false, false>);
-    if (int rc = prepare_smem(k, smem)) return rc;
+    if (int rc = prepare_smem_once(k, smem)) return rc;
     if (cudaLaunchKernelEx(&cfg, k, g) != cudaSuccess) return launch_status(what);
     return ok();
 }
@@ -913,7 +943,7 @@ int launch_narrow_backward(const hashgrid_linear_s* l, const Array& dy, const Ar
     const int blocks = std::min(kWorkSms, device_sms());
     const size_t smem = hl::narrow_smem(g.stages * g.stage_bytes, g.w_bytes);
     auto k = l->in <= 64 ? hl::narrow_backward_kernel<T, 1> : hl::narrow_backward_kernel<T, 2>;
-    if (int rc = prepare_smem(k, smem)) return rc;
+    if (int rc = prepare_smem_once(k, smem)) return rc;
     k<<<(unsigned)std::min<int64_t>(blocks, ceil_div(N, hl::kBm)), hl::kNarrowThreads, smem, s>>>(g);
     if (int rc = launch_status(what)) return rc;
     const int64_t nw = (int64_t)l->in * l->out, stride = nw + l->out;

@@ -283,20 +283,20 @@ __device__ __forceinline__ void load_residuals(const Epilogue& e, int64_t row, i
         q[r] = row + 8 * r < rows && in_bounds<kChkResidual>(p, 16) ? *reinterpret_cast<const uint4*>(p) : make_uint4(0u, 0u, 0u, 0u);
 }
 
-// Eight rows of a column, bias already added.
-template <typename T>
+// Eight rows of a column, bias already added. kFull: all of them are there.
+template <typename T, bool kFull>
 __device__ __forceinline__ void emit_column8(const Epilogue& e, void* out, int64_t row, int rows, int64_t col, float (&y)[8]) {
     float res[8];
 #pragma unroll
-    for (int p = 0; p < 8; ++p) res[p] = p < rows ? residual1<T>(e, row + p, col) : 0.f;
+    for (int p = 0; p < 8; ++p) res[p] = kFull || p < rows ? residual1<T>(e, row + p, col) : 0.f;
     if (e.z != nullptr)
 #pragma unroll
         for (int p = 0; p < 8; ++p)
-            if (p < rows) store_z1<T>(e, row + p, col, y[p]);
+            if (kFull || p < rows) store_z1<T>(e, row + p, col, y[p]);
     activate(y, e.act);
 #pragma unroll
     for (int p = 0; p < 8; ++p)
-        if (p < rows) store_y1<T>(e, out, row + p, col, y[p] + res[p]);
+        if (kFull || p < rows) store_y1<T>(e, out, row + p, col, y[p] + res[p]);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -682,7 +682,8 @@ __global__ void __launch_bounds__(kThreads, kPair ? 1 : 2) gemm_kernel(const __g
                         float y[8];
 #pragma unroll
                         for (int p = 0; p < 8; ++p) y[p] = sf[unit_of(r0 + p, lane >> 2) * 4 + (lane & 3)] + bias;
-                        emit_column8<T>(e, out, m0 + r0, rows - r0, c0 + lane, y);
+                        if (rows - r0 >= 8) emit_column8<T, true>(e, out, m0 + r0, 8, c0 + lane, y);
+                        else emit_column8<T, false>(e, out, m0 + r0, rows - r0, c0 + lane, y);
                     }
                 }
             }
