@@ -691,6 +691,29 @@ struct Array {
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
+// Launches a kernel that waits itself for what comes before it in the stream (after_previous_kernel), so
+// that its start overlaps the end of the previous one.
+template <typename... P, typename... A>
+int launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, unsigned cluster, cudaStream_t s, const char* what,
+                 const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2] = {};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return launch_status(what);
+    return ok();
+}
+
 // How a product is cut.
 struct Plan {
     int bn;       // tile width, a multiple of 16
@@ -698,6 +721,9 @@ struct Plan {
     int splits;   // or parts of K that go to a workspace
     bool pair;    // 256-row tiles by pairs of SMs
 };
+
+// The width of N's column tiles, at most `most`: a multiple of 16.
+int wide_tile(int64_t N, int most) { return ceil_div(ceil_div(N, ceil_div(N, most)), 16) * 16; }
 
 // Where 256 x 256 tiles by pairs of SMs occupy the device and K is long: those. Else 128-row tiles of up to
 // 128 columns, two blocks a SM, since with few steps of K what counts is how many warps write out: as few
@@ -749,15 +775,20 @@ int set_side(hg::linear::Side& s, CUtensorMap& map, const Array& a, int wanted, 
 
 bool vector_rows(const void* p, int64_t ld, size_t elem) { return p == nullptr || ((size_t)ld * elem) % 16 == 0; }
 
-// D[M, N] = A B^T over K on the tensor cores. plan.splits > 1: K is cut into so many parts, each an
-// fp32 [M, N] of its own in e.out.
-template <typename T>
-int launch_gemm(const Array& A, const Array& B, int64_t M, int64_t N, int64_t K, const hg::linear::Epilogue& e, const Plan& plan,
-                int* status, const char* what, cudaStream_t s) {
+// A product ready to be launched: D[M, N] = A B^T over K on the tensor cores. plan.splits > 1: K is cut into
+// so many parts, each an fp32 [M, N] of its own in e.out.
+struct Product {
+    hg::linear::Gemm g;
+    int64_t grid;  // blocks
+    size_t smem;
+    bool vectors;
+};
+
+int set_product(Product& p, bool half, const Array& A, const Array& B, int64_t M, int64_t N, int64_t K, const hg::linear::Epilogue& e,
+                const Plan& plan, int* status, const char* what) {
     namespace hl = hg::linear;
     const int bn = plan.bn, splits = std::max(plan.splits, plan.cluster), group = plan.pair ? 2 : 1;
-    hl::Gemm g;
-    std::memset(&g, 0, sizeof g);
+    hl::Gemm& g = p.g;
     if (int rc = set_side(g.a, g.ta, A, hl::kBm, what)) return rc;
     if (int rc = set_side(g.b, g.tb, B, bn / group, what)) return rc;
     g.M = M;
@@ -785,33 +816,43 @@ int launch_gemm(const Array& A, const Array& B, int64_t M, int64_t N, int64_t K,
     g.stages = std::min(hl::kMaxStages, (budget - kept - (int)hl::gemm_smem(0)) / g.stage_bytes);
     if (g.cluster > 1)  // a split product's shares lie in the stages
         while (g.stages * g.stage_bytes < 4 * ceil_div(bn, 32) * 4096) ++g.stages;
-    const uint32_t type = std::is_same<T, __half>::value ? 0u : 1u;
+    const uint32_t type = half ? 0u : 1u;
     g.idesc = (1u << 4) | (type << 7) | (type << 10) | ((A.mn ? 1u : 0u) << 15) | ((B.mn ? 1u : 0u) << 16) |
               ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(hl::kBm * group >> 4) << 24);
     g.e = e;
     const size_t os = e.out_f32 ? 4 : 2;
     g.split_stride = plan.splits > 1 ? M * N : 0;
-    const bool vectors = N % 8 == 0 && vector_rows(e.out, e.ldo, os) && vector_rows(e.residual, e.ldr, os) && vector_rows(e.z, e.ldz, 2);
+    p.vectors = N % 8 == 0 && vector_rows(e.out, e.ldo, os) && vector_rows(e.residual, e.ldr, os) && vector_rows(e.z, e.ldz, 2);
     g.status = status;
-    const size_t smem = hl::gemm_smem(g.stages * g.stage_bytes + kept);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(plan.cluster > 1 ? tiles : group * std::min<int64_t>(tiles, std::max(1, per_sm * sms / splits / group))),
-                       (unsigned)splits);
-    cfg.blockDim = dim3(hl::kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at = {};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)group;
-    at.val.clusterDim.y = (unsigned)plan.cluster;
-    at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = plan.cluster > 1 || plan.pair ? 1 : 0;
+    p.smem = hl::gemm_smem(g.stages * g.stage_bytes + kept);
+    g.blocks = (int)(plan.cluster > 1 ? tiles : std::min<int64_t>(tiles, std::max(1, per_sm * sms / splits / group)));
+    p.grid = (int64_t)g.blocks * splits * group;
+    return ok();
+}
+
+// Launches one product, or two of the same plan.pair and plan.cluster.
+template <typename T>
+int launch_products(const Product* p, int count, const Plan& plan, const char* what, cudaStream_t s) {
+    namespace hl = hg::linear;
+    hl::Gemms l;
+    std::memcpy(&l.of[0], &p[0].g, sizeof(hl::Gemm));
+    std::memcpy(&l.of[1], &p[count - 1].g, sizeof(hl::Gemm));
+    l.second = count > 1 ? (int)p[0].grid : 0x7fffffff;
+    const int64_t grid = p[0].grid + (count > 1 ? p[1].grid : 0);
+    const size_t smem = std::max(p[0].smem, p[count - 1].smem);
+    const bool vectors = p[0].vectors && p[count - 1].vectors;
     auto k = plan.pair ? (vectors ? hl::gemm_kernel<T, true, true> : hl::gemm_kernel<T, true, false>)
                        : (vectors ? hl::gemm_kernel<T, false, true> : hl::gemm_kernel<T, false, false>);
     if (int rc = prepare_smem_once(k, smem)) return rc;
-    if (cudaLaunchKernelEx(&cfg, k, g) != cudaSuccess) return launch_status(what);
-    return ok();
+    return launch_after(k, dim3((unsigned)grid), hl::kThreads, smem, plan.pair ? 2 : plan.cluster, s, what, l);
+}
+
+template <typename T>
+int launch_gemm(const Array& A, const Array& B, int64_t M, int64_t N, int64_t K, const hg::linear::Epilogue& e, const Plan& plan,
+                int* status, const char* what, cudaStream_t s) {
+    Product p;
+    if (int rc = set_product(p, std::is_same<T, __half>::value, A, B, M, N, K, e, plan, status, what)) return rc;
+    return launch_products<T>(&p, 1, plan, what, s);
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -845,8 +886,7 @@ int realign(Array* const* arrays, int count, char* work, const char* what, cudaS
     if (n == 0) return ok();
     const int64_t blocks = (l.total + 1023) / 1024;
     if (blocks > 0x7fffffffLL) return fail(HASHGRID_ERR_ARG, "%s: too many rows to realign", what);
-    hg::linear::realign_kernel<<<(unsigned)blocks, 256, 0, s>>>(l);
-    return launch_status(what);
+    return launch_after(hg::linear::realign_kernel, dim3((unsigned)blocks), 256, 0, 1, s, what, l);
 }
 
 // The backward pass's workspace: the copies of x and w (or dy) with aligned rows, dz (where it has to be
@@ -861,22 +901,22 @@ struct LinearWork {
 constexpr int kWorkSms = 148;  // the workspace's size may not depend on the device
 
 // Whether the one-pass kernel takes a layer: its tile of dy, z and x (x 2 stages) and W fit into shared
-// memory, and there are tiles enough for every SM.
+// memory, and there are 64 tiles or more.
 bool narrow_layer(const hashgrid_linear_s* l, int64_t N) {
-    if (l->in > 128 || l->out > 128 || l->in % 8 != 0 || l->out % 8 != 0 || N < 4 * kWorkSms * hg::linear::kBm) return false;
+    if (l->in > 128 || l->out > 128 || l->in % 8 != 0 || l->out % 8 != 0 || N < 64 * hg::linear::kBm) return false;
     const int boxes_out = ceil_div(l->out, 64), boxes_in = ceil_div(l->in, 64);
     const int stage = (boxes_out * (l->act == HASHGRID_ACT_NONE ? 1 : 2) + boxes_in) * hg::linear::kBox;
     return hg::linear::narrow_smem(2 * stage, ceil_div(l->out, 16) * 16 * boxes_in * 128) <= 226 * 1024;
 }
 
-// dw sums over the rows: beyond what a cluster's 8 blocks can share, so many shares of them that
-// every SM has a tile of one.
+// dw sums over the rows. Where its tiles are fewer than the SMs, the rows are cut into so many shares that
+// every SM has a tile of one, each share of four 64-row steps at least.
 LinearWork linear_work(const hashgrid_linear_s* l, int64_t N, int64_t lddy, int64_t ldx) {
     LinearWork w;
     w.lddz = (l->out + 7) / 8 * 8;
-    w.parts = (int)std::min<int64_t>(256, (N + 63) / 64);
-    const int64_t tiles = (int64_t)ceil_div(l->out, hg::linear::kBm) * ceil_div(l->in, 256);
-    w.splits = N <= 16384 ? 1 : (int)std::max<int64_t>(1, kWorkSms / tiles);
+    w.parts = N <= 256 ? 1 : (int)std::min<int64_t>(256, (N + 63) / 64);
+    const int64_t tiles = (int64_t)ceil_div(l->out, hg::linear::kBm) * ceil_div(l->in, 128);
+    w.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kWorkSms / tiles, N / (4 * hg::linear::kBk)));
     const bool plain = l->act == HASHGRID_ACT_NONE;
     w.copies = 0;
     w.dy = (l->in % 8 != 0 ? realigned_bytes(l->out, l->in) : 0) + (ldx % 8 != 0 ? realigned_bytes(N, l->in) : 0);
@@ -901,8 +941,7 @@ int launch_sums(const hg::linear::Sums* list, int count, const char* what, cudaS
     }
     if (count == 0) return ok();
     if (blocks > 0x7fffffffLL) return fail(HASHGRID_ERR_ARG, "%s: too many weights", what);
-    hg::linear::sum_parts_kernel<T><<<(unsigned)blocks, 256, 0, s>>>(l);
-    return launch_status(what);
+    return launch_after(hg::linear::sum_parts_kernel<T>, dim3((unsigned)blocks), 256, 0, 1, s, what, l);
 }
 
 template <typename T>
@@ -940,12 +979,11 @@ int launch_narrow_backward(const hashgrid_linear_s* l, const Array& dy, const Ar
     g.parts = reinterpret_cast<float*>(work);
     g.want_db = db != nullptr;
     g.status = status;
-    const int blocks = std::min(kWorkSms, device_sms());
+    const int blocks = std::min(std::min(kWorkSms, device_sms()), ceil_div(N, hl::kBm));
     const size_t smem = hl::narrow_smem(g.stages * g.stage_bytes, g.w_bytes);
     auto k = l->in <= 64 ? hl::narrow_backward_kernel<T, 1> : hl::narrow_backward_kernel<T, 2>;
     if (int rc = prepare_smem_once(k, smem)) return rc;
-    k<<<(unsigned)std::min<int64_t>(blocks, ceil_div(N, hl::kBm)), hl::kNarrowThreads, smem, s>>>(g);
-    if (int rc = launch_status(what)) return rc;
+    if (int rc = launch_after(k, dim3((unsigned)blocks), hl::kNarrowThreads, smem, 1, s, what, g)) return rc;
     const int64_t nw = (int64_t)l->in * l->out, stride = nw + l->out;
     hl::Sums sums[2] = {{g.parts, stride, nw, blocks, dw_dtype == HASHGRID_F32 ? 0 : 1, dw, hg::kChkGrad},
                         {g.parts + nw, stride, l->out, blocks, 0, db, hg::kChkBias}};
@@ -992,31 +1030,46 @@ int launch_linear_backward(const hashgrid_linear_s* l, const void* dy, int64_t l
         float* parts = db != nullptr ? reinterpret_cast<float*>(work + lw.sums) : nullptr;
         const dim3 grid((unsigned)((l->out + 63) / 64), (unsigned)lw.parts);
         auto k = aligned_rows(dz) && l->out % 8 == 0 ? hl::slope_kernel<T, true> : hl::slope_kernel<T, false>;
-        k<<<grid, 256, 0, s>>>(static_cast<const T*>(dy), lddy, static_cast<const T*>(z), N, l->out, l->act, to, lw.lddz, parts);
-        if (int rc = launch_status(what)) return rc;
+        if (int rc = launch_after(k, grid, 256, 0, 1, s, what, static_cast<const T*>(dy), lddy, static_cast<const T*>(z), N, l->out, l->act, to,
+                                  lw.lddz, lw.parts > 1 ? parts : db, lw.parts > 1 ? (int)hg::kChkWork : (int)hg::kChkBias))
+            return rc;
         if (convert) dz = Array{to, N, l->out, lw.lddz, false, hg::kChkWork};
-        if (db != nullptr) sums[nsums++] = hl::Sums{parts, l->out, l->out, lw.parts, 0, db, hg::kChkBias};
+        if (db != nullptr && lw.parts > 1) sums[nsums++] = hl::Sums{parts, l->out, l->out, lw.parts, 0, db, hg::kChkBias};
     }
     if (!convert && n > 0) {
         Array* d = &dz;
         if (int rc = realign(&d, 1, work + lw.dy, what, s)) return rc;
     }
-    if (dx != nullptr) {
-        const hl::Epilogue e{nullptr, nullptr, dx, nullptr, 0, lddx, 0, dx_dtype == HASHGRID_F32, hl::kNoAct, hg::kChkOut};
-        if (int rc = launch_gemm<T>(dz, W, N, l->in, l->out, e, make_plan(N, l->in, l->out, device_sms()), status, what, s)) return rc;
+    // dx and dW do not depend on each other. Where neither fills the device they share a launch, dW cut into parts
+    // of the rows that the sums kernel adds; else each has its own.
+    constexpr bool half = std::is_same<T, __half>::value;
+    const int sms = device_sms();
+    Plan px = make_plan(N, l->in, l->out, sms), pw = make_plan(l->out, l->in, N, sms);
+    if (lw.splits > 1) {
+        pw = Plan{wide_tile(l->in, 128), 1, lw.splits, false};
+        if (!px.pair) px.cluster = 1;
     }
-    if (dw != nullptr) {
-        const bool parts = lw.splits > 1;
-        float* out = reinterpret_cast<float*>(work + lw.dw);
-        const hl::Epilogue e{nullptr, nullptr, parts ? out : dw, nullptr, 0, l->in, 0, parts || dw_dtype == HASHGRID_F32,
-                             hl::kNoAct, parts ? hg::kChkWork : hg::kChkGrad};
-        const Plan plan = parts ? Plan{ceil_div(ceil_div(l->in, ceil_div(l->in, 256)), 16) * 16, 1, lw.splits, false}
-                                : make_plan(l->out, l->in, N, device_sms());
-        dz.mn = true;
-        if (int rc = launch_gemm<T>(dz, X, l->out, l->in, N, e, plan, status, what, s)) return rc;
-        const int64_t nw = (int64_t)l->in * l->out;
-        if (parts) sums[nsums++] = hl::Sums{out, nw, nw, lw.splits, dw_dtype == HASHGRID_F32 ? 0 : 1, dw, hg::kChkGrad};
+    const hl::Epilogue ex{nullptr, nullptr, dx, nullptr, 0, lddx, 0, dx_dtype == HASHGRID_F32, hl::kNoAct, hg::kChkOut};
+    const bool parts = pw.splits > 1;
+    float* out = reinterpret_cast<float*>(work + lw.dw);
+    const hl::Epilogue ew{nullptr, nullptr, parts ? out : dw, nullptr, 0, l->in, 0, parts || dw_dtype == HASHGRID_F32,
+                          hl::kNoAct, parts ? hg::kChkWork : hg::kChkGrad};
+    Product p[2];
+    int np = 0;
+    Array dzt = dz;
+    dzt.mn = true;
+    if (dw != nullptr)
+        if (int rc = set_product(p[np++], half, dzt, X, l->out, l->in, N, ew, pw, status, what)) return rc;
+    if (dx != nullptr)
+        if (int rc = set_product(p[np++], half, dz, W, N, l->in, l->out, ex, px, status, what)) return rc;
+    if (np == 2 && px.pair == pw.pair && px.cluster == pw.cluster) {
+        if (int rc = launch_products<T>(p, 2, px, what, s)) return rc;
+    } else {
+        for (int i = 0; i < np; ++i)
+            if (int rc = launch_products<T>(&p[i], 1, dw != nullptr && i == 0 ? pw : px, what, s)) return rc;
     }
+    const int64_t nw = (int64_t)l->in * l->out;
+    if (dw != nullptr && parts) sums[nsums++] = hl::Sums{out, nw, nw, lw.splits, dw_dtype == HASHGRID_F32 ? 0 : 1, dw, hg::kChkGrad};
     return launch_sums<T>(sums, nsums, what, s);
 }
 
@@ -1090,8 +1143,7 @@ int launch_adamw(const hashgrid_adamw_s* o, const hashgrid_adamw_s::Launch& l, h
     list.blocks = l.blocks;
     std::memcpy(list.t, o->tensors.data() + l.begin, sizeof(hg::adamw::Tensor) * l.count);
     const unsigned blocks = (l.blocks + hg::adamw::kWarps - 1) / hg::adamw::kWarps;
-    hg::adamw::step_kernel<kCap><<<blocks, 32 * hg::adamw::kWarps, 0, s>>>(list, a);
-    return launch_status("adamw_step");
+    return launch_after(hg::adamw::step_kernel<kCap>, dim3(blocks), 32 * hg::adamw::kWarps, 0, 1, s, "adamw_step", list, a);
 }
 
 }  // namespace

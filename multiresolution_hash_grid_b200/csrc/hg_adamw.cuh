@@ -367,6 +367,7 @@ __device__ __forceinline__ void step_block(const Tensor& T, const Params& a, con
 template <int kCap>
 __global__ void __launch_bounds__(32 * kWarps, 4) step_kernel(const __grid_constant__ List<kCap> list, const Params a) {
     Rates r{a.c1, a.root2, 0.f, 0.f, a.step};
+    after_previous_kernel();
     if (a.device_step != nullptr) {
         const int64_t t = *a.device_step;
         if (t < 1) return;

@@ -62,4 +62,12 @@ __device__ __forceinline__ constexpr bool in_bounds(const void*, uint32_t) {
 }
 #endif
 
+// Launched with programmatic stream serialization, a kernel may start while the one before it in the
+// stream still runs: it sets itself up and touches no global memory before this, which waits until
+// everything before it has finished and can be seen. The kernel after it may then do the same.
+__device__ __forceinline__ void after_previous_kernel() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 }  // namespace hg

@@ -283,20 +283,45 @@ __device__ __forceinline__ void load_residuals(const Epilogue& e, int64_t row, i
         q[r] = row + 8 * r < rows && in_bounds<kChkResidual>(p, 16) ? *reinterpret_cast<const uint4*>(p) : make_uint4(0u, 0u, 0u, 0u);
 }
 
-// Eight rows of a column, bias already added. kFull: all of them are there.
+// Eight rows of a column, bias already added. kFull: all of them are there. What depends on the call alone
+// is decided once for all eight, so that their loads go out together.
 template <typename T, bool kFull>
 __device__ __forceinline__ void emit_column8(const Epilogue& e, void* out, int64_t row, int rows, int64_t col, float (&y)[8]) {
-    float res[8];
+    float res[8] = {};
+    if (e.residual != nullptr) {
+        if (e.out_f32) {
+            const float* p = static_cast<const float*>(e.residual) + row * e.ldr + col;
 #pragma unroll
-    for (int p = 0; p < 8; ++p) res[p] = kFull || p < rows ? residual1<T>(e, row + p, col) : 0.f;
-    if (e.z != nullptr)
+            for (int k = 0; k < 8; ++k, p += e.ldr)
+                if ((kFull || k < rows) && in_bounds<kChkResidual>(p, 4)) res[k] = *p;
+        } else {
+            const T* p = static_cast<const T*>(e.residual) + row * e.ldr + col;
+            T raw[8] = {};
 #pragma unroll
-        for (int p = 0; p < 8; ++p)
-            if (kFull || p < rows) store_z1<T>(e, row + p, col, y[p]);
+            for (int k = 0; k < 8; ++k, p += e.ldr)
+                if ((kFull || k < rows) && in_bounds<kChkResidual>(p, sizeof(T))) raw[k] = *p;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) res[k] = to_float(raw[k]);
+        }
+    }
+    if (e.z != nullptr) {
+        T* p = static_cast<T*>(e.z) + row * e.ldz + col;
+#pragma unroll
+        for (int k = 0; k < 8; ++k, p += e.ldz)
+            if ((kFull || k < rows) && in_bounds<kChkZ>(p, sizeof(T))) *p = from_float<T>(y[k]);
+    }
     activate(y, e.act);
+    if (e.out_f32) {
+        float* p = static_cast<float*>(out) + row * e.ldo + col;
 #pragma unroll
-    for (int p = 0; p < 8; ++p)
-        if (kFull || p < rows) store_y1<T>(e, out, row + p, col, y[p] + res[p]);
+        for (int k = 0; k < 8; ++k, p += e.ldo)
+            if ((kFull || k < rows) && in_bounds_role(e.role, p, 4)) *p = y[k] + res[k];
+    } else {
+        T* p = static_cast<T*>(out) + row * e.ldo + col;
+#pragma unroll
+        for (int k = 0; k < 8; ++k, p += e.ldo)
+            if ((kFull || k < rows) && in_bounds_role(e.role, p, sizeof(T))) *p = from_float<T>(y[k] + res[k]);
+    }
 }
 
 // ---------------------------------------------------------------------------------------
@@ -349,10 +374,18 @@ struct Gemm {
     int cluster;          // blocks that share a tile's K (their shares meet in shared memory), or 1
     int kblocks, kblocks_per_split;
     int mt, nt;
+    int blocks;           // blocks (or pairs) that take turns at the tiles of a split
     uint32_t idesc, tmem_columns;
     Epilogue e;
     int64_t split_stride; // elements of fp32 output from one split to the next
     int* status;
+};
+
+// One launch computes one product or two that do not depend on each other (dx and dW): blocks from
+// `second` on take the second.
+struct Gemms {
+    Gemm of[2];
+    int second;
 };
 
 __host__ __device__ constexpr size_t gemm_smem(int stage_bytes_in_all) {
@@ -480,7 +513,10 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 template <typename T, bool kPair, bool kVectors>
-__global__ void __launch_bounds__(kThreads, kPair ? 1 : 2) gemm_kernel(const __grid_constant__ Gemm g) {
+__global__ void __launch_bounds__(kThreads, kPair ? 1 : 2) gemm_kernel(const __grid_constant__ Gemms list) {
+    const int which = (int)blockIdx.x >= list.second;
+    const Gemm& g = list.of[which];
+    const int block = (int)blockIdx.x - (which ? list.second : 0);
     extern __shared__ uint8_t raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     const int kept = g.resident ? g.kblocks * g.b.bytes : 0;
@@ -494,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, kPair ? 1 : 2) gemm_kernel(const __g
     // barriers: full[stage], empty[stage], accumulator done[2], accumulator free[2], B staged, drain
     const uint32_t full = bar0, empty = bar0 + 8 * kMaxStages, done = empty + 8 * kMaxStages, room = done + 16, bfull = room + 16,
                    drain = bfull + 8;
-    const uint32_t rank = kPair ? blockIdx.x & 1u : 0u;
+    const uint32_t rank = kPair ? block & 1u : 0u;
     if (threadIdx.x == 32 * (kOutWarps + 1)) {
         abort_flag = 0;
         for (int s = 0; s < g.stages; ++s) {
@@ -523,9 +559,11 @@ __global__ void __launch_bounds__(kThreads, kPair ? 1 : 2) gemm_kernel(const __g
     __syncthreads();
     if (kPair) cluster_sync();  // the other block's barriers and tensor memory are there
     mlp::fence_after();
+    after_previous_kernel();
     const uint32_t tmem = *tslot;
-    const int first = kPair ? blockIdx.x >> 1 : blockIdx.x, step = kPair ? gridDim.x >> 1 : gridDim.x;
-    const int kb0 = blockIdx.y * g.kblocks_per_split, kbs = max(0, min(g.kblocks_per_split, g.kblocks - kb0));
+    const int first = kPair ? block >> 1 : g.cluster > 1 ? block / g.cluster : block % g.blocks, step = g.blocks;
+    const int part = kPair ? 0 : g.cluster > 1 ? block % g.cluster : block / g.blocks;  // of K
+    const int kb0 = part * g.kblocks_per_split, kbs = max(0, min(g.kblocks_per_split, g.kblocks - kb0));
 
     if (warp == kOutWarps + 1) {
         // ------------------------------- TMA copies -------------------------------
@@ -621,8 +659,8 @@ __global__ void __launch_bounds__(kThreads, kPair ? 1 : 2) gemm_kernel(const __g
         // -------------------------------- way out ---------------------------------
         const int quarter = warp & 3, chunks = (g.bn + 31) / 32;
         float4* st = reinterpret_cast<float4*>(staging + warp * 4096);
-        const Epilogue& e = g.e;
-        void* out = g.split_stride != 0 ? static_cast<float*>(e.out) + blockIdx.y * g.split_stride : e.out;
+        const Epilogue e = g.e;  // in registers: read through the chosen product, each store would make it suspect
+        void* out = g.split_stride != 0 ? static_cast<float*>(e.out) + part * g.split_stride : e.out;
         uint32_t i = 0;
         for (Tiles t(g, first, step); t.more(); t.next(), ++i) {
             const int64_t m0 = (int64_t)(kPair ? 2 * t.m + (int)rank : t.m) * kBm + 32 * quarter;
@@ -707,11 +745,11 @@ __global__ void __launch_bounds__(kThreads, kPair ? 1 : 2) gemm_kernel(const __g
         // K is split over the cluster's blocks: their shares of the tile are added in rank order, every block
         // writing out the rows of its turn.
         cluster_sync();
-        const int chunks = (g.bn + 31) / 32, quarters = (int)min((int64_t)4, (g.M - (int64_t)(blockIdx.x / g.nt) * kBm + 31) / 32);
-        const int64_t tm = (int64_t)(blockIdx.x / g.nt) * kBm;
-        const int tn = (int)(blockIdx.x % g.nt) * g.bn, cols = (int)min(g.N, (int64_t)tn + g.bn);
+        const int chunks = (g.bn + 31) / 32, quarters = (int)min((int64_t)4, (g.M - (int64_t)(first / g.nt) * kBm + 31) / 32);
+        const int64_t tm = (int64_t)(first / g.nt) * kBm;
+        const int tn = (first % g.nt) * g.bn, cols = (int)min(g.N, (int64_t)tn + g.bn);
         if (warp < kOutWarps && abort_flag == 0)
-            for (int u = warp * g.cluster + blockIdx.y; u < quarters * chunks * 4; u += kOutWarps * g.cluster) {
+            for (int u = warp * g.cluster + part; u < quarters * chunks * 4; u += kOutWarps * g.cluster) {
                 const int chunk = u >> 2, r = 8 * (u & 3) + (lane >> 2);  // chunk = quarter * chunks + column chunk
                 const int64_t row = tm + 32 * (chunk / chunks) + r;
                 const int col = tn + 32 * (chunk % chunks) + 8 * (lane & 3);
@@ -833,6 +871,7 @@ __global__ void __launch_bounds__(256) realign_kernel(const __grid_constant__ Re
     constexpr int kAtOnce = 4;
     const int64_t i0 = (int64_t)blockIdx.x * (256 * kAtOnce) + threadIdx.x;
     Chunk c[kAtOnce];
+    after_previous_kernel();
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
         const int64_t i = i0 + 256 * u;
@@ -933,6 +972,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
     mlp::fence_before();
     __syncthreads();
     mlp::fence_after();
+    after_previous_kernel();
     const uint32_t tmem = *tslot;
     const int tiles = (int)((g.rows + kBm - 1) / kBm);
     const int mine = (tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1;  // at least one: the grid has no more blocks than tiles
@@ -1149,12 +1189,13 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
 template <typename T, bool kVectors>
 __global__ void __launch_bounds__(256) slope_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ z,
                                                     int64_t rows, int cols, int act, T* __restrict__ dz, int64_t lddz,
-                                                    float* __restrict__ sums) {
+                                                    float* __restrict__ sums, int role) {
     __shared__ float part[32][65];
     const int col = blockIdx.x * 64 + 8 * (threadIdx.x & 7), r = threadIdx.x >> 3;
     const int64_t share = (rows + gridDim.y - 1) / gridDim.y, r0 = blockIdx.y * share, r1 = min(rows, r0 + share);
     const int n = min(8, cols - col);
     float s[8] = {};
+    after_previous_kernel();
     if (n > 0) {
 #pragma unroll 2
         for (int64_t row = r0 + r; row < r1; row += 32) {
@@ -1192,7 +1233,7 @@ __global__ void __launch_bounds__(256) slope_kernel(const T* __restrict__ dy, in
     if (threadIdx.x < 64 && c < cols) {
         float t = 0.f;
         for (int k = 0; k < 32; ++k) t += part[k][threadIdx.x];
-        if (in_bounds<kChkWork>(sums + (int64_t)blockIdx.y * cols + c, 4)) sums[(int64_t)blockIdx.y * cols + c] = t;
+        if (in_bounds_role(role, sums + (int64_t)blockIdx.y * cols + c, 4)) sums[(int64_t)blockIdx.y * cols + c] = t;
     }
 }
 
@@ -1218,6 +1259,7 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const __grid_constant__ 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t i = (int64_t)(second ? blockIdx.x - l.blocks0 : blockIdx.x) * 32 + lane;
     float v = 0.f;
+    after_previous_kernel();
     if (i < s.n) {
 #pragma unroll 8
         for (int p = warp; p < s.count; p += 8) {
