@@ -722,8 +722,10 @@ struct Plan {
     bool pair;    // 256-row tiles by pairs of SMs
 };
 
-// The width of N's column tiles, at most `most`: a multiple of 16.
-int wide_tile(int64_t N, int most) { return ceil_div(ceil_div(N, ceil_div(N, most)), 16) * 16; }
+// The width of N's column tiles where they are nt: a multiple of 16, or, where there are several, of the 32 columns
+// that a store takes (it knows the array's end, not the tile's).
+int tile_width(int64_t N, int64_t nt) { return nt == 1 ? ceil_div(N, 16) * 16 : ceil_div(ceil_div(N, nt), 32) * 32; }
+int wide_tile(int64_t N, int most) { return tile_width(N, ceil_div(N, most)); }
 
 // Where 256 x 256 tiles by pairs of SMs occupy the device and K is long: those. Else 128-row tiles of up to
 // 128 columns, two blocks a SM, since with few steps of K what counts is how many warps write out: as few
@@ -737,7 +739,7 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int sms) {
     if (N >= 160 && (int64_t)ceil_div(M, 256) * nt >= sms / 2 && K >= 512) return Plan{wide, 1, 1, true};
     nt = ceil_div(N, 128);
     while (mt * nt < sms && ceil_div(N, nt) > 64) ++nt;
-    Plan p{ceil_div(ceil_div(N, nt), 16) * 16, 1, 1, false};
+    Plan p{tile_width(N, nt), 1, 1, false};
     const int64_t tiles = mt * ceil_div(N, p.bn);
     while (p.cluster < 8 && tiles * p.cluster * 2 <= 2 * sms && 4 * p.cluster * hg::linear::kBk <= K) p.cluster *= 2;
     return p;
@@ -753,6 +755,21 @@ int set_map(CUtensorMap& map, const Array& a, int box_rows, const char* what) {
                                          : encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(a.p), dims, strides, box, ones,
                                                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(HASHGRID_ERR_CUDA, "%s: encoding a tensor map failed (%d)", what, (int)r);
+    return ok();
+}
+
+// The map of an output of `parts` row-major [rows, cols] arrays, stored in chunks of 32 x 32.
+int set_store_map(CUtensorMap& map, void* p, int64_t rows, int64_t cols, int64_t ld, int parts, bool f32, const char* what) {
+    const cuuint64_t elem = f32 ? 4 : 2;
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * elem, (cuuint64_t)(parts > 1 ? rows * ld : ld) * elem};
+    const cuuint32_t box[3] = {32, 32, 1}, ones[3] = {1, 1, 1};
+    PFN_tensorMapEncodeTiled encode = tensor_map_fn();
+    const CUresult r = encode == nullptr ? CUDA_ERROR_NOT_SUPPORTED
+                                         : encode(&map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, p, dims, strides, box,
+                                                  ones, CU_TENSOR_MAP_INTERLEAVE_NONE, f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                                                  CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(HASHGRID_ERR_CUDA, "%s: encoding a tensor map failed (%d)", what, (int)r);
     return ok();
 }
@@ -813,7 +830,8 @@ int set_product(Product& p, bool half, const Array& A, const Array& B, int64_t M
     // reads 128 rows (two boxes) of A whatever the product has: the staging area behind the stages keeps that in bounds.
     const int per_sm = group == 1 && g.tmem_columns <= 256 ? 2 : 1;
     const int budget = (per_sm == 2 ? 113 : 227) * 1024 - 1024;  // less what the kernel has of its own
-    g.stages = std::min(hl::kMaxStages, (budget - kept - (int)hl::gemm_smem(0)) / g.stage_bytes);
+    const bool two = e.out_f32 && e.z != nullptr;
+    g.stages = std::min(hl::kMaxStages, (budget - kept - (int)hl::gemm_smem(0, two)) / g.stage_bytes);
     if (g.cluster > 1)  // a split product's shares lie in the stages
         while (g.stages * g.stage_bytes < 4 * ceil_div(bn, 32) * 4096) ++g.stages;
     const uint32_t type = half ? 0u : 1u;
@@ -822,9 +840,15 @@ int set_product(Product& p, bool half, const Array& A, const Array& B, int64_t M
     g.e = e;
     const size_t os = e.out_f32 ? 4 : 2;
     g.split_stride = plan.splits > 1 ? M * N : 0;
-    p.vectors = N % 8 == 0 && vector_rows(e.out, e.ldo, os) && vector_rows(e.residual, e.ldr, os) && vector_rows(e.z, e.ldz, 2);
+    // TMA writes whole 16-byte units: a last one that the product fills in part would take the caller's values behind it along.
+    p.vectors = N * os % 16 == 0 && vector_rows(e.out, e.ldo, os) && vector_rows(e.residual, e.ldr, os) && vector_rows(e.z, e.ldz, 2);
+    if (p.vectors) {
+        if (int rc = set_store_map(g.ty, e.out, M, N, e.ldo, plan.splits, e.out_f32 != 0, what)) return rc;
+        if (e.z != nullptr)
+            if (int rc = set_store_map(g.tz, e.z, M, N, e.ldz, 1, false, what)) return rc;
+    }
     g.status = status;
-    p.smem = hl::gemm_smem(g.stages * g.stage_bytes + kept);
+    p.smem = hl::gemm_smem(g.stages * g.stage_bytes + kept, two);
     g.blocks = (int)(plan.cluster > 1 ? tiles : std::min<int64_t>(tiles, std::max(1, per_sm * sms / splits / group)));
     p.grid = (int64_t)g.blocks * splits * group;
     return ok();
@@ -976,6 +1000,8 @@ int launch_narrow_backward(const hashgrid_linear_s* l, const Array& dy, const Ar
     g.id_dx = id;
     g.id_dw = id | (1u << 15);
     g.e = hl::Epilogue{nullptr, nullptr, dx, nullptr, 0, lddx, 0, dx_dtype == HASHGRID_F32, hl::kNoAct, hg::kChkOut};
+    if (dx != nullptr)
+        if (int rc = set_store_map(g.tdx, dx, N, l->in, lddx, 1, dx_dtype == HASHGRID_F32, what)) return rc;
     g.parts = reinterpret_cast<float*>(work);
     g.want_db = db != nullptr;
     g.status = status;

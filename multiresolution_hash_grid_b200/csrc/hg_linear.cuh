@@ -347,10 +347,12 @@ __device__ __forceinline__ void emit_column8(const Epilogue& e, void* out, int64
 // halves the shared-memory reads of B per MMA and leaves room for more stages; the first block
 // issues the MMAs of both, and each writes out its own 128 rows.
 //
-// Way out: a 32 x 32 chunk goes from TMEM (a lane holds a row) through 4 KB of shared memory a
-// warp, so that four neighbouring lanes then hold 32 neighbouring columns of a row: bias,
-// residual, z and y move in whole 16-byte vectors and 64-byte row pieces. Every value stays
-// fp32 until it is stored.
+// Way out: a lane reads 32 columns of its row from TMEM, adds bias, applies the activation and adds
+// the residual in fp32, and rounds. Where rows begin on 16-byte boundaries (kVectors) the chunk of 32 x 32
+// goes to 4 KB of shared memory a warp, and from there by TMA, which also keeps to the array's bounds: a
+// third of the instructions that 16-byte stores with their addresses and guards took (2^20 x 32 ->
+// 64: 71 us with those). Otherwise it passes through shared memory as fp32, and a lane takes
+// a column, so that a warp still writes 32 neighbours at a time.
 // ---------------------------------------------------------------------------------------
 constexpr int kBm = 128, kBk = 64;
 constexpr int kOutWarps = 8;
@@ -365,7 +367,7 @@ struct Side {             // one operand's share of a stage: `boxes` boxes of bo
 };
 
 struct Gemm {
-    CUtensorMap ta, tb;
+    CUtensorMap ta, tb, ty, tz;
     Side a, b;
     int64_t M, N;
     int bn, columns;      // tile width; columns from one accumulator to the next
@@ -388,8 +390,8 @@ struct Gemms {
     int second;
 };
 
-__host__ __device__ constexpr size_t gemm_smem(int stage_bytes_in_all) {
-    return 1024 + (size_t)stage_bytes_in_all + kStaging + (2 * kMaxStages + 6) * 8 + 16;
+__host__ __device__ constexpr size_t gemm_smem(int stage_bytes_in_all, bool two = false) {
+    return 1024 + (size_t)stage_bytes_in_all + (two ? 2 : 1) * kStaging + (2 * kMaxStages + 6) * 8 + 16;
 }
 
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
@@ -470,6 +472,28 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// Stores a chunk from shared memory; the thread then commits its stores as a group.
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map), "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// A lane's row of a chunk (32 values) into the warp's 4 KB: 16-bit rows of 64 bytes, whose 16-byte units are
+// exchanged by (row / 2) % 4 (the 64-byte swizzle), fp32 rows of 128 bytes, by row % 8.
+template <typename T>
+__device__ __forceinline__ void stage_row16(uint8_t* st, int lane, const float (&y)[32]) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(st + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) = pack8<T>(y + 8 * u);
+}
+__device__ __forceinline__ void stage_row32(uint8_t* st, int lane, const float (&y)[32]) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+        *reinterpret_cast<float4*>(st + lane * 128 + ((u ^ (lane & 7)) << 4)) = make_float4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
+}
+
 // Position in a ring of stages.
 struct Ring {
     int stage = 0;
@@ -521,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, kPair ? 1 : 2) gemm_kernel(const __g
     uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     const int kept = g.resident ? g.kblocks * g.b.bytes : 0;
     uint8_t* staging = sm + (size_t)g.stages * g.stage_bytes + kept;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kStaging);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(staging + (g.e.out_f32 && g.e.z != nullptr ? 2 : 1) * kStaging);  // fp32 y and z side by side
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 6);
     __shared__ volatile int abort_flag;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // the shuffle tells the compiler that it is uniform
@@ -669,14 +693,15 @@ __global__ void __launch_bounds__(kThreads, kPair ? 1 : 2) gemm_kernel(const __g
             bool waited = kbs == 0;
             for (int c = warp >> 2; c < chunks && rows > 0; c += 2) {
                 __syncwarp();
-                const int c0 = n0 + 32 * c, col = c0 + 8 * (lane & 3);
-                // bias and residual are on their way while the accumulator is waited for and read
-                const bool whole = kVectors && col < cols;  // cols is a multiple of 8 then
+                const int c0 = n0 + 32 * c;
+                // a 16-bit residual is on its way while the accumulator is waited for and read
                 uint4 q[4] = {};
-                float b[8];
-                if (whole && g.cluster == 1) {
-                    bias8(e, col, b);
-                    if (e.residual != nullptr && !e.out_f32) load_residuals<T, 4>(e, m0 + (lane >> 2), g.M, col, q);
+                const bool inside = c0 + 32 <= cols;
+                if (kVectors && g.cluster == 1 && e.residual != nullptr && !e.out_f32 && inside && lane < rows) {
+                    const T* p = static_cast<const T*>(e.residual) + (m0 + lane) * e.ldr + c0;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (in_bounds<kChkResidual>(p + 8 * u, 16)) q[u] = *reinterpret_cast<const uint4*>(p + 8 * u);
                 }
                 __syncwarp();
                 if (!waited) {
@@ -692,6 +717,63 @@ __global__ void __launch_bounds__(kThreads, kPair ? 1 : 2) gemm_kernel(const __g
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = 0u;
                 }
+                if (kVectors && g.cluster == 1) {
+                    float y[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(v[j]);
+                    if (e.bias != nullptr) {
+                        if (inside) {
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) {
+                                const float4 b = in_bounds<kChkBias>(e.bias + c0 + 4 * u, 16) ? __ldg(reinterpret_cast<const float4*>(e.bias + c0) + u)
+                                                                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+                                y[4 * u] += b.x; y[4 * u + 1] += b.y; y[4 * u + 2] += b.z; y[4 * u + 3] += b.w;
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (c0 + j < cols) y[j] += bias1(e, c0 + j);
+                        }
+                    }
+                    uint8_t* sy = staging + warp * 4096;  // y, and 16-bit z behind it
+                    uint8_t* sz = e.out_f32 ? staging + (kOutWarps + warp) * 4096 : sy + 2048;
+                    if (lane == 0) store_wait_read();  // the last chunk has left
+                    __syncwarp();
+                    if (e.z != nullptr) stage_row16<T>(sz, lane, y);
+                    activate(y, e.act);
+                    if (e.residual != nullptr) {
+                        if (inside && !e.out_f32) {
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const float2 r0 = unpack2<T>(q[u].x), r1 = unpack2<T>(q[u].y), r2 = unpack2<T>(q[u].z), r3 = unpack2<T>(q[u].w);
+                                y[8 * u] += r0.x; y[8 * u + 1] += r0.y; y[8 * u + 2] += r1.x; y[8 * u + 3] += r1.y;
+                                y[8 * u + 4] += r2.x; y[8 * u + 5] += r2.y; y[8 * u + 6] += r3.x; y[8 * u + 7] += r3.y;
+                            }
+                        } else if (inside && lane < rows) {
+                            const float* p = static_cast<const float*>(e.residual) + (m0 + lane) * e.ldr + c0;
+#pragma unroll
+                            for (int u = 0; u < 8; ++u)
+                                if (in_bounds<kChkResidual>(p + 4 * u, 16)) {
+                                    const float4 r = *reinterpret_cast<const float4*>(p + 4 * u);
+                                    y[4 * u] += r.x; y[4 * u + 1] += r.y; y[4 * u + 2] += r.z; y[4 * u + 3] += r.w;
+                                }
+                        } else if (lane < rows) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (c0 + j < cols) y[j] += residual1<T>(e, m0 + lane, c0 + j);
+                        }
+                    }
+                    if (e.out_f32) stage_row32(sy, lane, y);
+                    else stage_row16<T>(sy, lane, y);
+                    mlp::fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && c0 < cols) {
+                        if (e.z != nullptr) tma_store(&g.tz, (uint32_t)__cvta_generic_to_shared(sz), c0, (int)m0, 0);
+                        tma_store(&g.ty, (uint32_t)__cvta_generic_to_shared(sy), c0, (int)m0, part);
+                        store_commit();
+                    }
+                    continue;
+                }
                 // a split product leaves its share in the stages' memory, where the cluster's other blocks read it
                 if (g.cluster > 1) st = reinterpret_cast<float4*>(sm + (quarter * chunks + c) * 4096);
                 __syncwarp();
@@ -701,18 +783,7 @@ __global__ void __launch_bounds__(kThreads, kPair ? 1 : 2) gemm_kernel(const __g
                                                        __uint_as_float(v[4 * u + 2]), __uint_as_float(v[4 * u + 3]));
                 if (g.cluster > 1) continue;
                 __syncwarp();
-                if (whole) {
-                    float y[4][8];
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        const int r = 8 * p + (lane >> 2);
-                        const float4 lo = st[unit_of(r, 2 * (lane & 3))], hi = st[unit_of(r, 2 * (lane & 3) + 1)];
-                        y[p][0] = lo.x + b[0]; y[p][1] = lo.y + b[1]; y[p][2] = lo.z + b[2]; y[p][3] = lo.w + b[3];
-                        y[p][4] = hi.x + b[4]; y[p][5] = hi.y + b[5]; y[p][6] = hi.z + b[6]; y[p][7] = hi.w + b[7];
-                    }
-                    emit_vectors<T, 4>(e, out, m0 + (lane >> 2), g.M, col, y, q);
-                } else if (!kVectors && c0 + lane < cols) {
-                    // a lane holds a column, so that a warp writes 32 neighbours whatever their alignment
+                if (!kVectors && c0 + lane < cols) {
                     const float* sf = reinterpret_cast<const float*>(st);
                     const float bias = bias1(e, c0 + lane);
 #pragma unroll 1
@@ -738,7 +809,8 @@ __global__ void __launch_bounds__(kThreads, kPair ? 1 : 2) gemm_kernel(const __g
                 }
             }
         }
-    out_of_time:;
+    out_of_time:
+        if (kVectors && lane == 0) store_wait();
     }
     __syncwarp();
     if (!kPair && g.cluster > 1) {
@@ -762,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, kPair ? 1 : 2) gemm_kernel(const __g
                     y[0][0] += a.x; y[0][1] += a.y; y[0][2] += a.z; y[0][3] += a.w;
                     y[0][4] += b.x; y[0][5] += b.y; y[0][6] += b.z; y[0][7] += b.w;
                 }
-                if (kVectors) {
+                if (kVectors && col + 8 <= cols) {
                     float b[8];
                     uint4 q[1] = {};
                     if (g.e.residual != nullptr && !g.e.out_f32) load_residuals<T, 1>(g.e, row, row + 1, col, q);
@@ -914,7 +986,7 @@ constexpr int kNarrowStages = 4;
 constexpr int kBox = kBm * 128;  // bytes of a box of 128 rows x 64 columns
 
 struct Narrow {
-    CUtensorMap tdy, tz, tx, tw;
+    CUtensorMap tdy, tz, tx, tw, tdx;
     int64_t rows;
     int in, out, act;
     int boxes_in, boxes_out, columns;  // 64-wide boxes of x and of dy (and z); columns from one accumulator to the next
@@ -1047,40 +1119,36 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
     } else if (warp < 8) {
         // ---------------------------------- dx -----------------------------------
         const int quarter = warp & 3, chunks = (g.in + 31) / 32;
-        float4* st = reinterpret_cast<float4*>(staging + warp * 4096);
+        uint8_t* st = staging + warp * 4096;
         for (int i = 0; i < mine && dx; ++i) {
             const int b = i & 1;
-            const int64_t m0 = (blockIdx.x + (int64_t)i * gridDim.x) * kBm + 32 * quarter;
+            const int m0 = (int)(blockIdx.x + i * gridDim.x) * kBm + 32 * quarter;
             const bool ok = wait_bounded(done + 8 * b, (i >> 1) & 1u, &abort_flag);
             if (__any_sync(0xffffffffu, !ok)) break;
             mlp::fence_after();
             for (int c = warp >> 2; c < chunks; c += 2) {
-                const int col = 32 * c + 8 * (lane & 3);
                 uint32_t v[32];
                 __syncwarp();
                 tmem_ld32(tmem + ((uint32_t)(32 * quarter) << 16) + b * g.columns + 32 * c, v);
+                float y[32];
 #pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    st[unit_of(lane, u)] = make_float4(__uint_as_float(v[4 * u]), __uint_as_float(v[4 * u + 1]),
-                                                       __uint_as_float(v[4 * u + 2]), __uint_as_float(v[4 * u + 3]));
+                for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(v[j]);
+                if (lane == 0) store_wait_read();  // the last chunk has left
                 __syncwarp();
-                if (col < g.in) {
-                    float y[4][8];
-                    const uint4 q[4] = {};
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        const int r = 8 * p + (lane >> 2);
-                        const float4 lo = st[unit_of(r, 2 * (lane & 3))], hi = st[unit_of(r, 2 * (lane & 3) + 1)];
-                        y[p][0] = lo.x; y[p][1] = lo.y; y[p][2] = lo.z; y[p][3] = lo.w;
-                        y[p][4] = hi.x; y[p][5] = hi.y; y[p][6] = hi.z; y[p][7] = hi.w;
-                    }
-                    emit_vectors<T, 4>(g.e, g.e.out, m0 + (lane >> 2), g.rows, col, y, q);
+                if (g.e.out_f32) stage_row32(st, lane, y);
+                else stage_row16<T>(st, lane, y);
+                mlp::fence_async_smem();
+                __syncwarp();
+                if (lane == 0 && m0 < g.rows) {
+                    tma_store(&g.tdx, (uint32_t)__cvta_generic_to_shared(st), 32 * c, m0, 0);
+                    store_commit();
                 }
             }
             mlp::fence_before();
             __syncwarp();
             if (lane == 0) mlp::mbar_arrive(room + 8 * b);
         }
+        if (lane == 0) store_wait();
     } else {
         // --------------------------- dz, and dW's and db's sums ---------------------------
         const int tt = threadIdx.x - 32 * 10, quarter = warp & 3, half = (warp - 10) >> 2;
