@@ -455,8 +455,9 @@ class Linear:
         elif ldx % 8 or self.in_features % 8:
             size = lib.hashgrid_linear_forward_workspace(self.handle, N, ldx)
             workspace = self._scratch(size, x.device, stream)
-        hashgrid_linear_forward(self.handle, x.data_ptr(), ldx, N, w.data_ptr(), b, residual, ldr, y.data_ptr(), ldy,
-                                y_dtype, z, workspace, size, device_status, stream)
+        _check(lib.hashgrid_linear_forward(self.handle, x.data_ptr(), ldx, N, w.data_ptr(), None if b is None else b.data_ptr(),
+                                           None if residual is None else residual.data_ptr(), ldr, y.data_ptr(), ldy, y_dtype,
+                                           _ptr(z), _ptr(workspace), size, _ptr(device_status), _stream(stream)))
         return y
 
     def workspace(self, N: int, device, lddy: int | None = None, ldx: int | None = None):

@@ -722,24 +722,34 @@ struct Plan {
     bool pair;    // 256-row tiles by pairs of SMs
 };
 
-// The width of N's column tiles where they are nt: a multiple of 16, or, where there are several, of the 32 columns
-// that a store takes (it knows the array's end, not the tile's).
-int tile_width(int64_t N, int64_t nt) { return nt == 1 ? ceil_div(N, 16) * 16 : ceil_div(ceil_div(N, nt), 32) * 32; }
+// The width of N's column tiles where they are nt: a multiple of 16, or, where there are several that may leave by TMA
+// stores, of the 32 columns of a store (which knows the array's end, not the tile's).
+int tile_width(int64_t N, int64_t nt) {
+    const int unit = nt > 1 && N % 4 == 0 ? 32 : 16;
+    return ceil_div(ceil_div(N, nt), unit) * unit;
+}
 int wide_tile(int64_t N, int most) { return tile_width(N, ceil_div(N, most)); }
 
 // Where 256 x 256 tiles by pairs of SMs occupy the device and K is long: those. Else 128-row tiles of up to
-// 128 columns, two blocks a SM, since with few steps of K what counts is how many warps write out: as few
-// column tiles as there can be while every SM has one, then narrower ones, down to 64 columns, and
-// if those are still too few, a split of K over up to 8 blocks of a cluster, each with two 64-wide
-// steps at least.
+// 128 columns, two blocks a SM, since with few steps of K what counts is how many warps write out. The
+// number of column tiles is the one that costs least in rounds of the device times a tile's width (and
+// 24 columns' worth of what a tile costs anyway), down to 64 columns; if the tiles are still fewer than the SMs, K is
+// split over up to 8 blocks of a cluster, each with two 64-wide steps at least.
 Plan make_plan(int64_t M, int64_t N, int64_t K, int sms) {
     const int64_t mt = ceil_div(M, hg::linear::kBm);
-    int64_t nt = ceil_div(N, 256);
-    const int wide = ceil_div(ceil_div(N, nt), 32) * 32;
-    if (N >= 160 && (int64_t)ceil_div(M, 256) * nt >= sms / 2 && K >= 512) return Plan{wide, 1, 1, true};
-    nt = ceil_div(N, 128);
-    while (mt * nt < sms && ceil_div(N, nt) > 64) ++nt;
-    Plan p{tile_width(N, nt), 1, 1, false};
+    const int64_t pairs = ceil_div(N, 256);
+    if (N >= 160 && (int64_t)ceil_div(M, 256) * pairs >= sms / 2 && K >= 512)
+        return Plan{ceil_div(ceil_div(N, pairs), 32) * 32, 1, 1, true};
+    int64_t best = INT64_MAX;
+    Plan p{0, 1, 1, false};
+    for (int64_t nt = ceil_div(N, 128); nt <= ceil_div(N, 64); ++nt) {
+        const int bn = tile_width(N, nt);
+        const int64_t tiles = mt * ceil_div(N, bn), cost = (tiles + 2 * sms - 1) / (2 * sms) * (bn + 24);
+        if (cost < best) {
+            best = cost;
+            p.bn = bn;
+        }
+    }
     const int64_t tiles = mt * ceil_div(N, p.bn);
     while (p.cluster < 8 && tiles * p.cluster * 2 <= 2 * sms && 4 * p.cluster * hg::linear::kBk <= K) p.cluster *= 2;
     return p;
@@ -798,7 +808,7 @@ struct Product {
     hg::linear::Gemm g;
     int64_t grid;  // blocks
     size_t smem;
-    bool vectors;
+    bool vectors, gather;
 };
 
 int set_product(Product& p, bool half, const Array& A, const Array& B, int64_t M, int64_t N, int64_t K, const hg::linear::Epilogue& e,
@@ -828,7 +838,8 @@ int set_product(Product& p, bool half, const Array& A, const Array& B, int64_t M
     g.cluster = plan.cluster;
     // Two blocks a SM where tensor memory and shared memory allow: one's loads and stores then fill the other's gaps. The MMA
     // reads 128 rows (two boxes) of A whatever the product has: the staging area behind the stages keeps that in bounds.
-    const int per_sm = group == 1 && g.tmem_columns <= 256 ? 2 : 1;
+    p.gather = e.out_f32 && g.kblocks_per_split > hl::kSegment;
+    const int per_sm = group == 1 && g.tmem_columns <= 256 && !p.gather ? 2 : 1;
     const int budget = (per_sm == 2 ? 113 : 227) * 1024 - 1024;  // less what the kernel has of its own
     const bool two = e.out_f32 && e.z != nullptr;
     g.stages = std::min(hl::kMaxStages, (budget - kept - (int)hl::gemm_smem(0, two)) / g.stage_bytes);
@@ -865,8 +876,12 @@ int launch_products(const Product* p, int count, const Plan& plan, const char* w
     const int64_t grid = p[0].grid + (count > 1 ? p[1].grid : 0);
     const size_t smem = std::max(p[0].smem, p[count - 1].smem);
     const bool vectors = p[0].vectors && p[count - 1].vectors;
-    auto k = plan.pair ? (vectors ? hl::gemm_kernel<T, true, true> : hl::gemm_kernel<T, true, false>)
-                       : (vectors ? hl::gemm_kernel<T, false, true> : hl::gemm_kernel<T, false, false>);
+    const bool gather = p[0].gather || p[count - 1].gather;
+    static void (*const kernels[8])(const hl::Gemms) = {
+        hl::gemm_kernel<T, false, false, false>, hl::gemm_kernel<T, false, false, true>, hl::gemm_kernel<T, false, true, false>,
+        hl::gemm_kernel<T, false, true, true>,   hl::gemm_kernel<T, true, false, false>, hl::gemm_kernel<T, true, false, true>,
+        hl::gemm_kernel<T, true, true, false>,   hl::gemm_kernel<T, true, true, true>};
+    auto k = kernels[4 * plan.pair + 2 * vectors + gather];
     if (int rc = prepare_smem_once(k, smem)) return rc;
     return launch_after(k, dim3((unsigned)grid), hl::kThreads, smem, plan.pair ? 2 : plan.cluster, s, what, l);
 }
@@ -1168,6 +1183,11 @@ int launch_adamw(const hashgrid_adamw_s* o, const hashgrid_adamw_s::Launch& l, h
     list.count = (uint32_t)l.count;
     list.blocks = l.blocks;
     std::memcpy(list.t, o->tensors.data() + l.begin, sizeof(hg::adamw::Tensor) * l.count);
+    for (int i = 0; i < l.count; ++i) {
+        const float lr_scale = list.t[i].rate, decay = list.t[i].keep;
+        list.t[i].rate = lr_scale * a.lr;
+        list.t[i].keep = (float)(1.0 - (double)lr_scale * (double)a.lr * (double)decay);
+    }
     const unsigned blocks = (l.blocks + hg::adamw::kWarps - 1) / hg::adamw::kWarps;
     return launch_after(hg::adamw::step_kernel<kCap>, dim3(blocks), 32 * hg::adamw::kWarps, 0, 1, s, "adamw_step", list, a);
 }
@@ -1685,8 +1705,8 @@ int hashgrid_adamw_create(const hashgrid_adamw_tensor* tensors, int count, hashg
                 d.first = first;
                 d.types = (uint32_t)t.param_dtype | (uint32_t)t.grad_dtype << 4 | (uint32_t)t.state_dtype << 8 |
                           (uint32_t)(t.copy ? t.copy_dtype : (int)hg::adamw::kNone) << 12 | (uint32_t)k << 16;
-                d.lr_scale = t.lr_scale;
-                d.decay = t.weight_decay;
+                d.rate = t.lr_scale;
+                d.keep = t.weight_decay;
                 o->tensors.push_back(d);
                 first += (uint32_t)blocks_of(t.n);
             }

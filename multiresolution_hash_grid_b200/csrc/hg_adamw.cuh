@@ -47,7 +47,7 @@ struct Tensor {
     int64_t n;
     uint32_t first;   // index of the tensor's first 256-element block in the launch
     uint32_t types;   // param | grad << 4 | state << 8 | copy << 12 | place in the caller's list << 16
-    float lr_scale, decay;
+    float rate, keep;  // lr * lr_scale, 1 - rate * weight_decay (in the handle: lr_scale and weight_decay)
 };
 
 struct Params {
@@ -273,7 +273,7 @@ __device__ __forceinline__ void encode(const float2 (&x)[4], const uint32_t (&h)
 }
 
 struct Rates {
-    float c1, root2, rate, keep;  // 1/(1-b1^t), sqrt(1/(1-b2^t)), lr * lr_scale, 1 - rate * decay
+    float c1, root2;  // 1/(1-b1^t), sqrt(1/(1-b2^t))
     uint32_t step;
 };
 
@@ -320,7 +320,7 @@ __device__ __forceinline__ void step_block(const Tensor& T, const Params& a, con
         root[k] = make_float2(square_root(v[k].x), square_root(v[k].y));
         const float2 d = add2(mul2(root[k], both(r.root2)), both(a.eps)), s = mul2(m[k], both(r.c1));
         // the quotient alone is not correctly rounded (2 ulp of a step): a division in full costs a tenth of an 8-bit step
-        p[k] = sub2(mul2(p[k], both(r.keep)), mul2(both(r.rate), mul2(s, make_float2(reciprocal(d.x), reciprocal(d.y)))));
+        p[k] = sub2(mul2(p[k], both(T.keep)), mul2(both(T.rate), mul2(s, make_float2(reciprocal(d.x), reciprocal(d.y)))));
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -366,15 +366,6 @@ __device__ __forceinline__ void step_block(const Tensor& T, const Params& a, con
 
 template <int kCap>
 __global__ void __launch_bounds__(32 * kWarps, 4) step_kernel(const __grid_constant__ List<kCap> list, const Params a) {
-    Rates r{a.c1, a.root2, 0.f, 0.f, a.step};
-    after_previous_kernel();
-    if (a.device_step != nullptr) {
-        const int64_t t = *a.device_step;
-        if (t < 1) return;
-        r.step = (uint32_t)t;
-        r.c1 = (float)(1.0 / (1.0 - pow(a.db1, (double)t)));
-        r.root2 = (float)sqrt(1.0 / (1.0 - pow(a.db2, (double)t)));
-    }
     const int lane = threadIdx.x & 31;
     const uint32_t b = blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (b >= list.blocks) return;
@@ -383,9 +374,16 @@ __global__ void __launch_bounds__(32 * kWarps, 4) step_kernel(const __grid_const
         const uint32_t mid = (lo + hi) / 2;
         if (list.t[mid].first <= b) lo = mid; else hi = mid;
     }
+    after_previous_kernel();
+    Rates r{a.c1, a.root2, a.step};
+    if (a.device_step != nullptr) {
+        const int64_t t = *a.device_step;
+        if (t < 1) return;
+        r.step = (uint32_t)t;
+        r.c1 = (float)(1.0 / (1.0 - pow(a.db1, (double)t)));
+        r.root2 = (float)sqrt(1.0 / (1.0 - pow(a.db2, (double)t)));
+    }
     const Tensor& T = list.t[lo];
-    r.rate = __fmul_rn(T.lr_scale, a.lr);
-    r.keep = (float)(1.0 - (double)T.lr_scale * (double)a.lr * (double)T.decay);
     const int64_t blk = b - T.first;
     if ((blk + 1) * kBlock > T.n) return step_block<-1, -1, -1, false>(T, a, r, blk, lane);
     switch (T.types & 0xfffu) {

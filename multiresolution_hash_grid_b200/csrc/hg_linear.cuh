@@ -347,6 +347,10 @@ __device__ __forceinline__ void emit_column8(const Epilogue& e, void* out, int64
 // halves the shared-memory reads of B per MMA and leaves room for more stages; the first block
 // issues the MMAs of both, and each writes out its own 128 rows.
 //
+// fp32 results of long sums (kGather): the tensor cores' additions cut off instead of rounding, which for
+// random operands loses 1.1e-9 of the result for each k (measured: 9.1e-6 for K = 8192, where plain
+// fp32 has 9.6e-7). So every kSegment steps the accumulator is added to fp32 registers and begins again.
+//
 // Way out: a lane reads 32 columns of its row from TMEM, adds bias, applies the activation and adds
 // the residual in fp32, and rounds. Where rows begin on 16-byte boundaries (kVectors) the chunk of 32 x 32
 // goes to 4 KB of shared memory a warp, and from there by TMA, which also keeps to the array's bounds: a
@@ -358,6 +362,7 @@ constexpr int kBm = 128, kBk = 64;
 constexpr int kOutWarps = 8;
 constexpr int kThreads = 32 * (kOutWarps + 2);
 constexpr int kMaxStages = 16;
+constexpr int kSegment = 12;  // 64-wide steps of K (16 took it to the 1e-6 of plain fp32 sums, 12 leaves a quarter of room)
 constexpr int kStaging = kOutWarps * 32 * 32 * 4;
 
 struct Side {             // one operand's share of a stage: `boxes` boxes of box_rows x 64 elements
@@ -536,8 +541,8 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-template <typename T, bool kPair, bool kVectors>
-__global__ void __launch_bounds__(kThreads, kPair ? 1 : 2) gemm_kernel(const __grid_constant__ Gemms list) {
+template <typename T, bool kPair, bool kVectors, bool kGather>
+__global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kernel(const __grid_constant__ Gemms list) {
     const int which = (int)blockIdx.x >= list.second;
     const Gemm& g = list.of[which];
     const int block = (int)blockIdx.x - (which ? list.second : 0);
@@ -654,17 +659,27 @@ __global__ void __launch_bounds__(kThreads, kPair ? 1 : 2) gemm_kernel(const __g
             const uint32_t next_b = g.resident ? g.b.bytes >> 4 : 0;
             const uint64_t a0 = swizzled_desc(sm0, 64 * 128), b0 = swizzled_desc(g.resident ? sb0 : sm0 + g.a.bytes, 64 * 128);
             for (Tiles t(g, first, step); t.more() && ok && kbs > 0; t.next(), ++i) {
-                const uint32_t acc = tmem + (i & 1u) * g.columns;
+                uint32_t acc = tmem + (i & 1u) * g.columns;
                 if (!(ok = wait_bounded(room + 8 * (i & 1u), ((i >> 1) & 1u) ^ 1u, &abort_flag))) break;
                 mlp::fence_after();
-                for (int kb = 0; kb < kbs; ++kb) {
+                int kseg = 0;
+                for (int kb = 0; kb < kbs; ++kb, ++kseg) {
+                    if (kGather && kseg == kSegment) {  // this segment's sums go to registers, the next one starts from zero
+                        if (kPair && issues) commit_pair(done + 8 * (i & 1u));
+                        if (!kPair && issues) mlp::commit(done + 8 * (i & 1u));
+                        ++i;
+                        kseg = 0;
+                        acc = tmem + (i & 1u) * g.columns;
+                        if (!(ok = wait_bounded(room + 8 * (i & 1u), ((i >> 1) & 1u) ^ 1u, &abort_flag))) break;
+                        mlp::fence_after();
+                    }
                     if (!(ok = wait_bounded(full + 8 * r.stage, r.phase, &abort_flag))) break;
                     mlp::fence_after();
                     const uint64_t da = a0 + (uint32_t)r.stage * stage, db = b0 + (g.resident ? (uint32_t)kb * next_b : (uint32_t)r.stage * stage);
 #pragma unroll
                     for (int k = 0; k < kBk / 16; ++k) {
-                        if (kPair && issues) mma_pair(acc, da + k * step_a, db + k * step_b, g.idesc, (kb | k) != 0 ? 1u : 0u);
-                        if (!kPair && issues) mlp::mma(acc, da + k * step_a, db + k * step_b, g.idesc, (kb | k) != 0 ? 1u : 0u);
+                        if (kPair && issues) mma_pair(acc, da + k * step_a, db + k * step_b, g.idesc, (kseg | k) != 0 ? 1u : 0u);
+                        if (!kPair && issues) mlp::mma(acc, da + k * step_a, db + k * step_b, g.idesc, (kseg | k) != 0 ? 1u : 0u);
                     }
                     if (kPair && issues) commit_pair(empty + 8 * r.stage);
                     if (!kPair && issues) mlp::commit(empty + 8 * r.stage);
@@ -681,132 +696,167 @@ __global__ void __launch_bounds__(kThreads, kPair ? 1 : 2) gemm_kernel(const __g
         }
     } else {
         // -------------------------------- way out ---------------------------------
-        const int quarter = warp & 3, chunks = (g.bn + 31) / 32;
-        float4* st = reinterpret_cast<float4*>(staging + warp * 4096);
+        const int quarter = warp & 3, half = warp >> 2, chunks = (g.bn + 31) / 32;
         const Epilogue e = g.e;  // in registers: read through the chosen product, each store would make it suspect
-        void* out = g.split_stride != 0 ? static_cast<float*>(e.out) + part * g.split_stride : e.out;
+        [[maybe_unused]] void* out = g.split_stride != 0 ? static_cast<float*>(e.out) + part * g.split_stride : e.out;
         uint32_t i = 0;
-        for (Tiles t(g, first, step); t.more(); t.next(), ++i) {
+        for (Tiles t(g, first, step); t.more(); t.next()) {
             const int64_t m0 = (int64_t)(kPair ? 2 * t.m + (int)rank : t.m) * kBm + 32 * quarter;
             const int n0 = t.n * g.bn, cols = (int)min(g.N, (int64_t)n0 + g.bn);
             const int rows = (int)min((int64_t)32, g.M - m0);
-            bool waited = kbs == 0;
-            for (int c = warp >> 2; c < chunks && rows > 0; c += 2) {
-                __syncwarp();
+            // the 16-bit residuals of a lane's row
+            auto load_residual = [&](int c, uint4 (&q)[4]) {
                 const int c0 = n0 + 32 * c;
-                // a 16-bit residual is on its way while the accumulator is waited for and read
-                uint4 q[4] = {};
+                if (!kVectors || g.cluster > 1 || e.residual == nullptr || e.out_f32 || c0 + 32 > cols || lane >= rows) return;
+                const T* p = static_cast<const T*>(e.residual) + (m0 + lane) * e.ldr + c0;
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (in_bounds<kChkResidual>(p + 8 * u, 16)) q[u] = *reinterpret_cast<const uint4*>(p + 8 * u);
+            };
+            // one chunk's sums, a row a lane, on their way
+            auto emit_chunk = [&](int c, float (&y)[32], const uint4 (&q)[4]) {
+                const int c0 = n0 + 32 * c;
                 const bool inside = c0 + 32 <= cols;
-                if (kVectors && g.cluster == 1 && e.residual != nullptr && !e.out_f32 && inside && lane < rows) {
-                    const T* p = static_cast<const T*>(e.residual) + (m0 + lane) * e.ldr + c0;
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (in_bounds<kChkResidual>(p + 8 * u, 16)) q[u] = *reinterpret_cast<const uint4*>(p + 8 * u);
-                }
-                __syncwarp();
-                if (!waited) {
-                    const bool ok = wait_bounded(done + 8 * (i & 1u), (i >> 1) & 1u, &abort_flag);
-                    if (__any_sync(0xffffffffu, !ok)) goto out_of_time;
-                    mlp::fence_after();
-                    waited = true;
-                }
-                uint32_t v[32];
-                if (kbs > 0) {
-                    tmem_ld32(tmem + ((uint32_t)(32 * quarter) << 16) + (i & 1u) * g.columns + 32 * c, v);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0u;
-                }
-                if (kVectors && g.cluster == 1) {
-                    float y[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(v[j]);
-                    if (e.bias != nullptr) {
-                        if (inside) {
-#pragma unroll
-                            for (int u = 0; u < 8; ++u) {
-                                const float4 b = in_bounds<kChkBias>(e.bias + c0 + 4 * u, 16) ? __ldg(reinterpret_cast<const float4*>(e.bias + c0) + u)
-                                                                                            : make_float4(0.f, 0.f, 0.f, 0.f);
-                                y[4 * u] += b.x; y[4 * u + 1] += b.y; y[4 * u + 2] += b.z; y[4 * u + 3] += b.w;
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (c0 + j < cols) y[j] += bias1(e, c0 + j);
-                        }
-                    }
-                    uint8_t* sy = staging + warp * 4096;  // y, and 16-bit z behind it
-                    uint8_t* sz = e.out_f32 ? staging + (kOutWarps + warp) * 4096 : sy + 2048;
-                    if (lane == 0) store_wait_read();  // the last chunk has left
+                if (g.cluster > 1 || !kVectors) {
+                    // a split product leaves its share in the stages' memory, where the cluster's other blocks read it
+                    float4* st = reinterpret_cast<float4*>(g.cluster > 1 ? sm + (quarter * chunks + c) * 4096 : staging + warp * 4096);
                     __syncwarp();
-                    if (e.z != nullptr) stage_row16<T>(sz, lane, y);
-                    activate(y, e.act);
-                    if (e.residual != nullptr) {
-                        if (inside && !e.out_f32) {
 #pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const float2 r0 = unpack2<T>(q[u].x), r1 = unpack2<T>(q[u].y), r2 = unpack2<T>(q[u].z), r3 = unpack2<T>(q[u].w);
-                                y[8 * u] += r0.x; y[8 * u + 1] += r0.y; y[8 * u + 2] += r1.x; y[8 * u + 3] += r1.y;
-                                y[8 * u + 4] += r2.x; y[8 * u + 5] += r2.y; y[8 * u + 6] += r3.x; y[8 * u + 7] += r3.y;
-                            }
-                        } else if (inside && lane < rows) {
-                            const float* p = static_cast<const float*>(e.residual) + (m0 + lane) * e.ldr + c0;
-#pragma unroll
-                            for (int u = 0; u < 8; ++u)
-                                if (in_bounds<kChkResidual>(p + 4 * u, 16)) {
-                                    const float4 r = *reinterpret_cast<const float4*>(p + 4 * u);
-                                    y[4 * u] += r.x; y[4 * u + 1] += r.y; y[4 * u + 2] += r.z; y[4 * u + 3] += r.w;
-                                }
-                        } else if (lane < rows) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (c0 + j < cols) y[j] += residual1<T>(e, m0 + lane, c0 + j);
-                        }
-                    }
-                    if (e.out_f32) stage_row32(sy, lane, y);
-                    else stage_row16<T>(sy, lane, y);
-                    mlp::fence_async_smem();
+                    for (int u = 0; u < 8; ++u) st[unit_of(lane, u)] = make_float4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
                     __syncwarp();
-                    if (lane == 0 && c0 < cols) {
-                        if (e.z != nullptr) tma_store(&g.tz, (uint32_t)__cvta_generic_to_shared(sz), c0, (int)m0, 0);
-                        tma_store(&g.ty, (uint32_t)__cvta_generic_to_shared(sy), c0, (int)m0, part);
-                        store_commit();
-                    }
-                    continue;
-                }
-                // a split product leaves its share in the stages' memory, where the cluster's other blocks read it
-                if (g.cluster > 1) st = reinterpret_cast<float4*>(sm + (quarter * chunks + c) * 4096);
-                __syncwarp();
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    st[unit_of(lane, u)] = make_float4(__uint_as_float(v[4 * u]), __uint_as_float(v[4 * u + 1]),
-                                                       __uint_as_float(v[4 * u + 2]), __uint_as_float(v[4 * u + 3]));
-                if (g.cluster > 1) continue;
-                __syncwarp();
-                if (!kVectors && c0 + lane < cols) {
-                    const float* sf = reinterpret_cast<const float*>(st);
-                    const float bias = bias1(e, c0 + lane);
+                    if (!kVectors && g.cluster == 1 && c0 + lane < cols) {
+                        const float* sf = reinterpret_cast<const float*>(st);
+                        const float bias = bias1(e, c0 + lane);
 #pragma unroll 1
-                    for (int r0 = 0; r0 < rows; r0 += 8) {
-                        float y[8];
+                        for (int r0 = 0; r0 < rows; r0 += 8) {
+                            float s[8];
 #pragma unroll
-                        for (int p = 0; p < 8; ++p) y[p] = sf[unit_of(r0 + p, lane >> 2) * 4 + (lane & 3)] + bias;
-                        if (rows - r0 >= 8) emit_column8<T, true>(e, out, m0 + r0, 8, c0 + lane, y);
-                        else emit_column8<T, false>(e, out, m0 + r0, rows - r0, c0 + lane, y);
+                            for (int p = 0; p < 8; ++p) s[p] = sf[unit_of(r0 + p, lane >> 2) * 4 + (lane & 3)] + bias;
+                            if (rows - r0 >= 8) emit_column8<T, true>(e, out, m0 + r0, 8, c0 + lane, s);
+                            else emit_column8<T, false>(e, out, m0 + r0, rows - r0, c0 + lane, s);
+                        }
+                    }
+                    return;
+                }
+                if (e.bias != nullptr) {
+                    if (inside) {
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            const float4 b = in_bounds<kChkBias>(e.bias + c0 + 4 * u, 16) ? __ldg(reinterpret_cast<const float4*>(e.bias + c0) + u)
+                                                                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+                            y[4 * u] += b.x; y[4 * u + 1] += b.y; y[4 * u + 2] += b.z; y[4 * u + 3] += b.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (c0 + j < cols) y[j] += bias1(e, c0 + j);
                     }
                 }
-            }
-            if (kbs > 0) {
-                if (!waited) {  // a warp without a chunk of this tile keeps in step all the same
-                    const bool ok = wait_bounded(done + 8 * (i & 1u), (i >> 1) & 1u, &abort_flag);
-                    if (__any_sync(0xffffffffu, !ok)) goto out_of_time;
+                uint8_t* sy = staging + warp * 4096;  // y, and 16-bit z behind it
+                uint8_t* sz = e.out_f32 ? staging + (kOutWarps + warp) * 4096 : sy + 2048;
+                if (lane == 0) store_wait_read();  // the last chunk has left
+                __syncwarp();
+                if (e.z != nullptr) stage_row16<T>(sz, lane, y);
+                activate(y, e.act);
+                if (e.residual != nullptr) {
+                    if (inside && !e.out_f32) {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const float2 r0 = unpack2<T>(q[u].x), r1 = unpack2<T>(q[u].y), r2 = unpack2<T>(q[u].z), r3 = unpack2<T>(q[u].w);
+                            y[8 * u] += r0.x; y[8 * u + 1] += r0.y; y[8 * u + 2] += r1.x; y[8 * u + 3] += r1.y;
+                            y[8 * u + 4] += r2.x; y[8 * u + 5] += r2.y; y[8 * u + 6] += r3.x; y[8 * u + 7] += r3.y;
+                        }
+                    } else if (inside && lane < rows) {
+                        const float* p = static_cast<const float*>(e.residual) + (m0 + lane) * e.ldr + c0;
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            if (in_bounds<kChkResidual>(p + 4 * u, 16)) {
+                                const float4 r = *reinterpret_cast<const float4*>(p + 4 * u);
+                                y[4 * u] += r.x; y[4 * u + 1] += r.y; y[4 * u + 2] += r.z; y[4 * u + 3] += r.w;
+                            }
+                    } else if (lane < rows) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (c0 + j < cols) y[j] += residual1<T>(e, m0 + lane, c0 + j);
+                    }
                 }
+                if (e.out_f32) stage_row32(sy, lane, y);
+                else stage_row16<T>(sy, lane, y);
+                mlp::fence_async_smem();
+                __syncwarp();
+                if (lane == 0 && c0 < cols) {
+                    if (e.z != nullptr) tma_store(&g.tz, (uint32_t)__cvta_generic_to_shared(sz), c0, (int)m0, 0);
+                    tma_store(&g.ty, (uint32_t)__cvta_generic_to_shared(sy), c0, (int)m0, part);
+                    store_commit();
+                }
+            };
+            auto wait_accumulator = [&]() {
+                const bool ok = wait_bounded(done + 8 * (i & 1u), (i >> 1) & 1u, &abort_flag);
+                if (__any_sync(0xffffffffu, !ok)) return false;
+                mlp::fence_after();
+                return true;
+            };
+            auto free_accumulator = [&]() {
                 mlp::fence_before();
                 __syncwarp();
                 if (lane == 0) {
                     if (kPair) arrive_cluster(cluster_address(room + 8 * (i & 1u), 0));
                     else mlp::mbar_arrive(room + 8 * (i & 1u));
                 }
+                ++i;
+            };
+            const uint32_t row_of_tmem = tmem + ((uint32_t)(32 * quarter) << 16);
+            if (kGather) {
+                constexpr int kMine = kPair ? 4 : 2;  // chunks of a warp
+                float acc[kMine][32];
+#pragma unroll
+                for (int k = 0; k < kMine; ++k)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) acc[k][j] = 0.f;
+                for (int kb = 0; kb < kbs; kb += kSegment) {
+                    if (!wait_accumulator()) goto out_of_time;
+#pragma unroll
+                    for (int k = 0; k < kMine; ++k) {
+                        if (2 * k + half >= chunks || rows <= 0) continue;
+                        uint32_t v[32];
+                        __syncwarp();
+                        tmem_ld32(row_of_tmem + (i & 1u) * g.columns + 32 * (2 * k + half), v);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) acc[k][j] += __uint_as_float(v[j]);
+                    }
+                    free_accumulator();
+                }
+#pragma unroll
+                for (int k = 0; k < kMine; ++k) {
+                    if (2 * k + half >= chunks || rows <= 0) continue;
+                    uint4 q[4] = {};
+                    load_residual(2 * k + half, q);
+                    emit_chunk(2 * k + half, acc[k], q);
+                }
+                continue;
+            }
+            bool waited = kbs == 0;
+            for (int c = half; c < chunks && rows > 0; c += 2) {
+                uint4 q[4] = {};
+                load_residual(c, q);  // on its way while the accumulator is waited for and read
+                __syncwarp();
+                if (!waited && !wait_accumulator()) goto out_of_time;
+                waited = true;
+                uint32_t v[32];
+                float y[32];
+                if (kbs > 0) {
+                    tmem_ld32(row_of_tmem + (i & 1u) * g.columns + 32 * c, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0u;
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(v[j]);
+                emit_chunk(c, y, q);
+            }
+            if (kbs > 0) {
+                if (!waited && !wait_accumulator()) goto out_of_time;  // a warp without a chunk keeps in step all the same
+                free_accumulator();
             }
         }
     out_of_time:
@@ -973,14 +1023,13 @@ __global__ void __launch_bounds__(256) realign_kernel(const __grid_constant__ Re
 // registers). That one copy of dz then serves both products: with rows of 64 outputs it is a k-major
 // A operand of dx = dz W and, read the other way, an mn-major A operand of dW = dz^T x, as the tile of x
 // is its mn-major B operand. W stays in shared memory. dx goes out as in the kernel above; dW
-// gathers in tensor memory over kFlush tiles, and is then added to fp32 registers: the tensor
-// cores' sums lose up to a unit in the last place at each addition, registers only half of one, and only
-// one in kFlush * 8 (measured for 2^20 rows: see the error bounds in the tests). Each block writes its sums
-// to the workspace, where sum_parts_kernel adds them in order.
+// gathers in tensor memory over kFlush tiles, and is then added to fp32 registers (the tensor cores'
+// additions cut off: see kGather above). Each block writes its sums to the workspace, where
+// sum_parts_kernel adds them in order.
 //
 // Warps: 0-7 write dx, 8 issues MMAs, 9 copies, 10-17 make dz and keep dW's and db's sums.
 // ---------------------------------------------------------------------------------------
-constexpr int kFlush = 8;
+constexpr int kFlush = 6;
 constexpr int kNarrowThreads = 32 * 18;
 constexpr int kNarrowStages = 4;
 constexpr int kBox = kBm * 128;  // bytes of a box of 128 rows x 64 columns

@@ -194,6 +194,27 @@ def test_narrow_layers_over_many_rows(K, M):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N,K,M", [(4096, 4096, 2048), (300, 8200, 264), (64, 30000, 72), (40, 5000, 37)])
+def test_long_sums_in_fp32(N, K, M):
+    """fp32 results of sums over thousands of terms: the tensor cores' truncating additions alone would be off by 1e-9 a
+    term. With sums of 1024 terms added in fp32, an addition rounding by at most 2^-24, the bias is that of 1024 terms,
+    1.1e-6, and the additions add less than 2^-24 times their number's root."""
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.randn(N, K, device="cuda", generator=gen).bfloat16()
+    w = torch.randn(M, K, device="cuda", generator=gen).bfloat16()
+    ref = x.double() @ w.double().t()
+    y = hg.Linear(K, M).forward(x, w, y=torch.empty(N, M, device="cuda"))
+    bound = 1.1e-6 * 1.2 + U * (K / 1024) ** 0.5
+    assert float((y.double() - ref).norm() / ref.norm()) < bound
+    # the same product as a weight gradient (rows K) and as an input gradient
+    _, dw, _ = hg.Linear(M, N).backward(x.t().contiguous(), w.t().contiguous(), torch.zeros(N, M, device="cuda").bfloat16(), dL_dx=None)
+    assert float((dw.double() - ref).norm() / ref.norm()) < bound
+    dx, _, _ = hg.Linear(M, K).backward(x, torch.zeros(N, M, device="cuda").bfloat16(), w.t().contiguous(), dL_dw=None, dL_db=None,
+                                        dL_dx=torch.empty(N, M, device="cuda"))
+    assert float((dx.double() - ref).norm() / ref.norm()) < bound
+
+
+@pytest.mark.gpu
 def test_no_rows():
     layer = hg.Linear(32, 48, hg.HASHGRID_F16, hg.HASHGRID_ACT_GELU)
     x = torch.empty(0, 32, device="cuda", dtype=torch.float16)
