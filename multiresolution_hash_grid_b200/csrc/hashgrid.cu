@@ -900,17 +900,18 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 bool aligned_rows(const Array& a) { return a.outer <= 1 || a.ld % 8 == 0; }
 size_t realigned_bytes(int64_t outer, int64_t inner) { return align256((size_t)outer * ((inner + 7) / 8 * 8) * 2); }
 
-// Copies those of up to two arrays that need it into `work` and points them there.
-int realign(Array* const* arrays, int count, char* work, const char* what, cudaStream_t s) {
-    hg::linear::RealignList l;
+// Adds the copies of those of up to two arrays that need one to `l`, and points them there. Returns the bytes
+// of `work` that they take.
+size_t add_copies(hg::linear::RealignList& l, Array* const* arrays, int count, char* work) {
     std::memset(&l, 0, sizeof l);
+    size_t used = 0;
     int n = 0;
     for (int i = 0; i < count; ++i) {
         Array& a = *arrays[i];
         if (aligned_rows(a)) continue;
         hg::linear::Realign& r = l.a[n++];
         r.p = a.p;
-        r.to = reinterpret_cast<uint16_t*>(work);
+        r.to = reinterpret_cast<uint16_t*>(work + used);
         r.bytes = strided_bytes(a.outer, a.inner, a.ld, 2);
         r.outer = a.outer;
         r.ld = a.ld;
@@ -919,22 +920,29 @@ int realign(Array* const* arrays, int count, char* work, const char* what, cudaS
         r.role = a.role;
         l.total += a.outer * r.chunks;
         if (n == 1) l.first = l.total;
-        work += realigned_bytes(a.outer, a.inner);
+        used += realigned_bytes(a.outer, a.inner);
         a = Array{r.to, a.outer, a.inner, r.chunks * 8, a.mn, hg::kChkWork};
     }
-    if (n == 0) return ok();
-    const int64_t blocks = (l.total + 1023) / 1024;
-    if (blocks > 0x7fffffffLL) return fail(HASHGRID_ERR_ARG, "%s: too many rows to realign", what);
-    return launch_after(hg::linear::realign_kernel, dim3((unsigned)blocks), 256, 0, 1, s, what, l);
+    return used;
 }
 
-// The backward pass's workspace: the copies of x and w (or dy) with aligned rows, dz (where it has to be
-// computed), the parts of db, the parts of dw; or, for a narrow layer, the blocks' sums.
+// The launch before the products: `slope` (rows = 0: none) and the copies.
+template <typename T>
+int launch_prepare(const hg::linear::Slope& slope, bool vectors, const hg::linear::RealignList& copies, const char* what, cudaStream_t s) {
+    const int64_t slope_blocks = slope.rows == 0 ? 0 : (int64_t)slope.col_blocks * slope.shares, blocks = slope_blocks + (copies.total + 1023) / 1024;
+    if (blocks == 0) return ok();
+    if (blocks > 0x7fffffffLL) return fail(HASHGRID_ERR_ARG, "%s: too many rows to realign", what);
+    auto k = vectors ? hg::linear::prepare_kernel<T, true> : hg::linear::prepare_kernel<T, false>;
+    return launch_after(k, dim3((unsigned)blocks), 256, 0, 1, s, what, slope, copies, (int)slope_blocks);
+}
+
+// The backward pass's workspace: the copies of x and w with aligned rows, dz (where dy is not it), the parts of
+// db, the parts of dw.
 struct LinearWork {
     int64_t lddz;   // elements
-    int parts;      // row shares of the db sums
+    int shares;     // row shares of the db sums
     int splits;     // row shares of dw
-    size_t copies, dy, dz, sums, dw, bytes;  // offsets, total
+    size_t dz, sums, dw, bytes;  // offsets, total
 };
 
 constexpr int kWorkSms = 148;  // the workspace's size may not depend on the device
@@ -942,7 +950,7 @@ constexpr int kWorkSms = 148;  // the workspace's size may not depend on the dev
 // Whether the one-pass kernel takes a layer: its tile of dy, z and x (x 2 stages) and W fit into shared
 // memory, and there are 64 tiles or more.
 bool narrow_layer(const hashgrid_linear_s* l, int64_t N) {
-    if (l->in > 128 || l->out > 128 || l->in % 8 != 0 || l->out % 8 != 0 || N < 64 * hg::linear::kBm) return false;
+    if (l->in > 128 || l->out > 128 || N < 64 * hg::linear::kBm) return false;
     const int boxes_out = ceil_div(l->out, 64), boxes_in = ceil_div(l->in, 64);
     const int stage = (boxes_out * (l->act == HASHGRID_ACT_NONE ? 1 : 2) + boxes_in) * hg::linear::kBox;
     return hg::linear::narrow_smem(2 * stage, ceil_div(l->out, 16) * 16 * boxes_in * 128) <= 226 * 1024;
@@ -953,17 +961,15 @@ bool narrow_layer(const hashgrid_linear_s* l, int64_t N) {
 LinearWork linear_work(const hashgrid_linear_s* l, int64_t N, int64_t lddy, int64_t ldx) {
     LinearWork w;
     w.lddz = (l->out + 7) / 8 * 8;
-    w.parts = N <= 256 ? 1 : (int)std::min<int64_t>(256, (N + 63) / 64);
+    w.shares = N <= 256 ? 1 : (int)std::min<int64_t>(std::max(1, 4 * kWorkSms / ceil_div(l->out, 64)), (N + 127) / 128);
     const int64_t tiles = (int64_t)ceil_div(l->out, hg::linear::kBm) * ceil_div(l->in, 128);
     w.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kWorkSms / tiles, N / (4 * hg::linear::kBk)));
-    const bool plain = l->act == HASHGRID_ACT_NONE;
-    w.copies = 0;
-    w.dy = (l->in % 8 != 0 ? realigned_bytes(l->out, l->in) : 0) + (ldx % 8 != 0 ? realigned_bytes(N, l->in) : 0);
-    w.dz = w.dy + (plain && lddy % 8 != 0 ? realigned_bytes(N, l->out) : 0);
-    w.sums = w.dz + (plain ? 0 : align256((size_t)N * w.lddz * 2));
-    w.dw = w.sums + align256((size_t)w.parts * l->out * sizeof(float));
-    w.bytes = w.dw + (w.splits > 1 ? align256((size_t)w.splits * l->in * l->out * sizeof(float)) : 0);
-    if (narrow_layer(l, N)) w.bytes = std::max(w.bytes, align256((size_t)kWorkSms * (l->in + 1) * l->out * sizeof(float)));
+    w.dz = (l->in % 8 != 0 ? realigned_bytes(l->out, l->in) : 0) + (ldx % 8 != 0 ? realigned_bytes(N, l->in) : 0);
+    w.sums = w.dz + (l->act == HASHGRID_ACT_NONE && lddy % 8 == 0 ? 0 : align256((size_t)N * w.lddz * 2));
+    w.dw = w.sums + align256((size_t)w.shares * l->out * sizeof(float));
+    const size_t split = w.splits > 1 ? (size_t)w.splits * l->in * l->out : 0;
+    const size_t narrow = narrow_layer(l, N) ? (size_t)kWorkSms * (l->in + 1) * l->out : 0;
+    w.bytes = w.dw + align256(std::max(split, narrow) * sizeof(float));
     return w;
 }
 
@@ -984,8 +990,8 @@ int launch_sums(const hg::linear::Sums* list, int count, const char* what, cudaS
 }
 
 template <typename T>
-int launch_narrow_backward(const hashgrid_linear_s* l, const Array& dy, const Array& x, int64_t N, const void* w, const void* z, void* dx,
-                           int64_t lddx, int dx_dtype, void* dw, int dw_dtype, float* db, char* work, int* status, const char* what,
+int launch_narrow_backward(const hashgrid_linear_s* l, int act, const Array& dy, const Array& x, int64_t N, const Array& w, const void* z, void* dx,
+                           int64_t lddx, int dx_dtype, bool want_db, float* parts, int* blocks_out, int* status, const char* what,
                            cudaStream_t s) {
     namespace hl = hg::linear;
     hl::Narrow g;
@@ -993,7 +999,7 @@ int launch_narrow_backward(const hashgrid_linear_s* l, const Array& dy, const Ar
     g.rows = N;
     g.in = l->in;
     g.out = l->out;
-    g.act = l->act;
+    g.act = act;
     g.boxes_in = ceil_div(l->in, 64);
     g.boxes_out = ceil_div(l->out, 64);
     g.columns = ceil_div(l->in, 32) * 32;
@@ -1004,8 +1010,8 @@ int launch_narrow_backward(const hashgrid_linear_s* l, const Array& dy, const Ar
     if (int rc = set_map(g.tx, x, hl::kBm, what)) return rc;
     if (z != nullptr)
         if (int rc = set_map(g.tz, {z, N, l->out, l->out, false, hg::kChkZ}, hl::kBm, what)) return rc;
-    if (int rc = set_map(g.tw, {dx != nullptr ? w : dy.p, l->out, l->in, l->in, true, hg::kChkWeights}, g.k_out, what)) return rc;
-    g.stage_bytes = (g.boxes_out * (l->act == HASHGRID_ACT_NONE ? 1 : 2) + g.boxes_in) * hl::kBox;
+    if (int rc = set_map(g.tw, dx != nullptr ? w : dy, g.k_out, what)) return rc;
+    g.stage_bytes = (g.boxes_out * (act == HASHGRID_ACT_NONE ? 1 : 2) + g.boxes_in) * hl::kBox;
     g.w_bytes = g.k_out * g.boxes_in * 128;
     g.stages = hl::kNarrowStages;
     while (g.stages > 2 && hl::narrow_smem(g.stages * g.stage_bytes, g.w_bytes) > 226 * 1024) --g.stages;
@@ -1015,20 +1021,20 @@ int launch_narrow_backward(const hashgrid_linear_s* l, const Array& dy, const Ar
     g.id_dx = id;
     g.id_dw = id | (1u << 15);
     g.e = hl::Epilogue{nullptr, nullptr, dx, nullptr, 0, lddx, 0, dx_dtype == HASHGRID_F32, hl::kNoAct, hg::kChkOut};
-    if (dx != nullptr)
+    const size_t xs = dx_dtype == HASHGRID_F32 ? 4 : 2;
+    const bool vectors = dx == nullptr || (l->in * xs % 16 == 0 && vector_rows(dx, lddx, xs));
+    if (dx != nullptr && vectors)
         if (int rc = set_store_map(g.tdx, dx, N, l->in, lddx, 1, dx_dtype == HASHGRID_F32, what)) return rc;
-    g.parts = reinterpret_cast<float*>(work);
-    g.want_db = db != nullptr;
+    g.parts = parts;
+    g.want_db = want_db;
     g.status = status;
     const int blocks = std::min(std::min(kWorkSms, device_sms()), ceil_div(N, hl::kBm));
     const size_t smem = hl::narrow_smem(g.stages * g.stage_bytes, g.w_bytes);
-    auto k = l->in <= 64 ? hl::narrow_backward_kernel<T, 1> : hl::narrow_backward_kernel<T, 2>;
+    auto k = l->in <= 64 ? (vectors ? hl::narrow_backward_kernel<T, 1, true> : hl::narrow_backward_kernel<T, 1, false>)
+                         : (vectors ? hl::narrow_backward_kernel<T, 2, true> : hl::narrow_backward_kernel<T, 2, false>);
     if (int rc = prepare_smem_once(k, smem)) return rc;
-    if (int rc = launch_after(k, dim3((unsigned)blocks), hl::kNarrowThreads, smem, 1, s, what, g)) return rc;
-    const int64_t nw = (int64_t)l->in * l->out, stride = nw + l->out;
-    hl::Sums sums[2] = {{g.parts, stride, nw, blocks, dw_dtype == HASHGRID_F32 ? 0 : 1, dw, hg::kChkGrad},
-                        {g.parts + nw, stride, l->out, blocks, 0, db, hg::kChkBias}};
-    return launch_sums<T>(sums, db != nullptr ? 2 : 1, what, s);
+    *blocks_out = blocks;
+    return launch_after(k, dim3((unsigned)blocks), hl::kNarrowThreads, smem, 1, s, what, g);
 }
 
 size_t forward_work(const hashgrid_linear_s* l, int64_t N, int64_t ldx) {
@@ -1041,7 +1047,10 @@ int launch_linear_forward(const hashgrid_linear_s* l, const void* x, int64_t ldx
     static const char* what = "linear_forward";
     Array A{x, N, l->in, ldx, false, hg::kChkX}, B{w, l->out, l->in, l->in, false, hg::kChkWeights};
     Array* both[2] = {&A, &B};
-    if (int rc = realign(both, 2, work, what, s)) return rc;
+    hg::linear::RealignList copies;
+    add_copies(copies, both, 2, work);
+    hg::linear::Slope none = {};
+    if (int rc = launch_prepare<T>(none, false, copies, what, s)) return rc;
     return launch_gemm<T>(A, B, N, l->out, l->in, e, make_plan(N, l->out, l->in, device_sms()), status, what, s);
 }
 
@@ -1054,45 +1063,58 @@ int launch_linear_backward(const hashgrid_linear_s* l, const void* dy, int64_t l
     const LinearWork lw = linear_work(l, N, lddy, ldx);
     Array dz{dy, N, l->out, lddy, false, hg::kChkDout};
     Array W{w, l->out, l->in, l->in, true, hg::kChkWeights}, X{x, N, l->in, ldx, true, hg::kChkX};
-    const bool plain = l->act == HASHGRID_ACT_NONE;
-    if (dw != nullptr && narrow_layer(l, N) && aligned_rows(dz) && aligned_rows(X) &&
-        (dx == nullptr || vector_rows(dx, lddx, dx_dtype == HASHGRID_F32 ? 4 : 2)))
-        return launch_narrow_backward<T>(l, dz, X, N, w, plain ? nullptr : z, dx, lddx, dx_dtype, dw, dw_dtype, db, work, status, what, s);
-    Array* list[2];
+    const bool plain = l->act == HASHGRID_ACT_NONE, vectors = aligned_rows(dz) && (plain || l->out % 8 == 0);
+    // A narrow layer's kernel makes dz and db itself where TMA can read dy and z.
+    const bool narrow = dw != nullptr && narrow_layer(l, N), inside = narrow && vectors;
+    const bool convert = !inside && (!plain || !aligned_rows(dz)) && (dx != nullptr || dw != nullptr);
+    Array* list[2] = {};
     int n = 0;
     if (dx != nullptr) list[n++] = &W;
     if (dw != nullptr) list[n++] = &X;
-    if (int rc = realign(list, n, work + lw.copies, what, s)) return rc;
-    const bool convert = !plain && (dx != nullptr || dw != nullptr);
+    hl::RealignList copies;
+    add_copies(copies, list, n, work);
     hl::Sums sums[2];
     int nsums = 0;
-    if (convert || db != nullptr) {
-        T* to = convert ? reinterpret_cast<T*>(work + lw.dz) : nullptr;
-        float* parts = db != nullptr ? reinterpret_cast<float*>(work + lw.sums) : nullptr;
-        const dim3 grid((unsigned)((l->out + 63) / 64), (unsigned)lw.parts);
-        auto k = aligned_rows(dz) && l->out % 8 == 0 ? hl::slope_kernel<T, true> : hl::slope_kernel<T, false>;
-        if (int rc = launch_after(k, grid, 256, 0, 1, s, what, static_cast<const T*>(dy), lddy, static_cast<const T*>(z), N, l->out, l->act, to,
-                                  lw.lddz, lw.parts > 1 ? parts : db, lw.parts > 1 ? (int)hg::kChkWork : (int)hg::kChkBias))
+    hl::Slope slope = {};
+    if (convert || (db != nullptr && !inside)) {
+        slope.dy = dy;
+        slope.z = z;
+        slope.lddy = lddy;
+        slope.rows = N;
+        slope.lddz = lw.lddz;
+        slope.cols = l->out;
+        slope.act = l->act;
+        slope.dz = convert ? work + lw.dz : nullptr;
+        slope.sums = db == nullptr ? nullptr : lw.shares > 1 ? reinterpret_cast<float*>(work + lw.sums) : db;
+        slope.role = lw.shares > 1 ? hg::kChkWork : hg::kChkBias;
+        slope.groups = 1;
+        while (slope.groups < 8 && slope.groups * 8 < l->out) slope.groups *= 2;
+        slope.col_blocks = ceil_div(l->out, 64);
+        slope.shares = lw.shares;
+        if (convert) dz = Array{slope.dz, N, l->out, lw.lddz, false, hg::kChkWork};
+        if (db != nullptr && lw.shares > 1) sums[nsums++] = hl::Sums{slope.sums, l->out, l->out, lw.shares, 0, db, hg::kChkBias};
+    }
+    if (int rc = launch_prepare<T>(slope, vectors && l->out % 8 == 0, copies, what, s)) return rc;
+    const int64_t nw = (int64_t)l->in * l->out;
+    float* out = reinterpret_cast<float*>(work + lw.dw);
+    if (narrow) {
+        int blocks = 0;
+        if (int rc = launch_narrow_backward<T>(l, inside ? l->act : (int)HASHGRID_ACT_NONE, dz, X, N, W, inside && !plain ? z : nullptr, dx, lddx, dx_dtype,
+                                               inside && db != nullptr, out, &blocks, status, what, s))
             return rc;
-        if (convert) dz = Array{to, N, l->out, lw.lddz, false, hg::kChkWork};
-        if (db != nullptr && lw.parts > 1) sums[nsums++] = hl::Sums{parts, l->out, l->out, lw.parts, 0, db, hg::kChkBias};
+        sums[nsums++] = hl::Sums{out, nw + l->out, nw, blocks, dw_dtype == HASHGRID_F32 ? 0 : 1, dw, hg::kChkGrad};
+        if (inside && db != nullptr) sums[nsums++] = hl::Sums{out + nw, nw + l->out, l->out, blocks, 0, db, hg::kChkBias};
+        return launch_sums<T>(sums, nsums, what, s);
     }
-    if (!convert && n > 0) {
-        Array* d = &dz;
-        if (int rc = realign(&d, 1, work + lw.dy, what, s)) return rc;
-    }
-    // dx and dW do not depend on each other. Where neither fills the device they share a launch, dW cut into parts
-    // of the rows that the sums kernel adds; else each has its own.
+    // dx and dW do not depend on each other: where both are cut alike, and dW's sums are short, they share a
+    // launch. dW is cut into parts of the rows that the sums kernel adds where its tiles are few.
     constexpr bool half = std::is_same<T, __half>::value;
     const int sms = device_sms();
     Plan px = make_plan(N, l->in, l->out, sms), pw = make_plan(l->out, l->in, N, sms);
-    if (lw.splits > 1) {
-        pw = Plan{wide_tile(l->in, 128), 1, lw.splits, false};
-        if (!px.pair) px.cluster = 1;
-    }
+    if (lw.splits > 1) pw = Plan{wide_tile(l->in, 128), 1, lw.splits, false};
+    if (px.cluster == 2 && pw.cluster == 1) px.cluster = 1;
     const hl::Epilogue ex{nullptr, nullptr, dx, nullptr, 0, lddx, 0, dx_dtype == HASHGRID_F32, hl::kNoAct, hg::kChkOut};
     const bool parts = pw.splits > 1;
-    float* out = reinterpret_cast<float*>(work + lw.dw);
     const hl::Epilogue ew{nullptr, nullptr, parts ? out : dw, nullptr, 0, l->in, 0, parts || dw_dtype == HASHGRID_F32,
                           hl::kNoAct, parts ? hg::kChkWork : hg::kChkGrad};
     Product p[2];
@@ -1103,13 +1125,12 @@ int launch_linear_backward(const hashgrid_linear_s* l, const void* dy, int64_t l
         if (int rc = set_product(p[np++], half, dzt, X, l->out, l->in, N, ew, pw, status, what)) return rc;
     if (dx != nullptr)
         if (int rc = set_product(p[np++], half, dz, W, N, l->in, l->out, ex, px, status, what)) return rc;
-    if (np == 2 && px.pair == pw.pair && px.cluster == pw.cluster) {
+    if (np == 2 && px.pair == pw.pair && px.cluster == pw.cluster && p[0].gather == p[1].gather) {
         if (int rc = launch_products<T>(p, 2, px, what, s)) return rc;
     } else {
         for (int i = 0; i < np; ++i)
             if (int rc = launch_products<T>(&p[i], 1, dw != nullptr && i == 0 ? pw : px, what, s)) return rc;
     }
-    const int64_t nw = (int64_t)l->in * l->out;
     if (dw != nullptr && parts) sums[nsums++] = hl::Sums{out, nw, nw, lw.splits, dw_dtype == HASHGRID_F32 ? 0 : 1, dw, hg::kChkGrad};
     return launch_sums<T>(sums, nsums, what, s);
 }

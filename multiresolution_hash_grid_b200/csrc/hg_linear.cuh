@@ -989,11 +989,10 @@ __device__ __forceinline__ uint4 finish_chunk(const Chunk& c) {
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-__global__ void __launch_bounds__(256) realign_kernel(const __grid_constant__ RealignList l) {
+__device__ __forceinline__ void realign_block(const RealignList& l, int64_t block) {
     constexpr int kAtOnce = 4;
-    const int64_t i0 = (int64_t)blockIdx.x * (256 * kAtOnce) + threadIdx.x;
+    const int64_t i0 = block * (256 * kAtOnce) + threadIdx.x;
     Chunk c[kAtOnce];
-    after_previous_kernel();
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
         const int64_t i = i0 + 256 * u;
@@ -1051,7 +1050,7 @@ __host__ __device__ constexpr size_t narrow_smem(int stage_bytes_in_all, int w_b
     return 1024 + (size_t)stage_bytes_in_all + w_bytes + kStaging + 256 + 16;
 }
 
-template <typename T, int kChunks>  // kChunks * 64 >= in
+template <typename T, int kChunks, bool kVectors>  // kChunks * 64 >= in; kVectors: dx leaves by TMA
 __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(const __grid_constant__ Narrow g) {
     extern __shared__ uint8_t raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
@@ -1182,6 +1181,24 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
                 float y[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(v[j]);
+                if (!kVectors) {
+                    float4* sq = reinterpret_cast<float4*>(st);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) sq[unit_of(lane, u)] = make_float4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
+                    __syncwarp();
+                    const int rows = (int)min((int64_t)32, g.rows - m0);
+                    if (32 * c + lane < g.in)
+#pragma unroll 1
+                        for (int r0 = 0; r0 < rows; r0 += 8) {
+                            float s[8];
+#pragma unroll
+                            for (int p = 0; p < 8; ++p) s[p] = reinterpret_cast<const float*>(st)[unit_of(r0 + p, lane >> 2) * 4 + (lane & 3)];
+                            if (rows - r0 >= 8) emit_column8<T, true>(g.e, g.e.out, m0 + r0, 8, 32 * c + lane, s);
+                            else emit_column8<T, false>(g.e, g.e.out, m0 + r0, rows - r0, 32 * c + lane, s);
+                        }
+                    __syncwarp();
+                    continue;
+                }
                 if (lane == 0) store_wait_read();  // the last chunk has left
                 __syncwarp();
                 if (g.e.out_f32) stage_row32(st, lane, y);
@@ -1273,8 +1290,14 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
             for (int j = 0; j < 32; j += 4) {
                 const int col = 32 * (2 * c + half) + j;
                 float* p = part + (int64_t)o * g.in + col;
-                if (o < g.out && col < g.in && in_bounds<kChkWork>(p, 16))
-                    *reinterpret_cast<float4*>(p) = make_float4(acc[c][j], acc[c][j + 1], acc[c][j + 2], acc[c][j + 3]);
+                if (o >= g.out || col >= g.in) continue;
+                if (g.in % 4 == 0 && g.out % 4 == 0) {  // a block's sums are in * out + out floats
+                    if (in_bounds<kChkWork>(p, 16)) *reinterpret_cast<float4*>(p) = make_float4(acc[c][j], acc[c][j + 1], acc[c][j + 2], acc[c][j + 3]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (col + k < g.in && in_bounds<kChkWork>(p + k, 4)) p[k] = acc[c][j + k];
+                }
             }
         // db: the threads of a column chunk in order, through the first stage (every MMA that read it is done)
         if (g.want_db) {
@@ -1299,59 +1322,93 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(g.tmem_columns) : "memory");
 }
 
-// dz = dy act'(z), rounded to T, into dz (NULL: not wanted), and the sums of the unrounded dz
-// over this block's rows into sums[blockIdx.y][col] (NULL: not wanted). A block takes 64 columns, eight
-// neighbouring ones a thread, and every 32nd row of its share. kVectors: the rows of dy and z
-// begin on 16-byte boundaries and cols is a multiple of 8.
+// dz = dy act'(z), rounded to T, into dz (NULL: not wanted), and the sums of the unrounded dz over a
+// block's share of the rows into sums[share][col] (NULL: not wanted). A block takes up to 64 columns,
+// a thread eight neighbouring ones of every (256 / groups)-th row.
+struct Slope {
+    const void *dy, *z;
+    int64_t lddy, rows, lddz;
+    int cols, act;
+    void* dz;
+    float* sums;
+    int role;          // CheckRole of sums
+    int groups;        // column groups of eight in a block: 1, 2, 4 or 8
+    int col_blocks, shares;
+};
+
+// kVectors: the rows of dy and z begin on 16-byte boundaries and cols is a multiple of 8.
 template <typename T, bool kVectors>
-__global__ void __launch_bounds__(256) slope_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ z,
-                                                    int64_t rows, int cols, int act, T* __restrict__ dz, int64_t lddz,
-                                                    float* __restrict__ sums, int role) {
-    __shared__ float part[32][65];
-    const int col = blockIdx.x * 64 + 8 * (threadIdx.x & 7), r = threadIdx.x >> 3;
-    const int64_t share = (rows + gridDim.y - 1) / gridDim.y, r0 = blockIdx.y * share, r1 = min(rows, r0 + share);
-    const int n = min(8, cols - col);
+__device__ __forceinline__ void slope_block(const Slope& a, int block) {
+    __shared__ float part[8][64];
+    const T* dy = static_cast<const T*>(a.dy);
+    const T* z = static_cast<const T*>(a.z);
+    T* dz = static_cast<T*>(a.dz);
+    const int col_block = block % a.col_blocks, which = block / a.col_blocks, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int col = col_block * 64 + 8 * (threadIdx.x % a.groups), r = threadIdx.x / a.groups, step = 256 / a.groups;
+    const int64_t share = (a.rows + a.shares - 1) / a.shares, r0 = which * share, r1 = min(a.rows, r0 + share);
+    const int n = min(8, a.cols - col);
     float s[8] = {};
-    after_previous_kernel();
     if (n > 0) {
-#pragma unroll 2
-        for (int64_t row = r0 + r; row < r1; row += 32) {
+#pragma unroll 4
+        for (int64_t row = r0 + r; row < r1; row += step) {
             float d[8], v[8];
             if (kVectors) {
-                const T* p = dy + row * lddy + col;
+                const T* p = dy + row * a.lddy + col;
                 const uint4 q = in_bounds<kChkDout>(p, 16) ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
                 const float2 d0 = unpack2<T>(q.x), d1 = unpack2<T>(q.y), d2 = unpack2<T>(q.z), d3 = unpack2<T>(q.w);
                 d[0] = d0.x; d[1] = d0.y; d[2] = d1.x; d[3] = d1.y; d[4] = d2.x; d[5] = d2.y; d[6] = d3.x; d[7] = d3.y;
-                if (act != kNoAct) {
-                    const T* pz = z + row * cols + col;
+                if (a.act != kNoAct) {
+                    const T* pz = z + row * a.cols + col;
                     const uint4 zq = in_bounds<kChkZ>(pz, 16) ? __ldg(reinterpret_cast<const uint4*>(pz)) : make_uint4(0u, 0u, 0u, 0u);
                     const float2 z0 = unpack2<T>(zq.x), z1 = unpack2<T>(zq.y), z2 = unpack2<T>(zq.z), z3 = unpack2<T>(zq.w);
                     v[0] = z0.x; v[1] = z0.y; v[2] = z1.x; v[3] = z1.y; v[4] = z2.x; v[5] = z2.y; v[6] = z3.x; v[7] = z3.y;
                 }
             } else {
+                T dr[8], zr[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    d[j] = j < n && in_bounds<kChkDout>(dy + row * lddy + col + j, 2) ? to_float(dy[row * lddy + col + j]) : 0.f;
-                    v[j] = act != kNoAct && j < n && in_bounds<kChkZ>(z + row * cols + col + j, 2) ? to_float(z[row * cols + col + j]) : 0.f;
+                    const T zero = from_float<T>(0.f);
+                    dr[j] = j < n && in_bounds<kChkDout>(dy + row * a.lddy + col + j, 2) ? dy[row * a.lddy + col + j] : zero;
+                    zr[j] = a.act != kNoAct && j < n && in_bounds<kChkZ>(z + row * a.cols + col + j, 2) ? z[row * a.cols + col + j] : zero;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    d[j] = to_float(dr[j]);
+                    v[j] = to_float(zr[j]);
                 }
             }
-            if (act != kNoAct) times_slope(d, v, act);
+            if (a.act != kNoAct) times_slope(d, v, a.act);
             // rows of dz are multiples of 8 wide: what lies between `cols` and that is zero
-            if (dz != nullptr && in_bounds<kChkWork>(dz + row * lddz + col, 16)) *reinterpret_cast<uint4*>(dz + row * lddz + col) = pack8<T>(d);
+            if (dz != nullptr && in_bounds<kChkWork>(dz + row * a.lddz + col, 16)) *reinterpret_cast<uint4*>(dz + row * a.lddz + col) = pack8<T>(d);
 #pragma unroll
             for (int j = 0; j < 8; ++j) s[j] += d[j];
         }
     }
-    if (sums == nullptr) return;
+    if (a.sums == nullptr) return;
+    for (int o = 16; o >= a.groups; o >>= 1)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) part[r][8 * (threadIdx.x & 7) + j] = s[j];
+        for (int j = 0; j < 8; ++j) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
+    if (lane < a.groups)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) part[warp][8 * lane + j] = s[j];
     __syncthreads();
-    const int c = blockIdx.x * 64 + threadIdx.x;
-    if (threadIdx.x < 64 && c < cols) {
+    const int c = col_block * 64 + threadIdx.x;
+    if (threadIdx.x < 8 * a.groups && c < a.cols) {
         float t = 0.f;
-        for (int k = 0; k < 32; ++k) t += part[k][threadIdx.x];
-        if (in_bounds_role(role, sums + (int64_t)blockIdx.y * cols + c, 4)) sums[(int64_t)blockIdx.y * cols + c] = t;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) t += part[w][threadIdx.x];
+        float* p = a.sums + (int64_t)which * a.cols + c;
+        if (in_bounds_role(a.role, p, 4)) *p = t;
     }
+}
+
+// What comes before the products, in one launch: dz and db's sums (the first blocks), and the copies of
+// arrays that TMA cannot read as they are.
+template <typename T, bool kVectors>
+__global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ Slope slope, const __grid_constant__ RealignList copies, int slope_blocks) {
+    after_previous_kernel();
+    if ((int)blockIdx.x < slope_blocks) slope_block<T, kVectors>(slope, blockIdx.x);
+    else realign_block(copies, blockIdx.x - slope_blocks);
 }
 
 // Sums of parts in order, of one or two arrays: out[i] = sum over p of parts[p * stride + i]. A block takes
@@ -1378,7 +1435,7 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const __grid_constant__ 
     float v = 0.f;
     after_previous_kernel();
     if (i < s.n) {
-#pragma unroll 8
+#pragma unroll 16
         for (int p = warp; p < s.count; p += 8) {
             const float* at = s.parts + p * s.stride + i;
             if (in_bounds<kChkWork>(at, 4)) v += __ldg(at);

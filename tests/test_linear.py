@@ -184,12 +184,13 @@ def test_many_rows(N, K, M):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("K,M", [(64, 64), (32, 64), (64, 8), (8, 128), (128, 64), (128, 128), (24, 40), (104, 72)])
+@pytest.mark.parametrize("K,M", [(64, 64), (32, 64), (64, 8), (8, 128), (128, 64), (128, 128), (24, 40), (104, 72), (27, 31), (1, 2), (61, 128),
+                                 (128, 5), (65, 66)])
 def test_narrow_layers_over_many_rows(K, M):
     """Layers whose backward pass is one kernel; 128 tiles a block and a ragged last one, and three to five a block."""
     for i, (N, act) in enumerate([(4 * 148 * 128 + 77, hg.HASHGRID_ACT_RELU), (600 * 148 + 1, hg.HASHGRID_ACT_NONE),
                                   (1300 * 148 + 128, hg.HASHGRID_ACT_SILU), (90001, hg.HASHGRID_ACT_GELU)]):
-        check_backward(N, K, M, hg.HASHGRID_BF16 if i else hg.HASHGRID_F16, act, dx32=i == 1, dw32=i != 2, pad=(0, 8, 24, 0)[i],
+        check_backward(N, K, M, hg.HASHGRID_BF16 if i else hg.HASHGRID_F16, act, dx32=i == 1, dw32=i != 2, pad=(0, 8, 24, 3)[i],
                        want=(i != 3, True, i != 2))
 
 
