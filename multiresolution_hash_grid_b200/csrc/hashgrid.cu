@@ -961,9 +961,9 @@ bool narrow_layer(const hashgrid_linear_s* l, int64_t N) {
 LinearWork linear_work(const hashgrid_linear_s* l, int64_t N, int64_t lddy, int64_t ldx) {
     LinearWork w;
     w.lddz = (l->out + 7) / 8 * 8;
-    w.shares = N <= 256 ? 1 : (int)std::min<int64_t>(std::max(1, 4 * kWorkSms / ceil_div(l->out, 64)), (N + 127) / 128);
+    w.shares = N <= 512 ? 1 : (int)std::min<int64_t>(std::max(1, 2 * kWorkSms / ceil_div(l->out, 64)), (N + 127) / 128);
     const int64_t tiles = (int64_t)ceil_div(l->out, hg::linear::kBm) * ceil_div(l->in, 128);
-    w.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kWorkSms / tiles, N / (4 * hg::linear::kBk)));
+    w.splits = N <= 512 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(kWorkSms / tiles, N / (4 * hg::linear::kBk)));
     w.dz = (l->in % 8 != 0 ? realigned_bytes(l->out, l->in) : 0) + (ldx % 8 != 0 ? realigned_bytes(N, l->in) : 0);
     w.sums = w.dz + (l->act == HASHGRID_ACT_NONE && lddy % 8 == 0 ? 0 : align256((size_t)N * w.lddz * 2));
     w.dw = w.sums + align256((size_t)w.shares * l->out * sizeof(float));
@@ -1077,9 +1077,16 @@ int launch_linear_backward(const hashgrid_linear_s* l, const void* dy, int64_t l
     int nsums = 0;
     hl::Slope slope = {};
     if (convert || (db != nullptr && !inside)) {
-        slope.dy = dy;
-        slope.z = z;
-        slope.lddy = lddy;
+        slope.dy.p = dy;
+        slope.dy.bytes = strided_bytes(N, l->out, lddy, 2);
+        slope.dy.ld = lddy;
+        slope.dy.inner = l->out;
+        slope.dy.role = hg::kChkDout;
+        slope.z = slope.dy;
+        slope.z.p = z;
+        slope.z.bytes = strided_bytes(N, l->out, l->out, 2);
+        slope.z.ld = l->out;
+        slope.z.role = hg::kChkZ;
         slope.rows = N;
         slope.lddz = lw.lddz;
         slope.cols = l->out;
@@ -1112,7 +1119,9 @@ int launch_linear_backward(const hashgrid_linear_s* l, const void* dy, int64_t l
     const int sms = device_sms();
     Plan px = make_plan(N, l->in, l->out, sms), pw = make_plan(l->out, l->in, N, sms);
     if (lw.splits > 1) pw = Plan{wide_tile(l->in, 128), 1, lw.splits, false};
-    if (px.cluster == 2 && pw.cluster == 1) px.cluster = 1;
+    // Up to 16 steps of K one block takes for itself: sharing a launch saves more than splitting K does.
+    const bool short_x = ceil_div(l->out, hl::kBk) <= 16, short_w = ceil_div(N, hl::kBk) <= 16 || lw.splits > 1;
+    if (short_x && short_w && !px.pair && !pw.pair) px.cluster = pw.cluster = 1;
     const hl::Epilogue ex{nullptr, nullptr, dx, nullptr, 0, lddx, 0, dx_dtype == HASHGRID_F32, hl::kNoAct, hg::kChkOut};
     const bool parts = pw.splits > 1;
     const hl::Epilogue ew{nullptr, nullptr, parts ? out : dw, nullptr, 0, l->in, 0, parts || dw_dtype == HASHGRID_F32,

@@ -993,21 +993,49 @@ __device__ __forceinline__ void realign_block(const RealignList& l, int64_t bloc
     constexpr int kAtOnce = 4;
     const int64_t i0 = block * (256 * kAtOnce) + threadIdx.x;
     Chunk c[kAtOnce];
+    const bool second = i0 >= l.first;  // a block whose chunks lie in both arrays tells them apart below
+    const bool same = second == (i0 + 256 * (kAtOnce - 1) >= l.first) && i0 + 256 * (kAtOnce - 1) < l.total;
+    const Realign s = l.a[second];
+    const int64_t j0 = second ? i0 - l.first : i0;
+    auto place = [](int64_t j, int64_t chunks, int64_t& row, int& col) {
+        row = ((uint64_t)j >> 32) == 0 && chunks < (1 << 30) ? (int64_t)((uint32_t)j / (uint32_t)chunks) : j / chunks;
+        col = (int)(j - row * chunks) * 8;
+    };
+    int64_t last_row;
+    int last_col;
+    place(j0 + 256 * (kAtOnce - 1), s.chunks, last_row, last_col);
+    if (same && (((uint64_t)(last_row * s.ld + last_col) * 2) & ~15ull) + 32 <= s.bytes) {
+        // both units of every chunk lie inside the array: loads without guards, all under way before the first is used
+        const char* base = static_cast<const char*>(s.p);
 #pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) {
-        const int64_t i = i0 + 256 * u;
-        if (i >= l.total) continue;
-        const Realign& s = l.a[i >= l.first];
-        const int64_t j = i >= l.first ? i - l.first : i, row = j / s.chunks;
-        begin_chunk(s, row, (int)(j - row * s.chunks) * 8, c[u]);
+        for (int u = 0; u < kAtOnce; ++u) {
+            int64_t row;
+            int col;
+            place(j0 + 256 * u, s.chunks, row, col);
+            const uint64_t off = (uint64_t)(row * s.ld + col) * 2, at = off & ~15ull;
+            c[u].shift = (uint32_t)(off & 15u);
+            c[u].n = min(8, s.inner - col);
+            c[u].p = in_bounds_role(s.role, base + at, 16) ? __ldg(reinterpret_cast<const uint4*>(base + at)) : make_uint4(0u, 0u, 0u, 0u);
+            c[u].q = in_bounds_role(s.role, base + at + 16, 16) ? __ldg(reinterpret_cast<const uint4*>(base + at + 16)) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            uint16_t* to = s.to + 8 * (j0 + 256 * u);
+            if (in_bounds<kChkWork>(to, 16)) *reinterpret_cast<uint4*>(to) = finish_chunk(c[u]);
+        }
+        return;
     }
-#pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
         const int64_t i = i0 + 256 * u;
-        if (i >= l.total) continue;
-        const Realign& s = l.a[i >= l.first];
-        uint16_t* to = s.to + 8 * (i >= l.first ? i - l.first : i);
-        if (in_bounds<kChkWork>(to, 16)) *reinterpret_cast<uint4*>(to) = finish_chunk(c[u]);
+        if (i >= l.total) return;
+        const Realign& a = l.a[i >= l.first];
+        const int64_t j = i >= l.first ? i - l.first : i;
+        int64_t row;
+        int col;
+        place(j, a.chunks, row, col);
+        begin_chunk(a, row, col, c[0]);
+        uint16_t* to = a.to + 8 * j;
+        if (in_bounds<kChkWork>(to, 16)) *reinterpret_cast<uint4*>(to) = finish_chunk(c[0]);
     }
 }
 
@@ -1326,8 +1354,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
 // block's share of the rows into sums[share][col] (NULL: not wanted). A block takes up to 64 columns,
 // a thread eight neighbouring ones of every (256 / groups)-th row.
 struct Slope {
-    const void *dy, *z;
-    int64_t lddy, rows, lddz;
+    Realign dy, z;     // as sources
+    int64_t rows, lddz;
     int cols, act;
     void* dz;
     float* sums;
@@ -1340,48 +1368,85 @@ struct Slope {
 template <typename T, bool kVectors>
 __device__ __forceinline__ void slope_block(const Slope& a, int block) {
     __shared__ float part[8][64];
-    const T* dy = static_cast<const T*>(a.dy);
-    const T* z = static_cast<const T*>(a.z);
+    const T* dy = static_cast<const T*>(a.dy.p);
+    const T* z = static_cast<const T*>(a.z.p);
     T* dz = static_cast<T*>(a.dz);
     const int col_block = block % a.col_blocks, which = block / a.col_blocks, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = col_block * 64 + 8 * (threadIdx.x % a.groups), r = threadIdx.x / a.groups, step = 256 / a.groups;
     const int64_t share = (a.rows + a.shares - 1) / a.shares, r0 = which * share, r1 = min(a.rows, r0 + share);
     const int n = min(8, a.cols - col);
     float s[8] = {};
-    if (n > 0) {
-#pragma unroll 4
-        for (int64_t row = r0 + r; row < r1; row += step) {
-            float d[8], v[8];
-            if (kVectors) {
-                const T* p = dy + row * a.lddy + col;
-                const uint4 q = in_bounds<kChkDout>(p, 16) ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
-                const float2 d0 = unpack2<T>(q.x), d1 = unpack2<T>(q.y), d2 = unpack2<T>(q.z), d3 = unpack2<T>(q.w);
-                d[0] = d0.x; d[1] = d0.y; d[2] = d1.x; d[3] = d1.y; d[4] = d2.x; d[5] = d2.y; d[6] = d3.x; d[7] = d3.y;
-                if (a.act != kNoAct) {
-                    const T* pz = z + row * a.cols + col;
-                    const uint4 zq = in_bounds<kChkZ>(pz, 16) ? __ldg(reinterpret_cast<const uint4*>(pz)) : make_uint4(0u, 0u, 0u, 0u);
-                    const float2 z0 = unpack2<T>(zq.x), z1 = unpack2<T>(zq.y), z2 = unpack2<T>(zq.z), z3 = unpack2<T>(zq.w);
-                    v[0] = z0.x; v[1] = z0.y; v[2] = z1.x; v[3] = z1.y; v[4] = z2.x; v[5] = z2.y; v[6] = z3.x; v[7] = z3.y;
-                }
-            } else {
-                T dr[8], zr[8];
+    auto one = [&](int64_t row, uint4 q, uint4 zq) {
+        const float2 d0 = unpack2<T>(q.x), d1 = unpack2<T>(q.y), d2 = unpack2<T>(q.z), d3 = unpack2<T>(q.w);
+        float d[8] = {d0.x, d0.y, d1.x, d1.y, d2.x, d2.y, d3.x, d3.y};
+        if (a.act != kNoAct) {
+            const float2 z0 = unpack2<T>(zq.x), z1 = unpack2<T>(zq.y), z2 = unpack2<T>(zq.z), z3 = unpack2<T>(zq.w);
+            const float v[8] = {z0.x, z0.y, z1.x, z1.y, z2.x, z2.y, z3.x, z3.y};
+            times_slope(d, v, a.act);
+        }
+        // rows of dz are multiples of 8 wide: what lies between `cols` and that is zero
+        if (dz != nullptr && in_bounds<kChkWork>(dz + row * a.lddz + col, 16)) *reinterpret_cast<uint4*>(dz + row * a.lddz + col) = pack8<T>(d);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const T zero = from_float<T>(0.f);
-                    dr[j] = j < n && in_bounds<kChkDout>(dy + row * a.lddy + col + j, 2) ? dy[row * a.lddy + col + j] : zero;
-                    zr[j] = a.act != kNoAct && j < n && in_bounds<kChkZ>(z + row * a.cols + col + j, 2) ? z[row * a.cols + col + j] : zero;
-                }
+        for (int j = 0; j < 8; ++j) s[j] += d[j];
+    };
+    const uint4 nothing = make_uint4(0u, 0u, 0u, 0u);
+    int64_t row = n > 0 ? r0 + r : r1;
+    if (kVectors) {
+        auto load = [&](int64_t at, uint4& q, uint4& zq) {
+            const T* p = dy + at * a.dy.ld + col;
+            const T* pz = z + at * a.z.ld + col;
+            q = in_bounds<kChkDout>(p, 16) ? __ldg(reinterpret_cast<const uint4*>(p)) : nothing;
+            zq = a.act != kNoAct && in_bounds<kChkZ>(pz, 16) ? __ldg(reinterpret_cast<const uint4*>(pz)) : nothing;
+        };
+        for (; row + 3 * step < r1; row += 4 * step) {  // four rows' loads under way at a time
+            uint4 q[4], zq[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    d[j] = to_float(dr[j]);
-                    v[j] = to_float(zr[j]);
-                }
+            for (int k = 0; k < 4; ++k) load(row + k * step, q[k], zq[k]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) one(row + k * step, q[k], zq[k]);
+        }
+        for (; row < r1; row += step) {
+            uint4 q, zq;
+            load(row, q, zq);
+            one(row, q, zq);
+        }
+    } else {
+        // Several rows at a time while both 16-byte units that hold their elements lie inside the arrays: those loads need no
+        // guard, so that all of them are under way before the first is used.
+        constexpr int kRows = 4;
+        const char* by = static_cast<const char*>(a.dy.p);
+        const char* bz = static_cast<const char*>(a.z.p);
+        for (; row + (kRows - 1) * step < r1; row += kRows * step) {
+            const int64_t last = row + (kRows - 1) * step;
+            if ((((uint64_t)(last * a.dy.ld + col) * 2) & ~15ull) + 32 > a.dy.bytes ||
+                (a.act != kNoAct && (((uint64_t)(last * a.z.ld + col) * 2) & ~15ull) + 32 > a.z.bytes))
+                break;
+            Chunk c[kRows], cz[kRows];
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) {
+                const uint64_t off = (uint64_t)((row + k * step) * a.dy.ld + col) * 2, at = off & ~15ull;
+                c[k].shift = (uint32_t)(off & 15u);
+                c[k].n = n;
+                c[k].p = in_bounds<kChkDout>(by + at, 16) ? __ldg(reinterpret_cast<const uint4*>(by + at)) : nothing;
+                c[k].q = in_bounds<kChkDout>(by + at + 16, 16) ? __ldg(reinterpret_cast<const uint4*>(by + at + 16)) : nothing;
             }
-            if (a.act != kNoAct) times_slope(d, v, a.act);
-            // rows of dz are multiples of 8 wide: what lies between `cols` and that is zero
-            if (dz != nullptr && in_bounds<kChkWork>(dz + row * a.lddz + col, 16)) *reinterpret_cast<uint4*>(dz + row * a.lddz + col) = pack8<T>(d);
+            if (a.act != kNoAct)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s[j] += d[j];
+                for (int k = 0; k < kRows; ++k) {
+                    const uint64_t off = (uint64_t)((row + k * step) * a.z.ld + col) * 2, at = off & ~15ull;
+                    cz[k].shift = (uint32_t)(off & 15u);
+                    cz[k].n = n;
+                    cz[k].p = in_bounds<kChkZ>(bz + at, 16) ? __ldg(reinterpret_cast<const uint4*>(bz + at)) : nothing;
+                    cz[k].q = in_bounds<kChkZ>(bz + at + 16, 16) ? __ldg(reinterpret_cast<const uint4*>(bz + at + 16)) : nothing;
+                }
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) one(row + k * step, finish_chunk(c[k]), a.act != kNoAct ? finish_chunk(cz[k]) : nothing);
+        }
+        for (; row < r1; row += step) {
+            Chunk c, cz;
+            begin_chunk(a.dy, row, col, c);
+            if (a.act != kNoAct) begin_chunk(a.z, row, col, cz);
+            one(row, finish_chunk(c), a.act != kNoAct ? finish_chunk(cz) : nothing);
         }
     }
     if (a.sums == nullptr) return;
@@ -1429,17 +1494,28 @@ template <typename T>
 __global__ void __launch_bounds__(256) sum_parts_kernel(const __grid_constant__ SumsList l) {
     __shared__ float part[8][32];
     const bool second = (int)blockIdx.x >= l.blocks0;
-    const Sums& s = l.a[second];
+    const Sums s = l.a[second];  // in registers
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t i = (int64_t)(second ? blockIdx.x - l.blocks0 : blockIdx.x) * 32 + lane;
     float v = 0.f;
     after_previous_kernel();
     if (i < s.n) {
-#pragma unroll 16
-        for (int p = warp; p < s.count; p += 8) {
-            const float* at = s.parts + p * s.stride + i;
-            if (in_bounds<kChkWork>(at, 4)) v += __ldg(at);
+        const float* at = s.parts + i + warp * s.stride;
+        const int64_t step = 8 * s.stride;
+        int p = warp;
+        for (; p + 56 < s.count; p += 64, at += 8 * step) {  // eight loads under way at a time
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = in_bounds<kChkWork>(at + k * step, 4) ? __ldg(at + k * step) : 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v += x[k];
         }
+        float x[8] = {};
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (p + 8 * k < s.count && in_bounds<kChkWork>(at + k * step, 4)) x[k] = __ldg(at + k * step);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v += x[k];
     }
     part[warp][lane] = v;
     __syncthreads();
