@@ -605,7 +605,7 @@ size_t strided_bytes(int64_t rows, int64_t cols, int64_t ld, size_t elem) {
 // One strided array of a layer call: its row stride and then its extent.
 int check_rows(const void* p, int64_t rows, int64_t cols, int64_t ld, size_t elem, const char* name) {
     if (ld < cols) return fail(HASHGRID_ERR_ARG, "%s: row stride %lld is below its width %lld", name, (long long)ld, (long long)cols);
-    if (ld > ((int64_t)1 << 40)) return fail(HASHGRID_ERR_ARG, "%s: row stride %lld is too large", name, (long long)ld);
+    if (rows > 1 && ld >= ((int64_t)1 << 37)) return fail(HASHGRID_ERR_ARG, "%s: row stride %lld is too large", name, (long long)ld);
     return check_buffer(p, strided_bytes(rows, cols, ld, elem), name);
 }
 
@@ -710,7 +710,11 @@ int launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return launch_status(what);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(HASHGRID_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString(e));
+    }
     return ok();
 }
 
@@ -773,6 +777,7 @@ int set_map(CUtensorMap& map, const Array& a, int box_rows, const char* what) {
 int set_store_map(CUtensorMap& map, void* p, int64_t rows, int64_t cols, int64_t ld, int parts, bool f32, const char* what) {
     const cuuint64_t elem = f32 ? 4 : 2;
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
+    if (rows <= 1) ld = (cols + 7) / 8 * 8;  // no row follows
     const cuuint64_t strides[2] = {(cuuint64_t)ld * elem, (cuuint64_t)(parts > 1 ? rows * ld : ld) * elem};
     const cuuint32_t box[3] = {32, 32, 1}, ones[3] = {1, 1, 1};
     PFN_tensorMapEncodeTiled encode = tensor_map_fn();

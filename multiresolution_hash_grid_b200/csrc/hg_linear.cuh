@@ -118,6 +118,12 @@ __device__ __forceinline__ void activate(float (&y)[kN], int act) {
     }
 }
 
+// z within +-bound: the slopes are 0 or 1 to the last place there, where an infinite z (one that overflowed its 16 bits)
+// would make 0 times infinity. A NaN stays one.
+__device__ __forceinline__ float2 within(float2 z, float bound) {
+    return make_float2(z.x > bound ? bound : z.x < -bound ? -bound : z.x, z.y > bound ? bound : z.y < -bound ? -bound : z.y);
+}
+
 // d[j] act'(z[j]). GELU: Phi(z) + z phi(z); SILU: s (1 + z (1 - s)).
 template <int kN>
 __device__ __forceinline__ void times_slope(float (&d)[kN], const float (&z)[kN], int act) {
@@ -129,7 +135,7 @@ __device__ __forceinline__ void times_slope(float (&d)[kN], const float (&z)[kN]
         case kGelu:
 #pragma unroll
             for (int j = 0; j < kN; j += 2) {
-                const float2 v = make_float2(z[j], z[j + 1]), a = magnitude(v);
+                const float2 v = within(make_float2(z[j], z[j + 1]), 64.f), a = magnitude(v);
                 float2 e;
                 const float2 q = upper_tail(a, e);
                 const float2 cdf = make_float2(v.x > 0.f ? 1.f - q.x : q.x, v.y > 0.f ? 1.f - q.y : q.y);
@@ -141,7 +147,7 @@ __device__ __forceinline__ void times_slope(float (&d)[kN], const float (&z)[kN]
         case kSilu:
 #pragma unroll
             for (int j = 0; j < kN; j += 2) {
-                const float2 v = make_float2(z[j], z[j + 1]), s = sigmoid2(v);
+                const float2 v = within(make_float2(z[j], z[j + 1]), 80.f), s = sigmoid2(v);
                 const float2 r = mul2(s, fma2(v, fma2(s, both(-1.f), both(1.f)), both(1.f)));
                 d[j] *= r.x;
                 d[j + 1] *= r.y;
@@ -390,6 +396,8 @@ struct Gemm {
 
 // One launch computes one product or two that do not depend on each other (dx and dW): blocks from
 // `second` on take the second.
+// (Blocks of this kernel take 83 KB of shared memory or more, so that at most two share an SM, and at most 256 columns
+// of tensor memory where two can: no block ever waits for another launch's columns while its own cluster waits for it.)
 struct Gemms {
     Gemm of[2];
     int second;

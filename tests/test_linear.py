@@ -13,6 +13,8 @@ of one rounding; its subnormals are absolute, 2^-25 for fp16):
 """
 import ctypes
 import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -250,6 +252,40 @@ def test_values_that_are_not_finite_stay_in_their_rows():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("act", [hg.HASHGRID_ACT_RELU, hg.HASHGRID_ACT_GELU, hg.HASHGRID_ACT_SILU])
+@pytest.mark.parametrize("N", [40, 9000])
+def test_gradients_at_the_ends_of_the_range(act, N):
+    """z at and beyond what 16 bits hold: the slope is 1 above, 0 below; a NaN stays in its row (relu's slope there is 0)."""
+    z = torch.zeros(N, 16, device="cuda", dtype=torch.float16)
+    z[:, 0], z[:, 1], z[:, 2], z[:, 3] = 65504.0, -65504.0, float("inf"), float("-inf")
+    z[3, 4] = float("nan")
+    dy = torch.ones_like(z)
+    x, w = torch.ones(N, 8, device="cuda").half(), torch.eye(16, 8, device="cuda").half()
+    dx, dw, db = hg.Linear(8, 16, hg.HASHGRID_F16, act).backward(dy, x, w, z=z)
+    want = torch.tensor([1.0, 0.0, 1.0, 0.0], device="cuda")
+    # z enters the slope as at most 80 in size, where silu's is 80 exp(-80) = 1.4e-33 off at most
+    assert torch.equal(dx[0, :4].float(), want) and float((db[:4] - want * N).abs().max()) <= 1.5e-33 * N
+    assert torch.equal(dw[:4], (want * N)[:, None].expand(4, 8))      # of the rounded dz
+    nan = act != hg.HASHGRID_ACT_RELU
+    assert bool(torch.isnan(dx[3, 4])) == nan and bool(torch.isnan(db[4])) == nan and not bool(torch.isnan(db[5:]).any())
+    assert not bool(torch.isnan(dx[:3]).any()) and not bool(torch.isnan(dx[4:]).any())
+
+
+@pytest.mark.gpu
+def test_one_row_with_any_stride():
+    """A single row's stride means nothing: a large or an odd one is taken all the same."""
+    layer = hg.Linear(24, 40)
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    x, w = torch.randn(1, 24, device="cuda", generator=gen).bfloat16(), torch.randn(40, 24, device="cuda", generator=gen).bfloat16()
+    want = layer.forward(x, w)
+    for ld in (24, 41, 1 << 20, (1 << 36) + 1, 1 << 45):
+        y = torch.zeros(1, 40, device="cuda", dtype=torch.bfloat16)
+        work = torch.zeros(1 << 16, device="cuda", dtype=torch.uint8)
+        hg.hashgrid_linear_forward(layer.handle, x, ld, 1, w, None, None, 0, y, max(ld, 40), hg.HASHGRID_BF16, None, work, 1 << 16)
+        assert torch.equal(y, want), ld
+
+
+@pytest.mark.gpu
 def test_residual_in_place_and_slices_of_one_buffer():
     """y = act(x w^T) + y, and x and y side by side in one buffer (a concatenation)."""
     gen = torch.Generator(device="cuda").manual_seed(6)
@@ -387,6 +423,20 @@ def test_training_step_of_an_encoder_with_its_head():
     assert torch.equal(w1, master[0].bfloat16()) and torch.equal(w2, master[2].bfloat16())
     assert all(int(g.count_nonzero()) == 0 for g in grads)
     assert bool(torch.isfinite(dtable).all()) and int(dtable.count_nonzero()) > 0
+
+
+@pytest.mark.gpu
+@pytest.mark.timeout(900)
+def test_layers_and_optimiser_under_the_checked_build():
+    """These tests and those of the optimiser once more with every plain access range-checked (TMA copies are held to
+    their arrays by their tensor maps)."""
+    if hg.CHECKED:
+        pytest.skip("this is the checked build")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-m", "pytest", "tests/test_linear.py", "tests/test_adamw.py", "-m", "gpu", "-q", "-x",
+                        "-p", "no:cacheprovider"], cwd=root, env=dict(os.environ, HASHGRID_CHECKED="1"), capture_output=True,
+                       text=True, timeout=800)
+    assert r.returncode == 0 and " passed" in r.stdout, r.stdout[-3000:] + r.stderr[-2000:]
 
 
 def test_refusals():
