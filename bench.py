@@ -30,7 +30,6 @@ bounded sample of the same workload, on rank 0 only.
 from __future__ import annotations
 
 import argparse
-import glob
 import hashlib
 import json
 import os
@@ -146,9 +145,13 @@ def measure_l2_peaks(device) -> dict:
     return out
 
 
+# The files whose kernels the committed captures measured.
+PROFILED_SOURCES = ("hg_device.cuh", "hg_mlp.cuh", "hg_nd.cuh", "hg_probe.cuh")
+
+
 def csrc_digest() -> str:
     h = hashlib.sha256()
-    files = sorted(glob.glob(os.path.join(ROOT, "multiresolution_hash_grid_b200", "csrc", "*")))
+    files = [os.path.join(ROOT, "multiresolution_hash_grid_b200", "csrc", f) for f in PROFILED_SOURCES]
     for f in files:
         with open(f, "rb") as fh:
             h.update(os.path.basename(f).encode() + fh.read())
