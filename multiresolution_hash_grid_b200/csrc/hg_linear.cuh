@@ -604,53 +604,52 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
 
     if (warp == kOutWarps + 1) {
         // ------------------------------- TMA copies -------------------------------
-        if (lane == 0) {
-            const uint32_t bytes = g.a.bytes + (g.resident ? 0 : g.b.bytes);
-            if (g.resident && kbs > 0) {
-                arrive_expect(bfull, kept);
-                for (int kb = 0; kb < g.kblocks; ++kb)
-                    for (int j = 0; j < g.b.boxes; ++j)
-                        tma_load(sb0 + kb * g.b.bytes + j * g.b.box_rows * 128, &g.tb, g.b.mn ? 64 * j : kb * kBk, g.b.mn ? kb * kBk : 0, bfull);
-            }
-            Ring r;
-            uint32_t issued = 0;  // copies so far, at most counted to the number of stages
-            bool ok = true;
-            for (Tiles t(g, first, step); t.more() && ok; t.next()) {
-                const int m0 = (kPair ? 2 * t.m + (int)rank : t.m) * kBm, n0 = t.n * g.bn + (kPair ? (int)rank * (g.bn / 2) : 0);
-                for (int kb = 0; kb < kbs; ++kb) {
-                    if (!(ok = wait_bounded(empty + 8 * r.stage, r.phase ^ 1u, &abort_flag))) break;
-                    const uint32_t bar = kPair ? cluster_address(full + 8 * r.stage, 0) : full + 8 * r.stage;
-                    const uint32_t sa = sm0 + r.stage * g.stage_bytes, sb = sa + g.a.bytes;
-                    const int k0 = (kb0 + kb) * kBk;
-                    if (!kPair) arrive_expect(bar, bytes);
-                    else if (rank == 0) arrive_expect(full + 8 * r.stage, 2 * bytes);  // both blocks' copies
-                    for (int j = 0; j < g.a.boxes; ++j) {
-                        const uint32_t dst = sa + j * g.a.box_rows * 128;
-                        const int x = g.a.mn ? m0 + 64 * j : k0, y = g.a.mn ? k0 : m0;
-                        if (kPair) tma_load_pair(dst, &g.ta, x, y, bar);
-                        else tma_load(dst, &g.ta, x, y, bar);
-                    }
-                    if (!g.resident)
-                        for (int j = 0; j < g.b.boxes; ++j) {
-                            const uint32_t dst = sb + j * g.b.box_rows * 128;
-                            const int x = g.b.mn ? n0 + 64 * j : k0, y = g.b.mn ? k0 : n0;
-                            if (kPair) tma_load_pair(dst, &g.tb, x, y, bar);
-                            else tma_load(dst, &g.tb, x, y, bar);
-                        }
-                    r.next(g.stages);
-                    issued = min(issued + 1, (uint32_t)g.stages);
+        // (as in the MMA warp, all lanes walk and one issues)
+        const bool issues = elect_one();
+        const uint32_t bytes = g.a.bytes + (g.resident ? 0 : g.b.bytes);
+        if (g.resident && kbs > 0 && issues) {
+            arrive_expect(bfull, kept);
+            for (int kb = 0; kb < g.kblocks; ++kb)
+                for (int j = 0; j < g.b.boxes; ++j)
+                    tma_load(sb0 + kb * g.b.bytes + j * g.b.box_rows * 128, &g.tb, g.b.mn ? 64 * j : kb * kBk, g.b.mn ? kb * kBk : 0, bfull);
+        }
+        Ring r;
+        uint32_t issued = 0;  // copies so far, at most counted to the number of stages
+        bool ok = true;
+        const int a_boxes = g.a.boxes, b_boxes = g.resident ? 0 : g.b.boxes, a_step = g.a.box_rows * 128, b_step = g.b.box_rows * 128;
+        const bool a_mn = g.a.mn != 0, b_mn = g.b.mn != 0;
+        const uint32_t full0 = kPair ? cluster_address(full, 0) : full;
+        for (Tiles t(g, first, step); t.more() && ok; t.next()) {
+            const int m0 = (kPair ? 2 * t.m + (int)rank : t.m) * kBm, n0 = t.n * g.bn + (kPair ? (int)rank * (g.bn / 2) : 0);
+            for (int kb = 0; kb < kbs; ++kb) {
+                if (!(ok = wait_bounded(empty + 8 * r.stage, r.phase ^ 1u, &abort_flag))) break;
+                const uint32_t bar = full0 + 8 * r.stage, sa = sm0 + r.stage * g.stage_bytes, sb = sa + g.a.bytes;
+                const int k0 = (kb0 + kb) * kBk;
+                if (!kPair && issues) arrive_expect(bar, bytes);
+                if (kPair && rank == 0 && issues) arrive_expect(full + 8 * r.stage, 2 * bytes);  // both blocks' copies
+                for (int j = 0; j < a_boxes; ++j) {
+                    const int x = a_mn ? m0 + 64 * j : k0, y = a_mn ? k0 : m0;
+                    if (kPair && issues) tma_load_pair(sa + j * a_step, &g.ta, x, y, bar);
+                    if (!kPair && issues) tma_load(sa + j * a_step, &g.ta, x, y, bar);
                 }
-            }
-            // given up: the copies in flight still write to this block's shared memory
-            if (!ok && g.resident && kbs > 0) mlp::wait_parity(bfull, 0);
-            for (; !ok && issued > 0; --issued) {
-                if (r.stage == 0) {
-                    r.stage = g.stages;
-                    r.phase ^= 1u;
+                for (int j = 0; j < b_boxes; ++j) {
+                    const int x = b_mn ? n0 + 64 * j : k0, y = b_mn ? k0 : n0;
+                    if (kPair && issues) tma_load_pair(sb + j * b_step, &g.tb, x, y, bar);
+                    if (!kPair && issues) tma_load(sb + j * b_step, &g.tb, x, y, bar);
                 }
-                --r.stage;
-                mlp::wait_parity(full + 8 * r.stage, r.phase);
+                r.next(g.stages);
+                issued = min(issued + 1, (uint32_t)g.stages);
             }
+        }
+        // given up: the copies in flight still write to this block's shared memory
+        if (!ok && g.resident && kbs > 0) mlp::wait_parity(bfull, 0);
+        for (; !ok && issued > 0; --issued) {
+            if (r.stage == 0) {
+                r.stage = g.stages;
+                r.phase ^= 1u;
+            }
+            --r.stage;
+            mlp::wait_parity(full + 8 * r.stage, r.phase);
         }
     } else if (warp == kOutWarps) {
         // ---------------------------------- MMAs ----------------------------------
