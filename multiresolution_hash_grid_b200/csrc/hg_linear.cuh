@@ -1135,35 +1135,36 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
 
     if (warp == 9) {
         // ------------------------------- TMA copies -------------------------------
-        if (lane == 0) {
-            bool ok = true;
-            if (dx) {
-                arrive_expect(wfull, g.w_bytes);
-                for (int j = 0; j < g.boxes_in; ++j) tma_load(w0 + j * g.k_out * 128, &g.tw, 64 * j, 0, wfull);
-            }
-            Ring r;
-            int issued = 0;
-            for (int i = 0; i < mine; ++i) {
-                if (!(ok = wait_bounded(empty + 8 * r.stage, r.phase ^ 1u, &abort_flag))) break;
-                const uint32_t bar = full + 8 * r.stage, s = sm0 + r.stage * g.stage_bytes;
-                const int m0 = (int)(blockIdx.x + (int64_t)i * gridDim.x) * kBm;
+        const bool issues = elect_one();
+        bool ok = true;
+        if (dx && issues) {
+            arrive_expect(wfull, g.w_bytes);
+            for (int j = 0; j < g.boxes_in; ++j) tma_load(w0 + j * g.k_out * 128, &g.tw, 64 * j, 0, wfull);
+        }
+        Ring r;
+        int issued = 0;
+        for (int i = 0; i < mine; ++i) {
+            if (!(ok = wait_bounded(empty + 8 * r.stage, r.phase ^ 1u, &abort_flag))) break;
+            const uint32_t bar = full + 8 * r.stage, s = sm0 + r.stage * g.stage_bytes;
+            const int m0 = (int)(blockIdx.x + i * gridDim.x) * kBm;
+            if (issues) {
                 arrive_expect(bar, g.stage_bytes);
                 for (int j = 0; j < g.boxes_out; ++j) tma_load(s + j * kBox, &g.tdy, 64 * j, m0, bar);
                 if (g.act != kNoAct)
                     for (int j = 0; j < g.boxes_out; ++j) tma_load(s + z_at + j * kBox, &g.tz, 64 * j, m0, bar);
                 for (int j = 0; j < g.boxes_in; ++j) tma_load(s + x_at + j * kBox, &g.tx, 64 * j, m0, bar);
-                r.next(g.stages);
-                issued = min(issued + 1, g.stages);
             }
-            if (!ok && dx) mlp::wait_parity(wfull, 0);
-            for (; !ok && issued > 0; --issued) {  // copies in flight still write to this block's memory
-                if (r.stage == 0) {
-                    r.stage = g.stages;
-                    r.phase ^= 1u;
-                }
-                --r.stage;
-                mlp::wait_parity(full + 8 * r.stage, r.phase);
+            r.next(g.stages);
+            issued = min(issued + 1, g.stages);
+        }
+        if (!ok && dx) mlp::wait_parity(wfull, 0);
+        for (; !ok && issued > 0; --issued) {  // copies in flight still write to this block's memory
+            if (r.stage == 0) {
+                r.stage = g.stages;
+                r.phase ^= 1u;
             }
+            --r.stage;
+            mlp::wait_parity(full + 8 * r.stage, r.phase);
         }
     } else if (warp == 8) {
         // ---------------------------------- MMAs ----------------------------------
