@@ -54,10 +54,12 @@ struct hashgrid_linear_s {
 
 struct hashgrid_adamw_s {
     int device;
-    std::vector<hg::adamw::Tensor> tensors;  // `first` counts blocks within the tensor's launch
+    std::vector<hg::adamw::Tensor> tensors;
+    std::vector<uint32_t> first;  // the tensors' first blocks within their launches
     struct Launch {
         int begin, count;  // tensors
         uint32_t blocks;   // of 256 elements
+        hg::adamw::Buckets where;
     };
     std::vector<Launch> launches;
 };
@@ -1217,7 +1219,9 @@ int launch_adamw(const hashgrid_adamw_s* o, const hashgrid_adamw_s::Launch& l, h
     hg::adamw::List<kCap> list;
     list.count = (uint32_t)l.count;
     list.blocks = l.blocks;
+    list.where = l.where;
     std::memcpy(list.t, o->tensors.data() + l.begin, sizeof(hg::adamw::Tensor) * l.count);
+    std::memcpy(list.first, o->first.data() + l.begin, sizeof(uint32_t) * l.count);
     for (int i = 0; i < l.count; ++i) {
         const float lr_scale = list.t[i].rate, decay = list.t[i].keep;
         list.t[i].rate = lr_scale * a.lr;
@@ -1737,7 +1741,7 @@ int hashgrid_adamw_create(const hashgrid_adamw_tensor* tensors, int count, hashg
                 d.vs = t.v_scale;
                 d.copy = t.copy;
                 d.n = t.n;
-                d.first = first;
+                o->first.push_back(first);
                 d.types = (uint32_t)t.param_dtype | (uint32_t)t.grad_dtype << 4 | (uint32_t)t.state_dtype << 8 |
                           (uint32_t)(t.copy ? t.copy_dtype : (int)hg::adamw::kNone) << 12 | (uint32_t)k << 16;
                 d.rate = t.lr_scale;
@@ -1745,7 +1749,14 @@ int hashgrid_adamw_create(const hashgrid_adamw_tensor* tensors, int count, hashg
                 o->tensors.push_back(d);
                 first += (uint32_t)blocks_of(t.n);
             }
-            if (have > 0) o->launches.push_back({begin, have, (uint32_t)blocks});
+            if (have == 0) continue;
+            hashgrid_adamw_s::Launch l{begin, have, (uint32_t)blocks, {}};
+            while ((blocks - 1) >> l.where.shift >= (uint64_t)hg::adamw::kBuckets) ++l.where.shift;
+            for (int j = 0, at = 0; j < hg::adamw::kBuckets + 2; ++j) {
+                while (at + 1 < have && o->first[begin + at + 1] <= (uint64_t)j << l.where.shift) ++at;
+                l.where.tensor[j] = (uint16_t)at;
+            }
+            o->launches.push_back(l);
         }
     } catch (const std::bad_alloc&) {
         delete *opt;

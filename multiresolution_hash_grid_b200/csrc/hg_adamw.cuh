@@ -45,7 +45,6 @@ struct Tensor {
     float* vs;
     void* copy;
     int64_t n;
-    uint32_t first;   // index of the tensor's first 256-element block in the launch
     uint32_t types;   // param | grad << 4 | state << 8 | copy << 12 | place in the caller's list << 16
     float rate, keep;  // lr * lr_scale, 1 - rate * weight_decay (in the handle: lr_scale and weight_decay)
 };
@@ -59,10 +58,20 @@ struct Params {
 };
 
 // Lists of up to kSmall tensors take less kernel-parameter space than long ones.
-constexpr int kSmall = 40, kLarge = 400;
+constexpr int kSmall = 40, kLarge = 380;
+// Where a block's tensor is searched for: block b >> shift's entry is the last tensor that begins at or before the
+// bucket. (Searching the whole list took 7 of 48 us of a step with 8-bit states over 160 tensors.)
+constexpr int kBuckets = 128;
+struct Buckets {
+    uint32_t shift;
+    uint16_t tensor[kBuckets + 2];
+};
+
 template <int kCap>
 struct List {
     uint32_t count, blocks;
+    uint32_t first[kCap];  // index of a tensor's first 256-element block
+    Buckets where;
     Tensor t[kCap];
 };
 
@@ -369,10 +378,11 @@ __global__ void __launch_bounds__(32 * kWarps, 4) step_kernel(const __grid_const
     const int lane = threadIdx.x & 31;
     const uint32_t b = blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (b >= list.blocks) return;
-    uint32_t lo = 0, hi = list.count;  // the last tensor whose first block is at most b
+    uint32_t lo = list.where.tensor[b >> list.where.shift], hi = list.where.tensor[(b >> list.where.shift) + 1] + 1u;
+    // the last tensor whose first block is at most b: lo or one up to, not including, hi
     while (hi - lo > 1) {
         const uint32_t mid = (lo + hi) / 2;
-        if (list.t[mid].first <= b) lo = mid; else hi = mid;
+        if (list.first[mid] <= b) lo = mid; else hi = mid;
     }
     after_previous_kernel();
     Rates r{a.c1, a.root2, a.step};
@@ -384,7 +394,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) step_kernel(const __grid_const
         r.root2 = (float)sqrt(1.0 / (1.0 - pow(a.db2, (double)t)));
     }
     const Tensor& T = list.t[lo];
-    const int64_t blk = b - T.first;
+    const int64_t blk = b - list.first[lo];
     if ((blk + 1) * kBlock > T.n) return step_block<-1, -1, -1, false>(T, a, r, blk, lane);
     switch (T.types & 0xfffu) {
 #define HG_ADAMW_CASE(P, G, S) \
