@@ -97,7 +97,7 @@ __device__ __forceinline__ void activate(float (&y)[kN], int act) {
     switch (act) {
         case kRelu:
 #pragma unroll
-            for (int j = 0; j < kN; ++j) y[j] = y[j] > 0.f ? y[j] : 0.f;
+            for (int j = 0; j < kN; ++j) y[j] = fmaxf(y[j], 0.f);  // of a NaN and 0 it returns 0
             break;
         case kGelu:
 #pragma unroll

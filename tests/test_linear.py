@@ -75,25 +75,25 @@ def check_forward(N, K, M, dtype, act, bias=True, residual=True, keep=True, y32=
     w = (torch.randn(M, K, device="cuda", generator=gen) / K ** 0.5).to(t)
     b = torch.randn(M, device="cuda", generator=gen) if bias else None
     r = rows_of(N, M, pad, yt, gen) if residual else None
-    ybuf = torch.full((N, M + pad), 7.0, device="cuda", dtype=yt)
+    ybuf = torch.full((N + 40, M + pad), 7.0, device="cuda", dtype=yt)      # rows behind the last one stay too
     zbuf = torch.full((N * M + 64,), 7.0, device="cuda", dtype=t)
     z = zbuf[:N * M].view(N, M) if keep else None
     layer = hg.Linear(K, M, dtype, act)
     status = torch.zeros(4, dtype=torch.int32, device="cuda")
     need = hg.hashgrid_linear_forward_workspace(layer.handle, N, K + pad if N > 1 else K)
     work = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")   # NaN, whatever is read from it
-    layer.forward(x, w, b, residual=r, y=ybuf[:, :M], z=z, workspace=work[:max(16, need)], device_status=status)
+    layer.forward(x, w, b, residual=r, y=ybuf[:N, :M], z=z, workspace=work[:max(16, need)], device_status=status)
     torch.cuda.synchronize()
     assert int(status[0]) == 0
     assert bool((work[need:] == 0xFF).all())
-    assert bool((ybuf[:, M:] == 7.0).all()) and bool((zbuf[N * M:] == 7.0).all())
+    assert bool((ybuf[:, M:] == 7.0).all()) and bool((ybuf[N:] == 7.0).all()) and bool((zbuf[N * M:] == 7.0).all())
     X, W = x.double(), w.double()
     z64 = X @ W.t() + (b.double() if bias else 0)
     S = 2 * U * (K + 2) * (X.abs() @ W.abs().t()) + 2 * U * z64.abs()
     a64 = act64(z64, act)
     y64 = a64 + (r.double() if residual else 0)
     e, absolute = half_step(yt)
-    close(ybuf[:, :M], y64, 1.13 * S + 16 * U * (z64.abs() + 1) + 2 * U * y64.abs() + e * y64.abs() * 1.01 + absolute, "y")
+    close(ybuf[:N, :M], y64, 1.13 * S + 16 * U * (z64.abs() + 1) + 2 * U * y64.abs() + e * y64.abs() * 1.01 + absolute, "y")
     if keep:
         e, absolute = half_step(t)
         close(z, z64, S + e * (z64.abs() + S) + absolute, "z")
@@ -108,19 +108,19 @@ def check_backward(N, K, M, dtype, act, dx32=False, dw32=True, pad=0, seed=0, wa
     z = torch.randn(N, M, device="cuda", generator=gen).to(t)
     z[::3, ::2] = 0.0                        # the kink itself: relu's slope there is 0
     xt, wt = torch.float32 if dx32 else t, torch.float32 if dw32 else t
-    dxbuf = torch.full((N, K + pad), 7.0, device="cuda", dtype=xt)
+    dxbuf = torch.full((N + 40, K + pad), 7.0, device="cuda", dtype=xt)
     dw = torch.full((M, K), 7.0, device="cuda", dtype=wt)
     db = torch.full((M,), 7.0, device="cuda")
     layer = hg.Linear(K, M, dtype, act)
     status = torch.zeros(4, dtype=torch.int32, device="cuda")
     need = hg.hashgrid_linear_backward_workspace(layer.handle, N, M + pad if N > 1 else M, K + pad if N > 1 else K)
     work = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")   # NaN, whatever is read from it
-    layer.backward(dy, x, w, z=None if act == hg.HASHGRID_ACT_NONE else z, dL_dx=dxbuf[:, :K] if want[0] else None,
+    layer.backward(dy, x, w, z=None if act == hg.HASHGRID_ACT_NONE else z, dL_dx=dxbuf[:N, :K] if want[0] else None,
                    dL_dw=dw if want[1] else None, dL_db=db if want[2] else None, workspace=work[:max(16, need)],
                    device_status=status)
     torch.cuda.synchronize()
     assert int(status[0]) == 0
-    assert bool((work[need:] == 0xFF).all()) and bool((dxbuf[:, K:] == 7.0).all())
+    assert bool((work[need:] == 0xFF).all()) and bool((dxbuf[:, K:] == 7.0).all()) and bool((dxbuf[N:] == 7.0).all())
     X, W, DY, Z = x.double(), w.double(), dy.double(), z.double()
     dz = DY * slope64(Z, act)
     e, absolute = half_step(t)
@@ -128,7 +128,7 @@ def check_backward(N, K, M, dtype, act, dx32=False, dw32=True, pad=0, seed=0, wa
     raw = (32 * U * (1 + Z.abs()) * DY.abs()) if smooth else torch.zeros_like(dz)
     err = raw + (e * dz.abs() * 1.01 + absolute) if smooth else raw
     for on, got, ref, mag, carried, terms, name in (
-            (want[0], dxbuf[:, :K], dz @ W, dz.abs() @ W.abs(), err @ W.abs(), M, "dx"),
+            (want[0], dxbuf[:N, :K], dz @ W, dz.abs() @ W.abs(), err @ W.abs(), M, "dx"),
             (want[1], dw, dz.t() @ X, dz.abs().t() @ X.abs(), err.t() @ X.abs(), N, "dw"),
             (want[2], db, dz.sum(0), dz.abs().sum(0), raw.sum(0), N, "db")):
         if not on:
@@ -379,6 +379,51 @@ def test_streams_and_graphs():
     again = [yr, *layer.backward(dys, xs, w, z=z)]
     for _, out, *_ in graphs:
         assert all(torch.equal(a, b) for a, b in zip(out, again))
+
+
+@pytest.mark.gpu
+@pytest.mark.skipif(hg.CHECKED, reason="the checked build is for one stream at a time")
+def test_calls_on_several_streams_at_once():
+    """Wide products, products split over clusters, narrow layers' backward passes, optimiser steps and the fixed head on
+    streams of their own, all at once and many times over, give what they give alone: they share SMs, their shared
+    memory and their tensor memory."""
+    gen = torch.Generator(device="cuda").manual_seed(14)
+
+    def rand(*shape):
+        return torch.randn(*shape, device="cuda", generator=gen).bfloat16()
+    jobs = []
+    for N, K, M, act in ((6000, 1024, 1536, hg.HASHGRID_ACT_GELU), (16, 2048, 1024, hg.HASHGRID_ACT_NONE), (20000, 64, 64, hg.HASHGRID_ACT_RELU),
+                         (333, 77, 130, hg.HASHGRID_ACT_SILU), (40, 4096, 264, hg.HASHGRID_ACT_NONE)):
+        layer, x, w, dy = hg.Linear(K, M, activation=act), rand(N, K), rand(M, K), rand(N, M)
+        z, work = rand(N, M), layer.workspace(N, "cuda")
+        out = [torch.empty(N, M, device="cuda", dtype=torch.bfloat16), torch.empty(N, K, device="cuda"), torch.empty(M, K, device="cuda"),
+               torch.empty(M, device="cuda")]
+
+        def job(layer=layer, x=x, w=w, dy=dy, z=z, work=work, out=out, act=act):
+            layer.forward(x, w, y=out[0], workspace=work)
+            layer.backward(dy, x, w, z=None if act == hg.HASHGRID_ACT_NONE else z, dL_dx=out[1], dL_dw=out[2], dL_db=out[3], workspace=work)
+        jobs.append((job, out))
+    grid = hg.HashGrid(16, 2, 14, 16, 512)
+    table, pts = torch.rand(16, 1 << 14, 2, device="cuda", generator=gen), torch.rand(50000, 3, device="cuda", generator=gen)
+    ws, bs, y = [rand(o, i) for o, i in ((64, 32), (64, 64), (4, 64))], [torch.zeros(64, device="cuda")] * 3, torch.empty(50000, 4, device="cuda")
+    jobs.append((lambda: hg.hashgrid_mlp_forward(grid.handle, pts, 50000, table, ws[0], bs[0], ws[1], bs[1], ws[2], bs[2], y), [y]))
+    alone = []
+    for job, out in jobs:
+        job()
+        torch.cuda.synchronize()
+        alone.append([t.clone() for t in out])
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _, out in jobs:
+        for t in out:
+            t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for (job, _), s in zip(jobs, streams):
+            with torch.cuda.stream(s):
+                job()
+    torch.cuda.synchronize()
+    for (_, out), want in zip(jobs, alone):
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
 
 
 @pytest.mark.gpu
