@@ -489,13 +489,14 @@ int hashgrid_adamw_destroy(hashgrid_adamw_t opt);
 
 /*
  * hashgrid_adamw_step -- one AdamW step (decoupled weight decay) over all tensors of the list.
- * Per element, in fp32, each operation on m and v rounded to nearest, at step t >= 1:
+ * Per element, in fp32, each operation on m and v (its root included) rounded to nearest, at
+ * step t >= 1:
  *   m = beta1 m + (1 - beta1) g;   v = beta2 v + (1 - beta2) g^2;
  *   param = param (1 - lr lr_scale weight_decay)
  *           - lr lr_scale (m / (1 - beta1^t)) / (sqrt(v) / sqrt(1 - beta2^t) + eps).
  * (1 / (1 - beta1^t) and sqrt(1 / (1 - beta2^t)) are computed in fp64 and multiplied as fp32; the
- * root and the quotient are off by at most 2 units in the last place.) Unlike
- * hashgrid_adam_step, elements with a zero gradient decay too.
+ * quotient is off by at most 2 units in the last place.) Unlike hashgrid_adam_step, elements
+ * with a zero gradient decay too.
  *
  * 8-bit states (HASHGRID_E4M3): m is stored as codes c with m = c * m_scale[i / 256], v as
  * codes of its square root, v = (c * v_scale[i / 256])^2, which halves the range that its 8
