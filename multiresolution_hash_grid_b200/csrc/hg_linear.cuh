@@ -396,8 +396,9 @@ struct Gemm {
 
 // One launch computes one product or two that do not depend on each other (dx and dW): blocks from
 // `second` on take the second.
-// (Blocks of this kernel take 83 KB of shared memory or more, so that at most two share an SM, and at most 256 columns
-// of tensor memory where two can: no block ever waits for another launch's columns while its own cluster waits for it.)
+// (Blocks with more than 64 columns of tensor memory take 100 KB of shared memory or more, so that two of them share an
+// SM at most, and have 256 columns at most where two can; the others take 66 KB or more. So the columns of the
+// blocks on an SM always fit, and no block waits for another launch's while its own cluster waits for it.)
 struct Gemms {
     Gemm of[2];
     int second;

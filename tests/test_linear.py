@@ -197,6 +197,16 @@ def test_narrow_layers_over_many_rows(K, M):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N,K,M", [(19100, 512, 160), (9700, 520, 300), (9601, 1000, 417), (19001, 777, 224), (5000, 1600, 1030)])
+def test_wide_products(N, K, M):
+    """256-row tiles of every width, even and odd, with 16- and 32-bit results."""
+    check_forward(N, K, M, hg.HASHGRID_BF16, hg.HASHGRID_ACT_SILU, pad=8)
+    check_forward(N, K, M, hg.HASHGRID_F16, hg.HASHGRID_ACT_NONE, residual=False, y32=True)
+    check_backward(N, M, K, hg.HASHGRID_BF16, hg.HASHGRID_ACT_NONE, dx32=True)
+    check_backward(N, K, M, hg.HASHGRID_BF16, hg.HASHGRID_ACT_GELU, dw32=False, pad=8)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("N,K,M", [(4096, 4096, 2048), (300, 8200, 264), (64, 30000, 72), (40, 5000, 37)])
 def test_long_sums_in_fp32(N, K, M):
     """fp32 results of sums over thousands of terms: the tensor cores' truncating additions alone would be off by 1e-9 a
