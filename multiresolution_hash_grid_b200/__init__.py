@@ -440,10 +440,7 @@ class Linear:
         if b is not None:
             _flat(b, self._bias_shape, self._f32, "b")
         if y is None:
-            import torch
-            y = torch.empty((N, self.out_features), device=x.device,
-                            dtype=self._own[0] if residual is None else residual.dtype)
-            _record(y, stream)
+            y = _empty((N, self.out_features), self._own[0] if residual is None else residual.dtype, x.device, stream)
         ldy = _rows(y, N, self.out_features, self._either, "y")
         y_dtype = self.dtype if y.dtype is own[0] else HASHGRID_F32
         ldr = 0 if residual is None else _rows(residual, N, self.out_features, (y.dtype,), "residual")
@@ -469,16 +466,13 @@ class Linear:
 
     def _scratch(self, size: int, device, stream):
         import torch
-        t = torch.empty(max(16, size), dtype=torch.uint8, device=device)
-        _record(t, stream)
-        return t
+        return _empty((max(16, size),), torch.uint8, device, stream)
 
     def backward(self, dL_dy, x, w, z=None, dL_dx=True, dL_dw=True, dL_db=True, workspace=None, device_status=None,
                  stream=None):
         """Returns (dL_dx, dL_dw, dL_db). Each is a tensor to write (dL_dx and dL_dw of the layer's type or fp32, dL_db
         fp32), True to allocate it (the layer's type, fp32, fp32), or None to leave it out. ``z``: what ``forward``
         wrote (not needed without an activation)."""
-        import torch
         N, own, either = dL_dy.shape[0], self._own, self._either
         lddy = _rows(dL_dy, None, self.out_features, own, "dL_dy")
         ldx = _rows(x, N, self.in_features, own, "x")
@@ -486,14 +480,11 @@ class Linear:
         if z is not None:
             _flat(z, (N, self.out_features), own, "z")
         if dL_dx is True:
-            dL_dx = torch.empty((N, self.in_features), device=x.device, dtype=self._own[0])
-            _record(dL_dx, stream)
+            dL_dx = _empty((N, self.in_features), own[0], x.device, stream)
         if dL_dw is True:
-            dL_dw = torch.empty((self.out_features, self.in_features), device=x.device, dtype=torch.float32)
-            _record(dL_dw, stream)
+            dL_dw = _empty(self._shape, self._f32[0], x.device, stream)
         if dL_db is True:
-            dL_db = torch.empty(self.out_features, device=x.device, dtype=torch.float32)
-            _record(dL_db, stream)
+            dL_db = _empty(self._bias_shape, self._f32[0], x.device, stream)
         lddx = 0 if dL_dx is None else _rows(dL_dx, N, self.in_features, either, "dL_dx")
         if dL_dw is not None:
             _flat(dL_dw, self._shape, either, "dL_dw")
@@ -501,19 +492,25 @@ class Linear:
             _flat(dL_db, self._bias_shape, self._f32, "dL_db")
         if workspace is None:
             workspace = self._scratch(lib.hashgrid_linear_backward_workspace(self.handle, N, lddy, ldx), x.device, stream)
-        hashgrid_linear_backward(self.handle, dL_dy, lddy, x, ldx, N, w, z, dL_dx, lddx,
-                                 HASHGRID_F32 if dL_dx is None else _dtype_code(dL_dx, "dL_dx"), dL_dw,
-                                 HASHGRID_F32 if dL_dw is None else _dtype_code(dL_dw, "dL_dw"), dL_db, workspace,
-                                 workspace.numel() * workspace.element_size(), device_status, stream)
+        _check(lib.hashgrid_linear_backward(
+            self.handle, dL_dy.data_ptr(), lddy, x.data_ptr(), ldx, N, w.data_ptr(), _ptr(z), _ptr(dL_dx), lddx,
+            self.dtype if dL_dx is not None and dL_dx.dtype is own[0] else HASHGRID_F32, _ptr(dL_dw),
+            self.dtype if dL_dw is not None and dL_dw.dtype is own[0] else HASHGRID_F32, _ptr(dL_db), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _ptr(device_status), _stream(stream)))
         return dL_dx, dL_dw, dL_db
 
 
-def _record(t, stream) -> None:
-    """A tensor that was allocated here is used on ``stream``: torch must not hand it out again before."""
-    if stream is None or not t.is_cuda:
-        return
+def _empty(shape, dtype, device, stream):
+    """A tensor that is used on ``stream`` (None: the current one) first: its memory comes from that stream's pool, since
+    what the current stream's pool hands out may still be in use there by what had it before."""
     import torch
-    t.record_stream(torch.cuda.ExternalStream(stream, device=t.device) if isinstance(stream, int) else stream)
+    if stream is None or torch.device(device).type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)  # the caller goes on with it there
+    return t
 
 
 class AdamW:
