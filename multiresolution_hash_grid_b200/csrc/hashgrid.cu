@@ -779,7 +779,7 @@ int set_map(CUtensorMap& map, const Array& a, int box_rows, const char* what) {
 int set_store_map(CUtensorMap& map, void* p, int64_t rows, int64_t cols, int64_t ld, int parts, bool f32, const char* what) {
     const cuuint64_t elem = f32 ? 4 : 2;
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
-    if (rows <= 1) ld = (cols + 7) / 8 * 8;  // no row follows
+    if (rows <= 1 && parts <= 1) ld = (cols + 7) / 8 * 8;  // no row follows
     const cuuint64_t strides[2] = {(cuuint64_t)ld * elem, (cuuint64_t)(parts > 1 ? rows * ld : ld) * elem};
     const cuuint32_t box[3] = {32, 32, 1}, ones[3] = {1, 1, 1};
     PFN_tensorMapEncodeTiled encode = tensor_map_fn();

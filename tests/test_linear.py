@@ -207,6 +207,14 @@ def test_wide_products(N, K, M):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N,K,M", [(2865, 12, 1), (3000, 588, 1), (3000, 20, 1), (1, 12, 1), (2900, 588, 2)])
+def test_one_output_over_many_rows(N, K, M):
+    """A weight gradient of one row, summed in parts that follow one another without a gap."""
+    check_backward(N, K, M, hg.HASHGRID_F16, hg.HASHGRID_ACT_RELU)
+    check_backward(N, K, M, hg.HASHGRID_BF16, hg.HASHGRID_ACT_NONE, dw32=False, want=(False, True, False))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("N,K,M", [(4096, 4096, 2048), (300, 8200, 264), (64, 30000, 72), (40, 5000, 37)])
 def test_long_sums_in_fp32(N, K, M):
     """fp32 results of sums over thousands of terms: the tensor cores' truncating additions alone would be off by 1e-9 a
