@@ -839,7 +839,8 @@ int set_product(Product& p, bool half, const Array& A, const Array& B, int64_t M
     const int64_t tiles = (int64_t)g.mt * g.nt;
     if (tiles > (1 << 30)) return fail(HASHGRID_ERR_ARG, "%s: too many tiles", what);
     // B stays in shared memory where one column tile covers it, it is small and its block has several tiles to compute.
-    g.resident = splits == 1 && group == 1 && g.nt == 1 && g.kblocks * g.b.bytes <= 32 * 1024 && g.mt > 2 * sms;
+    const bool two = e.out_f32 && e.z != nullptr;  // staging areas
+    g.resident = splits == 1 && group == 1 && g.nt == 1 && g.kblocks * g.b.bytes <= (two ? 8 : 32) * 1024 && g.mt > 2 * sms;
     const int kept = g.resident ? g.kblocks * g.b.bytes : 0;
     g.stage_bytes = g.a.bytes + (g.resident ? 0 : g.b.bytes);
     g.cluster = plan.cluster;
@@ -848,10 +849,10 @@ int set_product(Product& p, bool half, const Array& A, const Array& B, int64_t M
     p.gather = e.out_f32 && g.kblocks_per_split > hl::kSegment;
     const int per_sm = group == 1 && g.tmem_columns <= 256 && !p.gather ? 2 : 1;
     const int budget = (per_sm == 2 ? 113 : 227) * 1024 - 1024;  // less what the kernel has of its own
-    const bool two = e.out_f32 && e.z != nullptr;
     g.stages = std::min(hl::kMaxStages, (budget - kept - (int)hl::gemm_smem(0, two)) / g.stage_bytes);
     if (g.cluster > 1)  // a split product's shares lie in the stages
         while (g.stages * g.stage_bytes < 4 * ceil_div(bn, 32) * 4096) ++g.stages;
+    if (g.stages < 1) return fail(HASHGRID_ERR_ARG, "%s: no stage fits", what);  // does not happen: a stage has 48 KB at most
     const uint32_t type = half ? 0u : 1u;
     g.idesc = (1u << 4) | (type << 7) | (type << 10) | ((A.mn ? 1u : 0u) << 15) | ((B.mn ? 1u : 0u) << 16) |
               ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(hl::kBm * group >> 4) << 24);

@@ -215,6 +215,14 @@ def test_one_output_over_many_rows(N, K, M):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N,K,M", [(40000, 128, 128), (40000, 64, 64), (40000, 200, 40)])
+def test_many_rows_with_fp32_results_and_kept_z(N, K, M):
+    """The second staging area leaves less shared memory to weights that stay there."""
+    check_forward(N, K, M, hg.HASHGRID_BF16, hg.HASHGRID_ACT_SILU, y32=True)
+    check_forward(N, K, M, hg.HASHGRID_F16, hg.HASHGRID_ACT_RELU, y32=True, residual=False)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("N,K,M", [(4096, 4096, 2048), (300, 8200, 264), (64, 30000, 72), (40, 5000, 37)])
 def test_long_sums_in_fp32(N, K, M):
     """fp32 results of sums over thousands of terms: the tensor cores' truncating additions alone would be off by 1e-9 a
