@@ -623,6 +623,7 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
         for (Tiles t(g, first, step); t.more() && ok; t.next()) {
             const int m0 = (kPair ? 2 * t.m + (int)rank : t.m) * kBm, n0 = t.n * g.bn + (kPair ? (int)rank * (g.bn / 2) : 0);
             for (int kb = 0; kb < kbs; ++kb) {
+                __syncwarp();  // a lane that fell behind by two phases would wait for good
                 if (!(ok = wait_bounded(empty + 8 * r.stage, r.phase ^ 1u, &abort_flag))) break;
                 const uint32_t bar = full0 + 8 * r.stage, sa = sm0 + r.stage * g.stage_bytes, sb = sa + g.a.bytes;
                 const int k0 = (kb0 + kb) * kBk;
@@ -681,6 +682,7 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
                         if (!(ok = wait_bounded(room + 8 * (i & 1u), ((i >> 1) & 1u) ^ 1u, &abort_flag))) break;
                         mlp::fence_after();
                     }
+                    __syncwarp();
                     if (!(ok = wait_bounded(full + 8 * r.stage, r.phase, &abort_flag))) break;
                     mlp::fence_after();
                     const uint64_t da = a0 + (uint32_t)r.stage * stage, db = b0 + (g.resident ? (uint32_t)kb * next_b : (uint32_t)r.stage * stage);
