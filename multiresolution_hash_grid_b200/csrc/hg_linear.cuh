@@ -643,6 +643,12 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
                 issued = min(issued + 1, (uint32_t)g.stages);
             }
         }
+        // the block (and with it its barriers) stays until the MMAs' last reports of free stages have arrived
+        Ring last = r;
+        for (int s = 0; s < g.stages && ok; ++s, last.next(g.stages)) {
+            __syncwarp();
+            ok = wait_bounded(empty + 8 * last.stage, last.phase ^ 1u, &abort_flag);
+        }
         // given up: the copies in flight still write to this block's shared memory
         if (!ok && g.resident && kbs > 0) mlp::wait_parity(bfull, 0);
         for (; !ok && issued > 0; --issued) {
@@ -927,6 +933,7 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
     if (kPair) cluster_sync();  // nor while the pair's MMAs read its memory
     mlp::fence_after();
     if (threadIdx.x == 0 && abort_flag != 0 && g.status != nullptr) atomicExch(g.status, 1);
+    __syncwarp();
     if (warp == 0) {
         if (kPair) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(g.tmem_columns) : "memory");
         else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(g.tmem_columns) : "memory");
