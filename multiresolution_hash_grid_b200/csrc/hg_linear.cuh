@@ -463,21 +463,23 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// A bounded wait that also ends, with false, once another role of the block has given up.
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+// A bounded wait of a whole warp, which also ends once another role of the block has given up. All lanes get the
+// same answer, false if any of them gave up, and none goes on before the others: a lane that fell behind by two
+// phases of a barrier would wait for a parity that had passed, and lanes that disagreed would part for good.
+__device__ __forceinline__ bool warp_waits(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    uint32_t done = 0;
     for (uint32_t it = 0; it < mlp::kWaitLimit; ++it) {
-        uint32_t done;
         asm volatile(
             "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}\n"
             : "=r"(done)
             : "r"(bar), "r"(parity)
             : "memory");
-        if (done) return true;
-        if ((it & 255u) == 255u && *abort_flag != 0) return false;
+        if (done || ((it & 255u) == 255u && *abort_flag != 0)) break;
     }
-    *abort_flag = 1;
-    return false;
+    const bool all = __all_sync(0xffffffffu, done);
+    if (!all) *abort_flag = 1;
+    return all;
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -623,8 +625,7 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
         for (Tiles t(g, first, step); t.more() && ok; t.next()) {
             const int m0 = (kPair ? 2 * t.m + (int)rank : t.m) * kBm, n0 = t.n * g.bn + (kPair ? (int)rank * (g.bn / 2) : 0);
             for (int kb = 0; kb < kbs; ++kb) {
-                __syncwarp();  // a lane that fell behind by two phases would wait for good
-                if (!(ok = wait_bounded(empty + 8 * r.stage, r.phase ^ 1u, &abort_flag))) break;
+                if (!(ok = warp_waits(empty + 8 * r.stage, r.phase ^ 1u, &abort_flag))) break;
                 const uint32_t bar = full0 + 8 * r.stage, sa = sm0 + r.stage * g.stage_bytes, sb = sa + g.a.bytes;
                 const int k0 = (kb0 + kb) * kBk;
                 if (!kPair && issues) arrive_expect(bar, bytes);
@@ -645,10 +646,7 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
         }
         // the block (and with it its barriers) stays until the MMAs' last reports of free stages have arrived
         Ring last = r;
-        for (int s = 0; s < g.stages && ok; ++s, last.next(g.stages)) {
-            __syncwarp();
-            ok = wait_bounded(empty + 8 * last.stage, last.phase ^ 1u, &abort_flag);
-        }
+        for (int s = 0; s < g.stages && ok; ++s, last.next(g.stages)) ok = warp_waits(empty + 8 * last.stage, last.phase ^ 1u, &abort_flag);
         // given up: the copies in flight still write to this block's shared memory
         if (!ok && g.resident && kbs > 0) mlp::wait_parity(bfull, 0);
         for (; !ok && issued > 0; --issued) {
@@ -668,14 +666,14 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
             const bool issues = elect_one();
             Ring r;
             uint32_t i = 0;
-            bool ok = kbs == 0 || !g.resident || wait_bounded(bfull, 0, &abort_flag);
+            bool ok = kbs == 0 || !g.resident || warp_waits(bfull, 0, &abort_flag);
             // Descriptors count addresses in units of 16 bytes: a stage and a step of 16 k are additions to them.
             const uint32_t step_a = g.a.mn ? 128 : 2, step_b = g.b.mn ? 128 : 2, stage = g.stage_bytes >> 4;
             const uint32_t next_b = g.resident ? g.b.bytes >> 4 : 0;
             const uint64_t a0 = swizzled_desc(sm0, 64 * 128), b0 = swizzled_desc(g.resident ? sb0 : sm0 + g.a.bytes, 64 * 128);
             for (Tiles t(g, first, step); t.more() && ok && kbs > 0; t.next(), ++i) {
                 uint32_t acc = tmem + (i & 1u) * g.columns;
-                if (!(ok = wait_bounded(room + 8 * (i & 1u), ((i >> 1) & 1u) ^ 1u, &abort_flag))) break;
+                if (!(ok = warp_waits(room + 8 * (i & 1u), ((i >> 1) & 1u) ^ 1u, &abort_flag))) break;
                 mlp::fence_after();
                 int kseg = 0;
                 for (int kb = 0; kb < kbs; ++kb, ++kseg) {
@@ -685,11 +683,10 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
                         ++i;
                         kseg = 0;
                         acc = tmem + (i & 1u) * g.columns;
-                        if (!(ok = wait_bounded(room + 8 * (i & 1u), ((i >> 1) & 1u) ^ 1u, &abort_flag))) break;
+                        if (!(ok = warp_waits(room + 8 * (i & 1u), ((i >> 1) & 1u) ^ 1u, &abort_flag))) break;
                         mlp::fence_after();
                     }
-                    __syncwarp();
-                    if (!(ok = wait_bounded(full + 8 * r.stage, r.phase, &abort_flag))) break;
+                    if (!(ok = warp_waits(full + 8 * r.stage, r.phase, &abort_flag))) break;
                     mlp::fence_after();
                     const uint64_t da = a0 + (uint32_t)r.stage * stage, db = b0 + (g.resident ? (uint32_t)kb * next_b : (uint32_t)r.stage * stage);
 #pragma unroll
@@ -807,10 +804,9 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
                 }
             };
             auto wait_accumulator = [&]() {
-                const bool ok = wait_bounded(done + 8 * (i & 1u), (i >> 1) & 1u, &abort_flag);
-                if (__any_sync(0xffffffffu, !ok)) return false;
+                const bool ok = warp_waits(done + 8 * (i & 1u), (i >> 1) & 1u, &abort_flag);
                 mlp::fence_after();
-                return true;
+                return ok;
             };
             auto free_accumulator = [&]() {
                 mlp::fence_before();
@@ -1154,7 +1150,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
         Ring r;
         int issued = 0;
         for (int i = 0; i < mine; ++i) {
-            if (!(ok = wait_bounded(empty + 8 * r.stage, r.phase ^ 1u, &abort_flag))) break;
+            if (!(ok = warp_waits(empty + 8 * r.stage, r.phase ^ 1u, &abort_flag))) break;
             const uint32_t bar = full + 8 * r.stage, s = sm0 + r.stage * g.stage_bytes;
             const int m0 = (int)(blockIdx.x + i * gridDim.x) * kBm;
             if (issues) {
@@ -1180,16 +1176,16 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
         // ---------------------------------- MMAs ----------------------------------
         const bool issues = elect_one();
         Ring r;
-        bool ok = !dx || wait_bounded(wfull, 0, &abort_flag);
+        bool ok = !dx || warp_waits(wfull, 0, &abort_flag);
         const uint32_t dw0 = tmem + 2 * g.columns, stage = g.stage_bytes >> 4;
         const uint64_t dz_k = swizzled_desc(sm0, 0), dz_mn = swizzled_desc(sm0, kBox), x_mn = swizzled_desc(sm0 + x_at, kBox),
                        w_mn = swizzled_desc(w0, g.k_out * 128);
         for (int i = 0; i < mine && ok; ++i) {
             const int b = i & 1, group = i / kFlush, f = group & 1;
-            if (!(ok = wait_bounded(full + 8 * r.stage, r.phase, &abort_flag))) break;
-            if (!(ok = wait_bounded(ready + 8 * r.stage, r.phase, &abort_flag))) break;
-            if (dx && !(ok = wait_bounded(room + 8 * b, ((i >> 1) & 1u) ^ 1u, &abort_flag))) break;
-            if (i % kFlush == 0 && !(ok = wait_bounded(wroom + 8 * f, ((group >> 1) & 1u) ^ 1u, &abort_flag))) break;
+            if (!(ok = warp_waits(full + 8 * r.stage, r.phase, &abort_flag))) break;
+            if (!(ok = warp_waits(ready + 8 * r.stage, r.phase, &abort_flag))) break;
+            if (dx && !(ok = warp_waits(room + 8 * b, ((i >> 1) & 1u) ^ 1u, &abort_flag))) break;
+            if (i % kFlush == 0 && !(ok = warp_waits(wroom + 8 * f, ((group >> 1) & 1u) ^ 1u, &abort_flag))) break;
             mlp::fence_after();
             const uint32_t off = (uint32_t)r.stage * stage;
             if (dx) {
@@ -1217,8 +1213,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
         for (int i = 0; i < mine && dx; ++i) {
             const int b = i & 1;
             const int m0 = (int)(blockIdx.x + i * gridDim.x) * kBm + 32 * quarter;
-            const bool ok = wait_bounded(done + 8 * b, (i >> 1) & 1u, &abort_flag);
-            if (__any_sync(0xffffffffu, !ok)) break;
+            if (!warp_waits(done + 8 * b, (i >> 1) & 1u, &abort_flag)) break;
             mlp::fence_after();
             for (int c = warp >> 2; c < chunks; c += 2) {
                 uint32_t v[32];
@@ -1275,8 +1270,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
         bool ok = true;
         auto flush = [&](int group) {  // adds what a group of tiles gathered in tensor memory
             const int f = group & 1;
-            const bool fine = wait_bounded(wdone + 8 * f, (group >> 1) & 1u, &abort_flag);
-            if (__any_sync(0xffffffffu, !fine)) return false;
+            if (!warp_waits(wdone + 8 * f, (group >> 1) & 1u, &abort_flag)) return false;
             mlp::fence_after();
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
@@ -1294,11 +1288,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
         };
         Ring r;
         for (int i = 0; i < mine && ok; ++i) {
-            ok = wait_bounded(full + 8 * r.stage, r.phase, &abort_flag);
-            if (__any_sync(0xffffffffu, !ok)) {
-                ok = false;
-                break;
-            }
+            if (!(ok = warp_waits(full + 8 * r.stage, r.phase, &abort_flag))) break;
             uint8_t* s = sm + r.stage * g.stage_bytes + box_at;
             if (g.act != kNoAct || g.want_db) {
 #pragma unroll 2

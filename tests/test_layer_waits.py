@@ -1,0 +1,31 @@
+"""The waits of the layers' kernels: none is unbounded, and a block that gives one up ends in order."""
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "multiresolution_hash_grid_b200", "csrc")
+
+
+def source():
+    """hg_linear.cuh without its comments."""
+    with open(os.path.join(CSRC, "hg_linear.cuh")) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def function(text, head):
+    """The body of the function whose signature `head` matches."""
+    at = text.index("{", re.search(head, text).end())
+    depth, end = 0, at
+    while True:
+        depth += (text[end] == "{") - (text[end] == "}")
+        end += 1
+        if depth == 0:
+            return text[at:end]
+
+
+def test_waits_are_votes_of_whole_warps():
+    """A warp goes on, or gives up, as a whole: lanes that polled a barrier for themselves could part (one gives up
+    where another sees the phase flip) and then stop at different meetings for good."""
+    text = source()
+    assert text.count("mbarrier.try_wait") == 1 and "test_wait" not in text
+    wait = function(text, r"bool warp_waits\(")
+    assert "mbarrier.try_wait" in wait and re.search(r"__all_sync\(0xffffffffu, \w+\);\s*if \(!\w+\) \*abort_flag = 1;\s*return \w+;\s*\}$", wait)
