@@ -1163,6 +1163,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
             r.next(g.stages);
             issued = min(issued + 1, g.stages);
         }
+        // the block (and with it its barriers) stays until the MMAs' last reports of free stages have arrived
+        Ring last = r;
+        for (int i = 0; i < g.stages && ok; ++i, last.next(g.stages)) ok = warp_waits(empty + 8 * last.stage, last.phase ^ 1u, &abort_flag);
         if (!ok && dx) mlp::wait_parity(wfull, 0);
         for (; !ok && issued > 0; --issued) {  // copies in flight still write to this block's memory
             if (r.stage == 0) {

@@ -29,3 +29,16 @@ def test_waits_are_votes_of_whole_warps():
     assert text.count("mbarrier.try_wait") == 1 and "test_wait" not in text
     wait = function(text, r"bool warp_waits\(")
     assert "mbarrier.try_wait" in wait and re.search(r"__all_sync\(0xffffffffu, \w+\);\s*if \(!\w+\) \*abort_flag = 1;\s*return \w+;\s*\}$", wait)
+
+
+def kernels():
+    text = source()
+    return [function(text, r"\bgemm_kernel\("), function(text, r"\bnarrow_backward_kernel\(")]
+
+
+def test_blocks_stay_until_free_stages_are_reported():
+    """The multiplying warp's reports of free stages arrive at a barrier of the block after its last wait for it: the
+    copying warp of each kernel waits once more for every stage."""
+    for k in kernels():
+        assert re.search(r"Ring last = r;\s*for \(int (\w) = 0; \1 < g\.stages && ok; \+\+\1, last\.next\(g\.stages\)\) "
+                         r"ok = warp_waits\(empty \+ 8 \* last\.stage", k)
