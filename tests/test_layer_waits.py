@@ -42,3 +42,10 @@ def test_blocks_stay_until_free_stages_are_reported():
     for k in kernels():
         assert re.search(r"Ring last = r;\s*for \(int (\w) = 0; \1 < g\.stages && ok; \+\+\1, last\.next\(g\.stages\)\) "
                          r"ok = warp_waits\(empty \+ 8 \* last\.stage", k)
+
+
+def test_tensor_memory_is_freed_by_a_whole_warp():
+    """The warp that frees it meets after a branch that one lane takes alone."""
+    for k in kernels():
+        tail = k[:k.index("tcgen05.dealloc")]
+        assert re.search(r"__syncwarp\(\);\s*if \(warp == 0\)[^;]*$", tail)
