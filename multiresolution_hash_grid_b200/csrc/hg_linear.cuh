@@ -564,6 +564,7 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
     uint64_t* bars = reinterpret_cast<uint64_t*>(staging + (g.e.out_f32 && g.e.z != nullptr ? 2 : 1) * kStaging);  // fp32 y and z side by side
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 6);
     __shared__ volatile int abort_flag;
+    __shared__ uint64_t copies_issued;  // stages that the copying warp filled
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // the shuffle tells the compiler that it is uniform
     const uint32_t sm0 = (uint32_t)__cvta_generic_to_shared(sm), bar0 = (uint32_t)__cvta_generic_to_shared(bars);
     const uint32_t sb0 = sm0 + g.stages * g.stage_bytes;  // B, where it stays
@@ -617,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
                     tma_load(sb0 + kb * g.b.bytes + j * g.b.box_rows * 128, &g.tb, g.b.mn ? 64 * j : kb * kBk, g.b.mn ? kb * kBk : 0, bfull);
         }
         Ring r;
-        uint32_t issued = 0;  // copies so far, at most counted to the number of stages
+        uint64_t issued = 0;
         bool ok = true;
         const int a_boxes = g.a.boxes, b_boxes = g.resident ? 0 : g.b.boxes, a_step = g.a.box_rows * 128, b_step = g.b.box_rows * 128;
         const bool a_mn = g.a.mn != 0, b_mn = g.b.mn != 0;
@@ -641,22 +642,13 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
                     if (!kPair && issues) tma_load(sb + j * b_step, &g.tb, x, y, bar);
                 }
                 r.next(g.stages);
-                issued = min(issued + 1, (uint32_t)g.stages);
+                ++issued;
             }
         }
+        if (lane == 0) copies_issued = issued;
         // the block (and with it its barriers) stays until the MMAs' last reports of free stages have arrived
         Ring last = r;
         for (int s = 0; s < g.stages && ok; ++s, last.next(g.stages)) ok = warp_waits(empty + 8 * last.stage, last.phase ^ 1u, &abort_flag);
-        // given up: the copies in flight still write to this block's shared memory
-        if (!ok && g.resident && kbs > 0) mlp::wait_parity(bfull, 0);
-        for (; !ok && issued > 0; --issued) {
-            if (r.stage == 0) {
-                r.stage = g.stages;
-                r.phase ^= 1u;
-            }
-            --r.stage;
-            mlp::wait_parity(full + 8 * r.stage, r.phase);
-        }
     } else if (warp == kOutWarps) {
         // ---------------------------------- MMAs ----------------------------------
         // The whole warp walks through the loop and one lane issues: with everything uniform the descriptors stay
@@ -700,11 +692,6 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
                 }
                 if (kPair && ok && issues) commit_pair(done + 8 * (i & 1u));
                 if (!kPair && ok && issues) mlp::commit(done + 8 * (i & 1u));
-            }
-            if (!ok && issues) {
-                if (kPair) commit_pair(drain);
-                else mlp::commit(drain);
-                mlp::wait_parity(drain, 0);
             }
         }
     } else {
@@ -926,6 +913,18 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
     }
     mlp::fence_before();
     __syncthreads();
+    if (abort_flag != 0) {  // some role gave up: copies and MMAs that the others did not wait for may still be under way
+        if (warp == kOutWarps + 1) {
+            if (g.resident && kbs > 0) mlp::wait_parity(bfull, 0);
+            for (uint64_t c = copies_issued - min(copies_issued, (uint64_t)g.stages); c < copies_issued; ++c)
+                mlp::wait_parity(full + 8 * (uint32_t)(c % g.stages), (uint32_t)(c / g.stages) & 1u);
+        } else if (warp == kOutWarps && rank == 0 && elect_one()) {
+            if (kPair) commit_pair(drain);
+            else mlp::commit(drain);
+            mlp::wait_parity(drain, 0);
+        }
+        __syncthreads();
+    }
     if (kPair) cluster_sync();  // nor while the pair's MMAs read its memory
     mlp::fence_after();
     if (threadIdx.x == 0 && abort_flag != 0 && g.status != nullptr) atomicExch(g.status, 1);
@@ -1100,6 +1099,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
     uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kStaging);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 32);
     __shared__ volatile int abort_flag;
+    __shared__ int copies_issued;  // stages that the copying warp filled
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t sm0 = (uint32_t)__cvta_generic_to_shared(sm), w0 = (uint32_t)__cvta_generic_to_shared(ws);
     const uint32_t bar0 = (uint32_t)__cvta_generic_to_shared(bars);
@@ -1161,20 +1161,12 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
                 for (int j = 0; j < g.boxes_in; ++j) tma_load(s + x_at + j * kBox, &g.tx, 64 * j, m0, bar);
             }
             r.next(g.stages);
-            issued = min(issued + 1, g.stages);
+            ++issued;
         }
+        if (lane == 0) copies_issued = issued;
         // the block (and with it its barriers) stays until the MMAs' last reports of free stages have arrived
         Ring last = r;
         for (int i = 0; i < g.stages && ok; ++i, last.next(g.stages)) ok = warp_waits(empty + 8 * last.stage, last.phase ^ 1u, &abort_flag);
-        if (!ok && dx) mlp::wait_parity(wfull, 0);
-        for (; !ok && issued > 0; --issued) {  // copies in flight still write to this block's memory
-            if (r.stage == 0) {
-                r.stage = g.stages;
-                r.phase ^= 1u;
-            }
-            --r.stage;
-            mlp::wait_parity(full + 8 * r.stage, r.phase);
-        }
     } else if (warp == 8) {
         // ---------------------------------- MMAs ----------------------------------
         const bool issues = elect_one();
@@ -1204,10 +1196,6 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
             if (issues) mlp::commit(empty + 8 * r.stage);
             if (issues && (i % kFlush == kFlush - 1 || i == mine - 1)) mlp::commit(wdone + 8 * f);
             r.next(g.stages);
-        }
-        if (!ok && issues) {
-            mlp::commit(drain);
-            mlp::wait_parity(drain, 0);
         }
     } else if (warp < 8) {
         // ---------------------------------- dx -----------------------------------
@@ -1355,6 +1343,17 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
     __syncwarp();
     mlp::fence_before();
     __syncthreads();
+    if (abort_flag != 0) {  // some role gave up: copies and MMAs that the others did not wait for may still be under way
+        if (warp == 9) {
+            if (dx) mlp::wait_parity(wfull, 0);
+            for (int c = max(0, copies_issued - g.stages); c < copies_issued; ++c)
+                mlp::wait_parity(full + 8 * (c % g.stages), (uint32_t)(c / g.stages) & 1u);
+        } else if (warp == 8 && elect_one()) {
+            mlp::commit(drain);
+            mlp::wait_parity(drain, 0);
+        }
+        __syncthreads();
+    }
     mlp::fence_after();
     if (threadIdx.x == 0 && abort_flag != 0 && g.status != nullptr) atomicExch(g.status, 1);
     __syncwarp();

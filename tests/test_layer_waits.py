@@ -49,3 +49,13 @@ def test_tensor_memory_is_freed_by_a_whole_warp():
     for k in kernels():
         tail = k[:k.index("tcgen05.dealloc")]
         assert re.search(r"__syncwarp\(\);\s*if \(warp == 0\)[^;]*$", tail)
+
+
+def test_a_block_that_gave_up_ends_after_its_copies_and_products():
+    """Whichever role gave up, the copying and the multiplying warp wait for what they issued, after all roles have
+    ended and before tensor memory is freed."""
+    for k in kernels():
+        tail = k[:k.index("tcgen05.dealloc")]
+        tail = tail[tail.rindex("if (abort_flag != 0) {"):]
+        assert "copies_issued" in tail and "commit(drain)" in tail and "wait_parity(drain, 0)" in tail and "__syncthreads();" in tail
+        assert k.count("wait_parity(drain, 0)") == 1 and "__syncthreads();" in k[:k.rindex("if (abort_flag != 0) {")][-60:]
