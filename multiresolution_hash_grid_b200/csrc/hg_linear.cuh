@@ -438,6 +438,15 @@ __device__ __forceinline__ void commit_pair(uint32_t mbar) {
 __device__ __forceinline__ void arrive_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}\n" ::"r"(bar), "r"(bytes) : "memory");
 }
+// Counts `bytes` as copied that nothing will copy any more.
+__device__ __forceinline__ void count_copied(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_address(uint32_t saddr, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+    return a;
+}
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -465,7 +474,9 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
 
 // A bounded wait of a whole warp, which also ends once another role of the block has given up. All lanes get the
 // same answer, false if any of them gave up, and none goes on before the others: a lane that fell behind by two
-// phases of a barrier would wait for a parity that had passed, and lanes that disagreed would part for good.
+// phases of a barrier would wait for a parity that had passed, and lanes that disagreed would part for good. A block
+// of a pair (kPair) tells the other one that it gave up.
+template <bool kPair>
 __device__ __forceinline__ bool warp_waits(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
     uint32_t done = 0;
     for (uint32_t it = 0; it < mlp::kWaitLimit; ++it) {
@@ -478,7 +489,17 @@ __device__ __forceinline__ bool warp_waits(uint32_t bar, uint32_t parity, volati
         if (done || ((it & 255u) == 255u && *abort_flag != 0)) break;
     }
     const bool all = __all_sync(0xffffffffu, done);
-    if (!all) *abort_flag = 1;
+    if (!all) {
+        *abort_flag = 1;
+        if (kPair) {
+            uint32_t rank;
+            asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+            asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(
+                             cluster_address((uint32_t)__cvta_generic_to_shared(const_cast<int*>(abort_flag)), rank ^ 1u)),
+                         "r"(1)
+                         : "memory");
+        }
+    }
     return all;
 }
 
@@ -538,14 +559,14 @@ struct Tiles {
     }
 };
 
-__device__ __forceinline__ uint32_t cluster_address(uint32_t saddr, uint32_t rank) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
-    return a;
-}
 __device__ __forceinline__ float4 cluster_load(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint64_t cluster_load64(uint32_t addr) {
+    uint64_t v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
     return v;
 }
 __device__ __forceinline__ void cluster_sync() {
@@ -626,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
         for (Tiles t(g, first, step); t.more() && ok; t.next()) {
             const int m0 = (kPair ? 2 * t.m + (int)rank : t.m) * kBm, n0 = t.n * g.bn + (kPair ? (int)rank * (g.bn / 2) : 0);
             for (int kb = 0; kb < kbs; ++kb) {
-                if (!(ok = warp_waits(empty + 8 * r.stage, r.phase ^ 1u, &abort_flag))) break;
+                if (!(ok = warp_waits<kPair>(empty + 8 * r.stage, r.phase ^ 1u, &abort_flag))) break;
                 const uint32_t bar = full0 + 8 * r.stage, sa = sm0 + r.stage * g.stage_bytes, sb = sa + g.a.bytes;
                 const int k0 = (kb0 + kb) * kBk;
                 if (!kPair && issues) arrive_expect(bar, bytes);
@@ -648,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
         if (lane == 0) copies_issued = issued;
         // the block (and with it its barriers) stays until the MMAs' last reports of free stages have arrived
         Ring last = r;
-        for (int s = 0; s < g.stages && ok; ++s, last.next(g.stages)) ok = warp_waits(empty + 8 * last.stage, last.phase ^ 1u, &abort_flag);
+        for (int s = 0; s < g.stages && ok; ++s, last.next(g.stages)) ok = warp_waits<kPair>(empty + 8 * last.stage, last.phase ^ 1u, &abort_flag);
     } else if (warp == kOutWarps) {
         // ---------------------------------- MMAs ----------------------------------
         // The whole warp walks through the loop and one lane issues: with everything uniform the descriptors stay
@@ -658,14 +679,14 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
             const bool issues = elect_one();
             Ring r;
             uint32_t i = 0;
-            bool ok = kbs == 0 || !g.resident || warp_waits(bfull, 0, &abort_flag);
+            bool ok = kbs == 0 || !g.resident || warp_waits<kPair>(bfull, 0, &abort_flag);
             // Descriptors count addresses in units of 16 bytes: a stage and a step of 16 k are additions to them.
             const uint32_t step_a = g.a.mn ? 128 : 2, step_b = g.b.mn ? 128 : 2, stage = g.stage_bytes >> 4;
             const uint32_t next_b = g.resident ? g.b.bytes >> 4 : 0;
             const uint64_t a0 = swizzled_desc(sm0, 64 * 128), b0 = swizzled_desc(g.resident ? sb0 : sm0 + g.a.bytes, 64 * 128);
             for (Tiles t(g, first, step); t.more() && ok && kbs > 0; t.next(), ++i) {
                 uint32_t acc = tmem + (i & 1u) * g.columns;
-                if (!(ok = warp_waits(room + 8 * (i & 1u), ((i >> 1) & 1u) ^ 1u, &abort_flag))) break;
+                if (!(ok = warp_waits<kPair>(room + 8 * (i & 1u), ((i >> 1) & 1u) ^ 1u, &abort_flag))) break;
                 mlp::fence_after();
                 int kseg = 0;
                 for (int kb = 0; kb < kbs; ++kb, ++kseg) {
@@ -675,10 +696,10 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
                         ++i;
                         kseg = 0;
                         acc = tmem + (i & 1u) * g.columns;
-                        if (!(ok = warp_waits(room + 8 * (i & 1u), ((i >> 1) & 1u) ^ 1u, &abort_flag))) break;
+                        if (!(ok = warp_waits<kPair>(room + 8 * (i & 1u), ((i >> 1) & 1u) ^ 1u, &abort_flag))) break;
                         mlp::fence_after();
                     }
-                    if (!(ok = warp_waits(full + 8 * r.stage, r.phase, &abort_flag))) break;
+                    if (!(ok = warp_waits<kPair>(full + 8 * r.stage, r.phase, &abort_flag))) break;
                     mlp::fence_after();
                     const uint64_t da = a0 + (uint32_t)r.stage * stage, db = b0 + (g.resident ? (uint32_t)kb * next_b : (uint32_t)r.stage * stage);
 #pragma unroll
@@ -791,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
                 }
             };
             auto wait_accumulator = [&]() {
-                const bool ok = warp_waits(done + 8 * (i & 1u), (i >> 1) & 1u, &abort_flag);
+                const bool ok = warp_waits<kPair>(done + 8 * (i & 1u), (i >> 1) & 1u, &abort_flag);
                 mlp::fence_after();
                 return ok;
             };
@@ -913,19 +934,33 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
     }
     mlp::fence_before();
     __syncthreads();
-    if (abort_flag != 0) {  // some role gave up: copies and MMAs that the others did not wait for may still be under way
-        if (warp == kOutWarps + 1) {
+    if (kPair) cluster_sync();  // nor while the pair's MMAs read its memory
+    if (abort_flag != 0) {
+        // Some role gave up (in a pair: of either block): copies and MMAs that the others did not wait for may still be under way.
+        // A pair's copies are counted by the first block's barriers, in pairs. Where one block issued more of them, the other's
+        // share is made up for: it will not come any more, or was not yet expected.
+        if (warp == kOutWarps + 1 && rank == 0) {
             if (g.resident && kbs > 0) mlp::wait_parity(bfull, 0);
-            for (uint64_t c = copies_issued - min(copies_issued, (uint64_t)g.stages); c < copies_issued; ++c)
+            const uint64_t mine = copies_issued;
+            const uint64_t theirs = kPair ? cluster_load64(cluster_address((uint32_t)__cvta_generic_to_shared(&copies_issued), 1)) : mine;
+            const uint64_t most = max(mine, theirs);
+            if (kPair && lane == 0) {
+                for (uint64_t c = mine; c < most; ++c) arrive_expect(full + 8 * (uint32_t)(c % g.stages), g.a.bytes + g.b.bytes);
+                for (uint64_t c = theirs; c < most; ++c) count_copied(full + 8 * (uint32_t)(c % g.stages), g.a.bytes + g.b.bytes);
+            }
+            __syncwarp();
+            for (uint64_t c = most - min(most, (uint64_t)g.stages); c < most; ++c)
                 mlp::wait_parity(full + 8 * (uint32_t)(c % g.stages), (uint32_t)(c / g.stages) & 1u);
-        } else if (warp == kOutWarps && rank == 0 && elect_one()) {
-            if (kPair) commit_pair(drain);
-            else mlp::commit(drain);
+        } else if (warp == kOutWarps) {
+            if (rank == 0 && elect_one()) {
+                if (kPair) commit_pair(drain);  // both blocks' MMAs, reported to both
+                else mlp::commit(drain);
+            }
             mlp::wait_parity(drain, 0);
         }
         __syncthreads();
+        if (kPair) cluster_sync();
     }
-    if (kPair) cluster_sync();  // nor while the pair's MMAs read its memory
     mlp::fence_after();
     if (threadIdx.x == 0 && abort_flag != 0 && g.status != nullptr) atomicExch(g.status, 1);
     __syncwarp();
@@ -1150,7 +1185,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
         Ring r;
         int issued = 0;
         for (int i = 0; i < mine; ++i) {
-            if (!(ok = warp_waits(empty + 8 * r.stage, r.phase ^ 1u, &abort_flag))) break;
+            if (!(ok = warp_waits<false>(empty + 8 * r.stage, r.phase ^ 1u, &abort_flag))) break;
             const uint32_t bar = full + 8 * r.stage, s = sm0 + r.stage * g.stage_bytes;
             const int m0 = (int)(blockIdx.x + i * gridDim.x) * kBm;
             if (issues) {
@@ -1166,21 +1201,21 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
         if (lane == 0) copies_issued = issued;
         // the block (and with it its barriers) stays until the MMAs' last reports of free stages have arrived
         Ring last = r;
-        for (int i = 0; i < g.stages && ok; ++i, last.next(g.stages)) ok = warp_waits(empty + 8 * last.stage, last.phase ^ 1u, &abort_flag);
+        for (int i = 0; i < g.stages && ok; ++i, last.next(g.stages)) ok = warp_waits<false>(empty + 8 * last.stage, last.phase ^ 1u, &abort_flag);
     } else if (warp == 8) {
         // ---------------------------------- MMAs ----------------------------------
         const bool issues = elect_one();
         Ring r;
-        bool ok = !dx || warp_waits(wfull, 0, &abort_flag);
+        bool ok = !dx || warp_waits<false>(wfull, 0, &abort_flag);
         const uint32_t dw0 = tmem + 2 * g.columns, stage = g.stage_bytes >> 4;
         const uint64_t dz_k = swizzled_desc(sm0, 0), dz_mn = swizzled_desc(sm0, kBox), x_mn = swizzled_desc(sm0 + x_at, kBox),
                        w_mn = swizzled_desc(w0, g.k_out * 128);
         for (int i = 0; i < mine && ok; ++i) {
             const int b = i & 1, group = i / kFlush, f = group & 1;
-            if (!(ok = warp_waits(full + 8 * r.stage, r.phase, &abort_flag))) break;
-            if (!(ok = warp_waits(ready + 8 * r.stage, r.phase, &abort_flag))) break;
-            if (dx && !(ok = warp_waits(room + 8 * b, ((i >> 1) & 1u) ^ 1u, &abort_flag))) break;
-            if (i % kFlush == 0 && !(ok = warp_waits(wroom + 8 * f, ((group >> 1) & 1u) ^ 1u, &abort_flag))) break;
+            if (!(ok = warp_waits<false>(full + 8 * r.stage, r.phase, &abort_flag))) break;
+            if (!(ok = warp_waits<false>(ready + 8 * r.stage, r.phase, &abort_flag))) break;
+            if (dx && !(ok = warp_waits<false>(room + 8 * b, ((i >> 1) & 1u) ^ 1u, &abort_flag))) break;
+            if (i % kFlush == 0 && !(ok = warp_waits<false>(wroom + 8 * f, ((group >> 1) & 1u) ^ 1u, &abort_flag))) break;
             mlp::fence_after();
             const uint32_t off = (uint32_t)r.stage * stage;
             if (dx) {
@@ -1204,7 +1239,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
         for (int i = 0; i < mine && dx; ++i) {
             const int b = i & 1;
             const int m0 = (int)(blockIdx.x + i * gridDim.x) * kBm + 32 * quarter;
-            if (!warp_waits(done + 8 * b, (i >> 1) & 1u, &abort_flag)) break;
+            if (!warp_waits<false>(done + 8 * b, (i >> 1) & 1u, &abort_flag)) break;
             mlp::fence_after();
             for (int c = warp >> 2; c < chunks; c += 2) {
                 uint32_t v[32];
@@ -1261,7 +1296,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
         bool ok = true;
         auto flush = [&](int group) {  // adds what a group of tiles gathered in tensor memory
             const int f = group & 1;
-            if (!warp_waits(wdone + 8 * f, (group >> 1) & 1u, &abort_flag)) return false;
+            if (!warp_waits<false>(wdone + 8 * f, (group >> 1) & 1u, &abort_flag)) return false;
             mlp::fence_after();
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
@@ -1279,7 +1314,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
         };
         Ring r;
         for (int i = 0; i < mine && ok; ++i) {
-            if (!(ok = warp_waits(full + 8 * r.stage, r.phase, &abort_flag))) break;
+            if (!(ok = warp_waits<false>(full + 8 * r.stage, r.phase, &abort_flag))) break;
             uint8_t* s = sm + r.stage * g.stage_bytes + box_at;
             if (g.act != kNoAct || g.want_db) {
 #pragma unroll 2
