@@ -456,6 +456,14 @@ int hashgrid_linear_backward(hashgrid_linear_t layer, const void *dL_dy, int64_t
                              void *dL_dw, int dw_dtype, float *dL_db, void *workspace, size_t workspace_bytes,
                              int *device_status, void *cuda_stream);
 
+/*
+ * hashgrid_debug_wait_limit -- how often a wait of the layer calls' kernels is polled before it is
+ * given up (for layer calls from now on, in all threads): 0 <= polls <= 2^22, the default, which a
+ * negative number restores. With 0 each call gives up, sets its device_status and leaves
+ * its outputs incomplete. For tests of what happens then.
+ */
+int hashgrid_debug_wait_limit(int64_t polls);
+
 typedef struct hashgrid_adamw_s *hashgrid_adamw_t; /* opaque, library-owned */
 
 #define HASHGRID_ADAMW_BLOCK 256 /* elements of an 8-bit state that share a scale */

@@ -113,6 +113,7 @@ def _load() -> ctypes.CDLL:
         "hashgrid_linear_forward_workspace": (sz, [vp, i64, i64]),
         "hashgrid_linear_backward_workspace": (sz, [vp, i64, i64, i64]),
         "hashgrid_linear_backward": (i32, [vp, vp, i64, vp, i64, i64, vp, vp, vp, i64, i32, vp, i32, vp, vp, sz, vp, vp]),
+        "hashgrid_debug_wait_limit": (i32, [i64]),
         "hashgrid_adamw_create": (i32, [ctypes.POINTER(AdamwTensor), i32, ctypes.POINTER(vp)]),
         "hashgrid_adamw_destroy": (i32, [vp]),
         "hashgrid_adamw_step": (i32, [vp, i64, vp, ctypes.c_float, ctypes.c_float, ctypes.c_float, ctypes.c_float,
@@ -289,6 +290,10 @@ def hashgrid_linear_backward(layer: int, dL_dy, lddy: int, x, ldx: int, N: int, 
     _check(lib.hashgrid_linear_backward(layer, _ptr(dL_dy), lddy, _ptr(x), ldx, N, _ptr(w), _ptr(z), _ptr(dL_dx), lddx,
                                         dx_dtype, _ptr(dL_dw), dw_dtype, _ptr(dL_db), _ptr(workspace), workspace_bytes,
                                         _ptr(device_status), _stream(stream)))
+
+
+def hashgrid_debug_wait_limit(polls: int = -1) -> None:
+    _check(lib.hashgrid_debug_wait_limit(polls))
 
 
 def hashgrid_adamw_create(tensors) -> int:

@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <cmath>
 #include <cstdarg>
@@ -720,6 +721,22 @@ int launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
     return ok();
 }
 
+// What hashgrid_debug_wait_limit set, or nothing (< 0).
+std::atomic<int64_t> g_wait_limit{-1};
+
+// How long a layer's kernel waits. Test hook of the checked build: HASHGRID_CHECK_GIVE_UP=role,n,parity makes the nth wait
+// of a role's warps give up (copying 1, multiplying 2, writing out 3, making dz 4), in the even (0), odd (1) or all (2) blocks.
+hg::linear::Patience patience() {
+    const int64_t limit = g_wait_limit.load(std::memory_order_relaxed);
+    hg::linear::Patience p = {};
+    p.polls = limit < 0 ? hg::mlp::kWaitLimit : (uint32_t)std::min<int64_t>(limit, hg::mlp::kWaitLimit);
+#ifdef HASHGRID_CHECKED
+    if (const char* text = std::getenv("HASHGRID_CHECK_GIVE_UP"))
+        if (std::sscanf(text, "%d,%d,%d", &p.role, &p.nth, &p.parity) != 3) p.role = p.nth = 0;
+#endif
+    return p;
+}
+
 // How a product is cut.
 struct Plan {
     int bn;       // tile width, a multiple of 16
@@ -880,6 +897,7 @@ int launch_products(const Product* p, int count, const Plan& plan, const char* w
     hl::Gemms l;
     std::memcpy(&l.of[0], &p[0].g, sizeof(hl::Gemm));
     std::memcpy(&l.of[1], &p[count - 1].g, sizeof(hl::Gemm));
+    l.patience = patience();
     l.second = count > 1 ? (int)p[0].grid : 0x7fffffff;
     const int64_t grid = p[0].grid + (count > 1 ? p[1].grid : 0);
     const size_t smem = std::max(p[0].smem, p[count - 1].smem);
@@ -1036,6 +1054,7 @@ int launch_narrow_backward(const hashgrid_linear_s* l, int act, const Array& dy,
     g.parts = parts;
     g.want_db = want_db;
     g.status = status;
+    g.patience = patience();
     const int blocks = std::min(std::min(kWorkSms, device_sms()), ceil_div(N, hl::kBm));
     const size_t smem = hl::narrow_smem(g.stages * g.stage_bytes, g.w_bytes);
     auto k = l->in <= 64 ? (vectors ? hl::narrow_backward_kernel<T, 1, true> : hl::narrow_backward_kernel<T, 1, false>)
@@ -1574,6 +1593,11 @@ int hashgrid_debug_indices(hashgrid_t h, const float* x, int64_t N, uint32_t* id
             hg::indices_kernel<<<(unsigned)blocks, threads, 0, s>>>(h->lp, x, N, idx_out);
         return launch_status("debug_indices");
     });
+}
+
+int hashgrid_debug_wait_limit(int64_t polls) {
+    g_wait_limit.store(polls, std::memory_order_relaxed);
+    return ok();
 }
 
 int hashgrid_linear_create(int in, int out, int dtype, int activation, hashgrid_linear_t* layer) {

@@ -371,6 +371,16 @@ constexpr int kMaxStages = 16;
 constexpr int kSegment = 12;  // 64-wide steps of K (16 took it to the 1e-6 of plain fp32 sums, 12 leaves a quarter of room)
 constexpr int kStaging = kOutWarps * 32 * 32 * 4;
 
+// How long the warps of a kernel wait. The checked build can make the nth wait of a role give up at once, in the
+// blocks of one parity or (2) in all.
+struct Patience {
+    uint32_t polls;
+#ifdef HASHGRID_CHECKED
+    int role, nth, parity;
+#endif
+};
+enum Role { kCopies = 1, kMmas = 2, kOut = 3, kSlopes = 4 };
+
 struct Side {             // one operand's share of a stage: `boxes` boxes of box_rows x 64 elements
     int mn;               // k runs along the array's columns
     int box_rows, boxes;
@@ -402,6 +412,7 @@ struct Gemm {
 struct Gemms {
     Gemm of[2];
     int second;
+    Patience patience;
 };
 
 __host__ __device__ constexpr size_t gemm_smem(int stage_bytes_in_all, bool two = false) {
@@ -472,30 +483,49 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// A warp's waits.
+struct Waits {
+    volatile int* abort_flag;  // of the block
+    uint32_t polls;
+#ifdef HASHGRID_CHECKED
+    int left;
+#endif
+    __device__ __forceinline__ Waits(volatile int* flag, const Patience& p, Role role) : abort_flag(flag), polls(p.polls) {
+#ifdef HASHGRID_CHECKED
+        left = p.role == role && (p.parity == 2 || p.parity == (int)(blockIdx.x & 1u)) ? p.nth : 0;
+#else
+        (void)role;
+#endif
+    }
+};
+
 // A bounded wait of a whole warp, which also ends once another role of the block has given up. All lanes get the
 // same answer, false if any of them gave up, and none goes on before the others: a lane that fell behind by two
 // phases of a barrier would wait for a parity that had passed, and lanes that disagreed would part for good. A block
 // of a pair (kPair) tells the other one that it gave up.
 template <bool kPair>
-__device__ __forceinline__ bool warp_waits(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-    uint32_t done = 0;
-    for (uint32_t it = 0; it < mlp::kWaitLimit; ++it) {
+__device__ __forceinline__ bool warp_waits(uint32_t bar, uint32_t parity, Waits& w) {
+    uint32_t done = 0, polls = w.polls;
+#ifdef HASHGRID_CHECKED
+    if (w.left > 0 && --w.left == 0) polls = 0;
+#endif
+    for (uint32_t it = 0; it < polls; ++it) {
         asm volatile(
             "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}\n"
             : "=r"(done)
             : "r"(bar), "r"(parity)
             : "memory");
-        if (done || ((it & 255u) == 255u && *abort_flag != 0)) break;
+        if (done || ((it & 255u) == 255u && *w.abort_flag != 0)) break;
     }
     const bool all = __all_sync(0xffffffffu, done);
     if (!all) {
-        *abort_flag = 1;
+        *w.abort_flag = 1;
         if (kPair) {
             uint32_t rank;
             asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
             asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(
-                             cluster_address((uint32_t)__cvta_generic_to_shared(const_cast<int*>(abort_flag)), rank ^ 1u)),
+                             cluster_address((uint32_t)__cvta_generic_to_shared(const_cast<int*>(w.abort_flag)), rank ^ 1u)),
                          "r"(1)
                          : "memory");
         }
@@ -630,6 +660,7 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
     if (warp == kOutWarps + 1) {
         // ------------------------------- TMA copies -------------------------------
         // (as in the MMA warp, all lanes walk and one issues)
+        Waits waits(&abort_flag, list.patience, kCopies);
         const bool issues = elect_one();
         const uint32_t bytes = g.a.bytes + (g.resident ? 0 : g.b.bytes);
         if (g.resident && kbs > 0 && issues) {
@@ -647,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
         for (Tiles t(g, first, step); t.more() && ok; t.next()) {
             const int m0 = (kPair ? 2 * t.m + (int)rank : t.m) * kBm, n0 = t.n * g.bn + (kPair ? (int)rank * (g.bn / 2) : 0);
             for (int kb = 0; kb < kbs; ++kb) {
-                if (!(ok = warp_waits<kPair>(empty + 8 * r.stage, r.phase ^ 1u, &abort_flag))) break;
+                if (!(ok = warp_waits<kPair>(empty + 8 * r.stage, r.phase ^ 1u, waits))) break;
                 const uint32_t bar = full0 + 8 * r.stage, sa = sm0 + r.stage * g.stage_bytes, sb = sa + g.a.bytes;
                 const int k0 = (kb0 + kb) * kBk;
                 if (!kPair && issues) arrive_expect(bar, bytes);
@@ -669,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
         if (lane == 0) copies_issued = issued;
         // the block (and with it its barriers) stays until the MMAs' last reports of free stages have arrived
         Ring last = r;
-        for (int s = 0; s < g.stages && ok; ++s, last.next(g.stages)) ok = warp_waits<kPair>(empty + 8 * last.stage, last.phase ^ 1u, &abort_flag);
+        for (int s = 0; s < g.stages && ok; ++s, last.next(g.stages)) ok = warp_waits<kPair>(empty + 8 * last.stage, last.phase ^ 1u, waits);
     } else if (warp == kOutWarps) {
         // ---------------------------------- MMAs ----------------------------------
         // The whole warp walks through the loop and one lane issues: with everything uniform the descriptors stay
@@ -677,16 +708,17 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
         // thousand cycles for 8192 x 4096 x 4096).
         if (rank == 0) {
             const bool issues = elect_one();
+            Waits waits(&abort_flag, list.patience, kMmas);
             Ring r;
             uint32_t i = 0;
-            bool ok = kbs == 0 || !g.resident || warp_waits<kPair>(bfull, 0, &abort_flag);
+            bool ok = kbs == 0 || !g.resident || warp_waits<kPair>(bfull, 0, waits);
             // Descriptors count addresses in units of 16 bytes: a stage and a step of 16 k are additions to them.
             const uint32_t step_a = g.a.mn ? 128 : 2, step_b = g.b.mn ? 128 : 2, stage = g.stage_bytes >> 4;
             const uint32_t next_b = g.resident ? g.b.bytes >> 4 : 0;
             const uint64_t a0 = swizzled_desc(sm0, 64 * 128), b0 = swizzled_desc(g.resident ? sb0 : sm0 + g.a.bytes, 64 * 128);
             for (Tiles t(g, first, step); t.more() && ok && kbs > 0; t.next(), ++i) {
                 uint32_t acc = tmem + (i & 1u) * g.columns;
-                if (!(ok = warp_waits<kPair>(room + 8 * (i & 1u), ((i >> 1) & 1u) ^ 1u, &abort_flag))) break;
+                if (!(ok = warp_waits<kPair>(room + 8 * (i & 1u), ((i >> 1) & 1u) ^ 1u, waits))) break;
                 mlp::fence_after();
                 int kseg = 0;
                 for (int kb = 0; kb < kbs; ++kb, ++kseg) {
@@ -696,10 +728,10 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
                         ++i;
                         kseg = 0;
                         acc = tmem + (i & 1u) * g.columns;
-                        if (!(ok = warp_waits<kPair>(room + 8 * (i & 1u), ((i >> 1) & 1u) ^ 1u, &abort_flag))) break;
+                        if (!(ok = warp_waits<kPair>(room + 8 * (i & 1u), ((i >> 1) & 1u) ^ 1u, waits))) break;
                         mlp::fence_after();
                     }
-                    if (!(ok = warp_waits<kPair>(full + 8 * r.stage, r.phase, &abort_flag))) break;
+                    if (!(ok = warp_waits<kPair>(full + 8 * r.stage, r.phase, waits))) break;
                     mlp::fence_after();
                     const uint64_t da = a0 + (uint32_t)r.stage * stage, db = b0 + (g.resident ? (uint32_t)kb * next_b : (uint32_t)r.stage * stage);
 #pragma unroll
@@ -717,6 +749,7 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
         }
     } else {
         // -------------------------------- way out ---------------------------------
+        Waits waits(&abort_flag, list.patience, kOut);
         const int quarter = warp & 3, half = warp >> 2, chunks = (g.bn + 31) / 32;
         const Epilogue e = g.e;  // in registers: read through the chosen product, each store would make it suspect
         [[maybe_unused]] void* out = g.split_stride != 0 ? static_cast<float*>(e.out) + part * g.split_stride : e.out;
@@ -812,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
                 }
             };
             auto wait_accumulator = [&]() {
-                const bool ok = warp_waits<kPair>(done + 8 * (i & 1u), (i >> 1) & 1u, &abort_flag);
+                const bool ok = warp_waits<kPair>(done + 8 * (i & 1u), (i >> 1) & 1u, waits);
                 mlp::fence_after();
                 return ok;
             };
@@ -1119,6 +1152,7 @@ struct Narrow {
     float* parts;                      // [blocks][out * in + out]
     int want_db;
     int* status;
+    Patience patience;
 };
 
 __host__ __device__ constexpr size_t narrow_smem(int stage_bytes_in_all, int w_bytes) {
@@ -1177,6 +1211,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
     if (warp == 9) {
         // ------------------------------- TMA copies -------------------------------
         const bool issues = elect_one();
+        Waits waits(&abort_flag, g.patience, kCopies);
         bool ok = true;
         if (dx && issues) {
             arrive_expect(wfull, g.w_bytes);
@@ -1185,7 +1220,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
         Ring r;
         int issued = 0;
         for (int i = 0; i < mine; ++i) {
-            if (!(ok = warp_waits<false>(empty + 8 * r.stage, r.phase ^ 1u, &abort_flag))) break;
+            if (!(ok = warp_waits<false>(empty + 8 * r.stage, r.phase ^ 1u, waits))) break;
             const uint32_t bar = full + 8 * r.stage, s = sm0 + r.stage * g.stage_bytes;
             const int m0 = (int)(blockIdx.x + i * gridDim.x) * kBm;
             if (issues) {
@@ -1201,21 +1236,22 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
         if (lane == 0) copies_issued = issued;
         // the block (and with it its barriers) stays until the MMAs' last reports of free stages have arrived
         Ring last = r;
-        for (int i = 0; i < g.stages && ok; ++i, last.next(g.stages)) ok = warp_waits<false>(empty + 8 * last.stage, last.phase ^ 1u, &abort_flag);
+        for (int i = 0; i < g.stages && ok; ++i, last.next(g.stages)) ok = warp_waits<false>(empty + 8 * last.stage, last.phase ^ 1u, waits);
     } else if (warp == 8) {
         // ---------------------------------- MMAs ----------------------------------
         const bool issues = elect_one();
+        Waits waits(&abort_flag, g.patience, kMmas);
         Ring r;
-        bool ok = !dx || warp_waits<false>(wfull, 0, &abort_flag);
+        bool ok = !dx || warp_waits<false>(wfull, 0, waits);
         const uint32_t dw0 = tmem + 2 * g.columns, stage = g.stage_bytes >> 4;
         const uint64_t dz_k = swizzled_desc(sm0, 0), dz_mn = swizzled_desc(sm0, kBox), x_mn = swizzled_desc(sm0 + x_at, kBox),
                        w_mn = swizzled_desc(w0, g.k_out * 128);
         for (int i = 0; i < mine && ok; ++i) {
             const int b = i & 1, group = i / kFlush, f = group & 1;
-            if (!(ok = warp_waits<false>(full + 8 * r.stage, r.phase, &abort_flag))) break;
-            if (!(ok = warp_waits<false>(ready + 8 * r.stage, r.phase, &abort_flag))) break;
-            if (dx && !(ok = warp_waits<false>(room + 8 * b, ((i >> 1) & 1u) ^ 1u, &abort_flag))) break;
-            if (i % kFlush == 0 && !(ok = warp_waits<false>(wroom + 8 * f, ((group >> 1) & 1u) ^ 1u, &abort_flag))) break;
+            if (!(ok = warp_waits<false>(full + 8 * r.stage, r.phase, waits))) break;
+            if (!(ok = warp_waits<false>(ready + 8 * r.stage, r.phase, waits))) break;
+            if (dx && !(ok = warp_waits<false>(room + 8 * b, ((i >> 1) & 1u) ^ 1u, waits))) break;
+            if (i % kFlush == 0 && !(ok = warp_waits<false>(wroom + 8 * f, ((group >> 1) & 1u) ^ 1u, waits))) break;
             mlp::fence_after();
             const uint32_t off = (uint32_t)r.stage * stage;
             if (dx) {
@@ -1234,12 +1270,13 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
         }
     } else if (warp < 8) {
         // ---------------------------------- dx -----------------------------------
+        Waits waits(&abort_flag, g.patience, kOut);
         const int quarter = warp & 3, chunks = (g.in + 31) / 32;
         uint8_t* st = staging + warp * 4096;
         for (int i = 0; i < mine && dx; ++i) {
             const int b = i & 1;
             const int m0 = (int)(blockIdx.x + i * gridDim.x) * kBm + 32 * quarter;
-            if (!warp_waits<false>(done + 8 * b, (i >> 1) & 1u, &abort_flag)) break;
+            if (!warp_waits<false>(done + 8 * b, (i >> 1) & 1u, waits)) break;
             mlp::fence_after();
             for (int c = warp >> 2; c < chunks; c += 2) {
                 uint32_t v[32];
@@ -1284,6 +1321,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
         if (lane == 0) store_wait();
     } else {
         // --------------------------- dz, and dW's and db's sums ---------------------------
+        Waits waits(&abort_flag, g.patience, kSlopes);
         const int tt = threadIdx.x - 32 * 10, quarter = warp & 3, half = (warp - 10) >> 2;
         // a thread keeps one 16-byte column chunk and takes every 256 / (8 boxes_out)-th row
         const int per_row = 8 * g.boxes_out, chunk = tt % per_row, row_step = 256 / per_row, row0 = tt / per_row;
@@ -1296,7 +1334,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
         bool ok = true;
         auto flush = [&](int group) {  // adds what a group of tiles gathered in tensor memory
             const int f = group & 1;
-            if (!warp_waits<false>(wdone + 8 * f, (group >> 1) & 1u, &abort_flag)) return false;
+            if (!warp_waits<false>(wdone + 8 * f, (group >> 1) & 1u, waits)) return false;
             mlp::fence_after();
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
@@ -1314,7 +1352,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
         };
         Ring r;
         for (int i = 0; i < mine && ok; ++i) {
-            if (!(ok = warp_waits<false>(full + 8 * r.stage, r.phase, &abort_flag))) break;
+            if (!(ok = warp_waits<false>(full + 8 * r.stage, r.phase, waits))) break;
             uint8_t* s = sm + r.stage * g.stage_bytes + box_at;
             if (g.act != kNoAct || g.want_db) {
 #pragma unroll 2

@@ -2,6 +2,8 @@
 import os
 import re
 
+import pytest
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "multiresolution_hash_grid_b200", "csrc")
 
 
@@ -97,3 +99,104 @@ def test_copies_in_flight_of_a_pair_are_all_counted():
             for second in range(max(0, first - stages), first + stages + 1):
                 assert left_waiting(stages, first, second) == []
                 assert (left_waiting(stages, first, second, mended=False) == []) == (first == second)
+
+
+SHAPES = [(16, 2048, 1024), (333, 77, 130), (2000, 64, 96), (50000, 64, 64), (40, 4096, 264),  # over clusters, odd, plain, kept weights
+          (19100, 512, 160), (5000, 1600, 1030), (9700, 1000, 300),                            # pairs, also gathering
+          (90001, 64, 64), (20000, 128, 128), (30000, 27, 31)]                                 # one-pass backward
+
+
+def calls(hg, torch, shape, y32):
+    """One forward and one backward call of a layer as a function that returns their outputs and their status words."""
+    N, K, M = shape
+    gen = torch.Generator(device="cuda").manual_seed(N + K)
+    layer = hg.Linear(K, M, activation=hg.HASHGRID_ACT_RELU)
+    x, w, dy, z = (torch.randn(*s, device="cuda", generator=gen).bfloat16() for s in ((N, K), (M, K), (N, M), (N, M)))
+    kind = torch.float32 if y32 else torch.bfloat16
+    out = [torch.empty(N, M, device="cuda", dtype=kind), torch.empty(N, K, device="cuda", dtype=kind),
+           torch.empty(M, K, device="cuda"), torch.empty(M, device="cuda")]
+    work, status = layer.workspace(N, "cuda"), torch.zeros(8, dtype=torch.int32, device="cuda")
+
+    def run():
+        status.zero_()
+        for t in out:
+            t.fill_(7.0)
+        layer.forward(x, w, y=out[0], workspace=work, device_status=status[:4])
+        layer.backward(dy, x, w, z=z, dL_dx=out[1], dL_dw=out[2], dL_db=out[3], workspace=work, device_status=status[4:])
+        torch.cuda.synchronize()
+        return [t.clone() for t in out], status[::4].tolist()
+    return run
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_waits_that_run_out(shape):
+    """With a limit of no polls each call gives up and says so; with few, it gives up or is right; afterwards it is right."""
+    import torch
+
+    import multiresolution_hash_grid_b200 as hg
+    for y32 in (False, True):
+        run = calls(hg, torch, shape, y32)
+        want, status = run()
+        assert status == [0, 0]
+        try:
+            for limit in (0, 1, 2, 3, 5, 9, 30, 0):
+                hg.hashgrid_debug_wait_limit(limit)
+                got, status = run()
+                assert status == [1, 1] or limit > 0
+                if status[0] == 0:
+                    assert torch.equal(got[0], want[0])
+                if status[1] == 0:
+                    assert all(torch.equal(a, b) for a, b in zip(got[1:], want[1:]))
+        finally:
+            hg.hashgrid_debug_wait_limit()
+        got, status = run()
+        assert status == [0, 0] and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+GIVE_UP = r"""
+import os, time, torch, multiresolution_hash_grid_b200 as hg
+from tests.test_layer_waits import SHAPES, calls
+assert "checked" in hg.hashgrid_version()
+seen = set()
+for shape in SHAPES:
+    for y32 in (False, True):
+        run = calls(hg, torch, shape, y32)
+        want, status = run()
+        assert status == [0, 0], shape
+        for role in (1, 2, 3, 4):
+            for nth in (1, 2, 3, 6):
+                for parity in (0, 1, 2):
+                    os.environ["HASHGRID_CHECK_GIVE_UP"] = "%d,%d,%d" % (role, nth, parity)
+                    t = time.time()
+                    got, status = run()
+                    assert time.time() - t < 20, (shape, role, nth, parity)
+                    assert role == 4 or nth > 1 or parity != 2 or status == [1, 1], (shape, role, status)
+                    if status[0] == 0:
+                        assert torch.equal(got[0], want[0])
+                    else:
+                        seen.add((role, nth))
+                    if status[1] == 0:
+                        assert all(torch.equal(a, b) for a, b in zip(got[1:], want[1:]))
+                    else:
+                        seen.add((role, nth))
+        del os.environ["HASHGRID_CHECK_GIVE_UP"]
+        got, status = run()
+        assert status == [0, 0] and all(torch.equal(a, b) for a, b in zip(got, want)), shape
+    print(shape, flush=True)
+assert len(seen) == 16, seen
+print("ok")
+"""
+
+
+@pytest.mark.gpu
+@pytest.mark.timeout(900)
+def test_any_role_gives_up_at_any_time():
+    """The copying, the multiplying, the writing and the dz warps in turn, at their first and at later waits, with
+    copies and products under way, in the blocks of one side of a pair or in all: each call returns and says so."""
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", GIVE_UP], cwd=root, env=dict(os.environ, HASHGRID_CHECKED="1"), capture_output=True,
+                       text=True, timeout=800)
+    assert r.returncode == 0 and r.stdout.endswith("ok\n"), r.stdout[-2000:] + r.stderr[-2000:]
