@@ -77,7 +77,8 @@ enum hashgrid_status {
     HASHGRID_ERR_ALIGN = 2,        /* a pointer is not 16-byte aligned */
     HASHGRID_ERR_CUDA = 3,         /* a CUDA runtime call or a launch failed */
     HASHGRID_ERR_OOM = 4,          /* host allocation of the handle failed */
-    HASHGRID_ERR_DEVICE_CHECK = 5  /* checked build only: a device-side range check tripped */
+    HASHGRID_ERR_DEVICE_CHECK = 5, /* checked build only: a device-side range check tripped */
+    HASHGRID_ERR_TIMEOUT = 6       /* a wait of an earlier layer call ran out: its outputs are incomplete */
 };
 
 /* The checked build (libhashgrid_checked.so, compiled with -DHASHGRID_CHECKED) tests every
@@ -419,12 +420,18 @@ int hashgrid_linear_params(hashgrid_linear_t layer, int *in, int *out, int *dtyp
  * workspace: workspace_bytes >= hashgrid_linear_forward_workspace(layer, N, ldx) of device memory
  * that no other call uses until this one has finished (a captured graph uses it at every
  * replay); its contents need no preparation and mean nothing afterwards.
- * device_status: as for hashgrid_mlp_forward (NULL, or a device int the caller sets to 0 and
- * the kernel sets to 1 if a bounded wait ran out, y being incomplete then).
+ * device_status: NULL, or a device int the caller sets to 0 and the kernel sets to 1 if a bounded
+ * wait ran out, y being incomplete then. Where it is NULL (in a captured graph too), the first
+ * layer call on the device after that returns HASHGRID_ERR_TIMEOUT instead, and does nothing else;
+ * hashgrid_linear_status does so without a call.
  */
 int hashgrid_linear_forward(hashgrid_linear_t layer, const void *x, int64_t ldx, int64_t N, const void *w,
                             const float *b, const void *residual, int64_t ldr, void *y, int64_t ldy, int y_dtype,
                             void *z, void *workspace, size_t workspace_bytes, int *device_status, void *cuda_stream);
+
+/* HASHGRID_ERR_TIMEOUT, once, if a layer call without device_status whose work has finished gave up a
+ * wait on the current device, else HASHGRID_OK. Does not wait for the device. */
+int hashgrid_linear_status(void);
 
 /* Bytes of workspace that the two calls need for N rows of these strides (0 for a NULL layer or
  * an N outside [1, 2^31 - 256)). The forward call needs some only where rows do not begin on
@@ -449,7 +456,8 @@ size_t hashgrid_linear_backward_workspace(hashgrid_linear_t layer, int64_t N, in
  * lddx apart; dL_dw: [out][in] of dw_dtype (HASHGRID_F32 or the layer's dtype), contiguous;
  * dL_db: [out] fp32. Each of the three may be NULL, and is not computed then; all are
  * OVERWRITTEN. N = 0 writes zeros to dL_dw and dL_db. No output may overlap an input.
- * workspace: as for the forward call, of hashgrid_linear_backward_workspace bytes.
+ * workspace: as for the forward call, of hashgrid_linear_backward_workspace bytes. device_status: as
+ * for the forward call.
  */
 int hashgrid_linear_backward(hashgrid_linear_t layer, const void *dL_dy, int64_t lddy, const void *x, int64_t ldx,
                              int64_t N, const void *w, const void *z, void *dL_dx, int64_t lddx, int dx_dtype,

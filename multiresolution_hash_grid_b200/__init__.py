@@ -37,6 +37,7 @@ HASHGRID_ERR_ALIGN = 2
 HASHGRID_ERR_CUDA = 3
 HASHGRID_ERR_OOM = 4
 HASHGRID_ERR_DEVICE_CHECK = 5
+HASHGRID_ERR_TIMEOUT = 6
 
 MAX_LEVELS = 32
 
@@ -113,6 +114,7 @@ def _load() -> ctypes.CDLL:
         "hashgrid_linear_forward_workspace": (sz, [vp, i64, i64]),
         "hashgrid_linear_backward_workspace": (sz, [vp, i64, i64, i64]),
         "hashgrid_linear_backward": (i32, [vp, vp, i64, vp, i64, i64, vp, vp, vp, i64, i32, vp, i32, vp, vp, sz, vp, vp]),
+        "hashgrid_linear_status": (i32, []),
         "hashgrid_debug_wait_limit": (i32, [i64]),
         "hashgrid_adamw_create": (i32, [ctypes.POINTER(AdamwTensor), i32, ctypes.POINTER(vp)]),
         "hashgrid_adamw_destroy": (i32, [vp]),
@@ -292,6 +294,11 @@ def hashgrid_linear_backward(layer: int, dL_dy, lddy: int, x, ldx: int, N: int, 
                                         _ptr(device_status), _stream(stream)))
 
 
+def hashgrid_linear_status() -> None:
+    """Raises if an earlier layer call without a status word, its work done by now, left its outputs incomplete."""
+    _check(lib.hashgrid_linear_status())
+
+
 def hashgrid_debug_wait_limit(polls: int = -1) -> None:
     _check(lib.hashgrid_debug_wait_limit(polls))
 
@@ -417,7 +424,8 @@ class Linear:
     """A linear layer with its activation and residual, and its gradients (``hashgrid_linear_*``):
     ``z = x w^T + b``, ``y = act(z) + residual``. Holds a handle only; weights are arguments. Tensors
     are [N, features] with contiguous rows (any row stride), of the layer's 16-bit type where not
-    said otherwise."""
+    said otherwise. A call that gave up a wait and left its outputs incomplete says so in ``device_status`` (an int32
+    CUDA tensor of zeros), or, without one, through the next call's or ``hashgrid_linear_status()``'s error."""
 
     def __init__(self, in_features: int, out_features: int, dtype: int = HASHGRID_BF16,
                  activation: int = HASHGRID_ACT_NONE):

@@ -737,6 +737,51 @@ hg::linear::Patience patience() {
     return p;
 }
 
+// A device's status word for layer calls that are given none: pinned memory, which the kernels write and the host reads
+// at the next call. NULL where there is none to be had.
+volatile int* given_up_word() {
+    constexpr int kDevices = 64, kApart = 32;
+    static std::mutex lock;
+    static std::atomic<int*> words{nullptr};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) {
+        cudaGetLastError();
+        return nullptr;
+    }
+    int* p = words.load(std::memory_order_acquire);
+    if (p == nullptr) {
+        std::lock_guard<std::mutex> hold(lock);
+        p = words.load(std::memory_order_relaxed);
+        if (p == nullptr) {
+            // the first call may come inside a stream's capture, which this allocation is no part of
+            cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+            cudaThreadExchangeStreamCaptureMode(&mode);
+            void* fresh = nullptr;
+            const cudaError_t e = cudaHostAlloc(&fresh, kDevices * kApart * sizeof(int), cudaHostAllocPortable | cudaHostAllocMapped);
+            cudaThreadExchangeStreamCaptureMode(&mode);
+            if (e != cudaSuccess) {
+                cudaGetLastError();
+                return nullptr;
+            }
+            p = static_cast<int*>(fresh);
+            std::memset(p, 0, kDevices * kApart * sizeof(int));
+            words.store(p, std::memory_order_release);
+        }
+    }
+    return p + dev * kApart;
+}
+
+// Reports, once, that an earlier layer call without a status word gave up.
+int check_given_up() {
+    volatile int* word = given_up_word();
+    if (word == nullptr || *word == 0) return ok();
+    *word = 0;
+    return fail(HASHGRID_ERR_TIMEOUT, "an earlier layer call on this device gave up a wait: its outputs are incomplete");
+}
+
+// The status word of a layer call.
+int* status_word(int* device_status) { return device_status != nullptr ? device_status : const_cast<int*>(given_up_word()); }
+
 // How a product is cut.
 struct Plan {
     int bn;       // tile width, a multiple of 16
@@ -1595,6 +1640,8 @@ int hashgrid_debug_indices(hashgrid_t h, const float* x, int64_t N, uint32_t* id
     });
 }
 
+int hashgrid_linear_status(void) { return check_given_up(); }
+
 int hashgrid_debug_wait_limit(int64_t polls) {
     g_wait_limit.store(polls, std::memory_order_relaxed);
     return ok();
@@ -1654,6 +1701,8 @@ int hashgrid_linear_forward(hashgrid_linear_t l, const void* x, int64_t ldx, int
     if (int rc = check_workspace(workspace, workspace_bytes, need, N)) return rc;
     if (device_status != nullptr)
         if (int rc = check_buffer(device_status, sizeof(int), "device_status")) return rc;
+    if (int rc = check_given_up()) return rc;
+    device_status = status_word(device_status);
     const hg::linear::Epilogue e{b, residual, y, z, ldr, ldy, l->out, y_dtype == HASHGRID_F32, l->act, hg::kChkOut};
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
     return run_checked(s, {{hg::kChkX, x, strided_bytes(N, l->in, ldx, 2)}, {hg::kChkWeights, w, (size_t)l->in * l->out * 2},
@@ -1711,6 +1760,8 @@ int hashgrid_linear_backward(hashgrid_linear_t l, const void* dL_dy, int64_t ldd
     if (int rc = check_workspace(workspace, workspace_bytes, need, N)) return rc;
     if (device_status != nullptr)
         if (int rc = check_buffer(device_status, sizeof(int), "device_status")) return rc;
+    if (int rc = check_given_up()) return rc;
+    device_status = status_word(device_status);
     return run_checked(s, {{hg::kChkX, x, strided_bytes(N, l->in, ldx, 2)}, {hg::kChkWeights, w, (size_t)l->in * l->out * 2},
                            {hg::kChkBias, dL_db, bb}, {hg::kChkDout, dL_dy, strided_bytes(N, l->out, lddy, 2)},
                            {hg::kChkZ, z, (size_t)N * l->out * 2}, {hg::kChkWork, workspace, need},

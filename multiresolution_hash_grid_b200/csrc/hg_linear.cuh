@@ -561,6 +561,13 @@ __device__ __forceinline__ void stage_row32(uint8_t* st, int lane, const float (
         *reinterpret_cast<float4*>(st + lane * 128 + ((u ^ (lane & 7)) << 4)) = make_float4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
 }
 
+// The status word may be the host's memory.
+__device__ __forceinline__ void report_given_up(int* status) {
+    if (status == nullptr) return;
+    *static_cast<volatile int*>(status) = 1;
+    __threadfence_system();
+}
+
 // Position in a ring of stages.
 struct Ring {
     int stage = 0;
@@ -995,7 +1002,7 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
         if (kPair) cluster_sync();
     }
     mlp::fence_after();
-    if (threadIdx.x == 0 && abort_flag != 0 && g.status != nullptr) atomicExch(g.status, 1);
+    if (threadIdx.x == 0 && abort_flag != 0) report_given_up(g.status);
     __syncwarp();
     if (warp == 0) {
         if (kPair) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(g.tmem_columns) : "memory");
@@ -1428,7 +1435,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
         __syncthreads();
     }
     mlp::fence_after();
-    if (threadIdx.x == 0 && abort_flag != 0 && g.status != nullptr) atomicExch(g.status, 1);
+    if (threadIdx.x == 0 && abort_flag != 0) report_given_up(g.status);
     __syncwarp();
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(g.tmem_columns) : "memory");

@@ -200,3 +200,73 @@ def test_any_role_gives_up_at_any_time():
     r = subprocess.run([sys.executable, "-c", GIVE_UP], cwd=root, env=dict(os.environ, HASHGRID_CHECKED="1"), capture_output=True,
                        text=True, timeout=800)
     assert r.returncode == 0 and r.stdout.endswith("ok\n"), r.stdout[-2000:] + r.stderr[-2000:]
+
+
+@pytest.mark.gpu
+def test_a_call_that_gave_up_without_a_status_word_is_reported():
+    """By the next call, which does nothing else, or by the status call; once; also out of a captured graph."""
+    import torch
+
+    import multiresolution_hash_grid_b200 as hg
+    layer = hg.Linear(64, 96)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x, w = (torch.randn(*s, device="cuda", generator=gen).bfloat16() for s in ((500, 64), (96, 64)))
+    want = layer.forward(x, w)
+    hg.hashgrid_linear_status()
+    y, seven = torch.empty_like(want), torch.full_like(want, 7.0)
+
+    def give_up():
+        try:
+            hg.hashgrid_debug_wait_limit(0)
+            layer.forward(x, w, y=y)
+        finally:
+            hg.hashgrid_debug_wait_limit()
+
+    def refused(call):
+        with pytest.raises(hg.HashGridError, match="incomplete") as e:
+            call()
+        assert e.value.code == hg.HASHGRID_ERR_TIMEOUT
+    for call in (lambda: layer.forward(x, w, y=seven), lambda: layer.backward(want, x, w), hg.hashgrid_linear_status):
+        give_up()
+        torch.cuda.synchronize()
+        refused(call)
+        torch.cuda.synchronize()
+        assert bool((seven == 7.0).all())
+        assert torch.equal(layer.forward(x, w), want)
+        hg.hashgrid_linear_status()
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    hg.hashgrid_debug_wait_limit(0)
+    layer.forward(x, w, y=y, device_status=status)
+    hg.hashgrid_debug_wait_limit()
+    torch.cuda.synchronize()
+    assert int(status[0]) == 1
+    hg.hashgrid_linear_status()                        # a call with a status word of its own is not reported twice
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        give_up()
+    torch.cuda.synchronize()
+    hg.hashgrid_linear_status()
+    g.replay()
+    torch.cuda.synchronize()
+    refused(hg.hashgrid_linear_status)
+
+
+@pytest.mark.gpu
+def test_the_first_call_of_a_process_may_be_captured():
+    import subprocess
+    import sys
+    code = r"""
+import torch, multiresolution_hash_grid_b200 as hg
+x, w = torch.ones(300, 64, device="cuda").bfloat16(), torch.ones(96, 64, device="cuda").bfloat16()
+y, layer, g = torch.zeros(300, 96, device="cuda").bfloat16(), hg.Linear(64, 96), torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    layer.forward(x, w, y=y)
+g.replay()
+torch.cuda.synchronize()
+assert bool((y == 64).all())
+hg.hashgrid_linear_status()
+print("ok")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, env=dict(os.environ, HASHGRID_CHECKED="0"), capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "ok" in r.stdout, r.stdout + r.stderr
