@@ -609,6 +609,9 @@ size_t strided_bytes(int64_t rows, int64_t cols, int64_t ld, size_t elem) {
 int check_rows(const void* p, int64_t rows, int64_t cols, int64_t ld, size_t elem, const char* name) {
     if (ld < cols) return fail(HASHGRID_ERR_ARG, "%s: row stride %lld is below its width %lld", name, (long long)ld, (long long)cols);
     if (rows > 1 && ld >= ((int64_t)1 << 37)) return fail(HASHGRID_ERR_ARG, "%s: row stride %lld is too large", name, (long long)ld);
+    // an extent in bytes could pass 64 bits and come out small
+    if (rows > 1 && rows - 1 > ((int64_t)1 << 48) / ld)
+        return fail(HASHGRID_ERR_ARG, "%s: %lld rows %lld elements apart are more than any memory holds", name, (long long)rows, (long long)ld);
     return check_buffer(p, strided_bytes(rows, cols, ld, elem), name);
 }
 
