@@ -1,0 +1,90 @@
+"""Values of the layers that other tests do not reach: long sums, NaN, many groups of tiles, the way on to the tables."""
+import numpy as np
+import pytest
+import torch
+
+import multiresolution_hash_grid_b200 as hg
+from tests.test_linear import ACTS, check_backward
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("tiles", [6, 7, 12, 13, 18, 25])
+@pytest.mark.parametrize("K,M", [(64, 64), (32, 64), (128, 24), (128, 128), (24, 104)])
+def test_one_pass_backward_over_many_groups_of_tiles(K, M, tiles):
+    """So many tiles of 128 rows for each of 148 blocks, with one more for some and a ragged last one: dW's sums leave tensor
+    memory every six tiles, by two accumulators in turn, each several times over, and in groups of one tile too."""
+    for rows in ((148 * tiles) * 128, (148 * tiles) * 128 + 1, (148 * tiles + 100) * 128 - 51):
+        act = ACTS[(tiles + rows) % 4]
+        check_backward(rows, K, M, hg.HASHGRID_BF16, act, dx32=tiles % 2 == 0, dw32=True, seed=tiles, want=(tiles % 5 != 0, True, True))
+
+
+@pytest.mark.skipif(hg.CHECKED, reason="the checked build is for one stream at a time")
+def test_optimiser_steps_beside_layers():
+    """Steps of three lists on streams of their own, while layers run on others, do what they do alone."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    base = [torch.randn(n, device="cuda", generator=gen) for n in (1, 255, 4097, 1 << 20, 300000)]
+    grad = [torch.randn(p.numel(), device="cuda", generator=gen).bfloat16() for p in base]
+
+    def lists():
+        made = []
+        for bits in (32, 8, 8):
+            p = [t.clone() for t in base]
+            made.append((p, hg.AdamW(p, [g.clone() for g in grad], bits=bits, weight_decay=0.01)))
+        return made
+    layer, work = hg.Linear(64, 64, activation=hg.HASHGRID_ACT_RELU), hg.Linear(64, 64).workspace(60000, "cuda")
+    wide = hg.Linear(1024, 512)
+    rnd = lambda *s: torch.randn(*s, device="cuda", generator=gen).bfloat16()  # noqa: E731
+    x, w, dy, z, xw, ww = rnd(60000, 64), rnd(64, 64), rnd(60000, 64), rnd(60000, 64), rnd(5000, 1024), rnd(512, 1024)
+    out = [torch.empty(60000, 64, device="cuda"), torch.empty(64, 64, device="cuda"), torch.empty(64, device="cuda")]
+    yw = torch.empty(5000, 512, device="cuda").bfloat16()
+
+    def layers():
+        layer.backward(dy, x, w, z=z, dL_dx=out[0], dL_dw=out[1], dL_db=out[2], workspace=work)
+        wide.forward(xw, ww, y=yw)
+    layers()
+    alone = lists()
+    for k in range(1, 31):
+        for i, (_, opt) in enumerate(alone):
+            opt.step(k, lr=1e-3, seed=i)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in out + [yw]]
+    beside = lists()
+    for t in out + [yw]:
+        t.zero_()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    for k in range(1, 31):
+        with torch.cuda.stream(streams[3]):
+            layers()
+        for i, (_, opt) in enumerate(beside):
+            with torch.cuda.stream(streams[i]):
+                opt.step(k, lr=1e-3, seed=i)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out + [yw], want))
+    for (p, a), (q, b) in zip(alone, beside):
+        assert all(torch.equal(s, t) for s, t in zip(p, q))
+        assert all(torch.equal(s.view(torch.uint8), t.view(torch.uint8)) for s, t in zip(a.m + a.v, b.m + b.v))
+
+
+def test_gradient_of_the_tables_through_the_layers():
+    """What two layers hand down as dL/d(encoding), in fp32, becomes the tables' gradient that the oracle has for it."""
+    import oracle
+    from tests.test_parity import check_gradient
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    grid, og = hg.HashGrid(L=4, F=2, log2T=10, N_min=2, N_max=16), oracle.Grid(4, 2, 10, 2, 16)
+    table = torch.rand(4, 1024, 2, device="cuda", generator=gen) * 2 - 1
+    pts = torch.rand(1777, 3, device="cuda", generator=gen)
+    l1, l2 = hg.Linear(8, 64, activation=hg.HASHGRID_ACT_SILU), hg.Linear(64, 4)
+    w1, w2 = (torch.randn(*s, device="cuda", generator=gen).bfloat16() for s in ((64, 8), (4, 64)))
+    enc = grid.forward(pts, table).bfloat16()
+    z = torch.empty(1777, 64, device="cuda", dtype=torch.bfloat16)
+    h = l1.forward(enc, w1, z=z)
+    dy = torch.randn(1777, 4, device="cuda", generator=gen).bfloat16()
+    dh, _, _ = l2.backward(dy, h, w2)
+    denc, _, _ = l1.backward(dh, enc, w1, z=z, dL_dx=torch.empty(1777, 8, device="cuda"))
+    dtable = grid.backward(pts, denc)
+    torch.cuda.synchronize()
+    ref = og.backward(pts.cpu().numpy(), denc.cpu().numpy())
+    check_gradient(dtable.cpu().numpy(), ref)
+    assert np.abs(ref).max() > 0.1
