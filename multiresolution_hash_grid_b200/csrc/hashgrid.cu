@@ -911,7 +911,7 @@ int set_product(Product& p, bool half, const Array& A, const Array& B, int64_t M
     g.cluster = plan.cluster;
     // Two blocks a SM where tensor memory and shared memory allow: one's loads and stores then fill the other's gaps. The MMA
     // reads 128 rows (two boxes) of A whatever the product has: the staging area behind the stages keeps that in bounds.
-    p.gather = e.out_f32 && g.kblocks_per_split > hl::kSegment;
+    p.gather = g.kblocks_per_split > (e.out_f32 ? hl::kSegment : hl::kSegment16);
     const int per_sm = group == 1 && g.tmem_columns <= 256 && !p.gather ? 2 : 1;
     const int budget = (per_sm == 2 ? 113 : 227) * 1024 - 1024;  // less what the kernel has of its own
     g.stages = std::min(hl::kMaxStages, (budget - kept - (int)hl::gemm_smem(0, two)) / g.stage_bytes);

@@ -9,6 +9,28 @@ from tests.test_linear import ACTS, check_backward
 pytestmark = pytest.mark.gpu
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("N,K,M", [(1 << 19, 1024, 1280), (300001, 1100, 1030)])
+def test_long_sums_with_16_bit_results(N, K, M, dtype):
+    """A weight gradient in 16 bits whose rows are not cut into parts. The tensor cores' additions cut off, 1.1e-9 of the
+    result a term, 5.8e-4 for 2^19 terms, more than the rounding of fp16 at the end. Added up in fp32 every 768 terms,
+    8.4e-7 of it remains, and the at most 683 additions of such sums round by 2^-24 each, to nearest: together 1.6e-6
+    where their errors add up as their root, 2^-24 * 683 = 4.1e-5 at the very worst. Rounding the result to nearest moves
+    no sum of values of either sign: it adds half a step, 2^-11 or 2^-8, times 1 / sqrt(values), a thousandth."""
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    dy = torch.randn(N, M, device="cuda", generator=gen).to(dtype)
+    x = torch.randn(N, K, device="cuda", generator=gen).to(dtype)
+    w = torch.zeros(M, K, device="cuda", dtype=dtype)
+    code = hg.HASHGRID_F16 if dtype == torch.float16 else hg.HASHGRID_BF16
+    _, dw, _ = hg.Linear(K, M, code).backward(dy, x, w, dL_dx=None, dL_db=None, dL_dw=torch.empty_like(w))
+    ref = torch.zeros(M, K, device="cuda", dtype=torch.float64)
+    for at in range(0, N, 1 << 16):
+        ref += dy[at:at + (1 << 16)].double().t() @ x[at:at + (1 << 16)].double()
+    d = dw.double() - ref
+    bias = float((d * ref.sign()).sum() / ref.abs().sum())
+    assert abs(bias) < 4.1e-5 + 8.4e-7 + {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}[dtype] * 4 / (K * M) ** 0.5, bias
+
+
 @pytest.mark.parametrize("tiles", [6, 7, 12, 13, 18, 25])
 @pytest.mark.parametrize("K,M", [(64, 64), (32, 64), (128, 24), (128, 128), (24, 104)])
 def test_one_pass_backward_over_many_groups_of_tiles(K, M, tiles):
