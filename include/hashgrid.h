@@ -382,8 +382,8 @@ int hashgrid_get_option(hashgrid_t h, int option, int *value);
 
 typedef struct hashgrid_linear_s *hashgrid_linear_t; /* opaque, library-owned */
 
-/* act(z) of a layer and its derivative: NONE z; RELU max(z, 0), derivative 1 for z > 0 else 0;
- * GELU z (1 + erf(z / sqrt 2)) / 2; SILU z / (1 + exp(-z)). A NaN gives 0 under RELU. */
+/* act(z) of a layer and its derivative: NONE z; RELU max(z, 0), derivative 0 for z <= 0 else 1;
+ * GELU z (1 + erf(z / sqrt 2)) / 2; SILU z / (1 + exp(-z)). A NaN stays a NaN under each. */
 enum hashgrid_activation {
     HASHGRID_ACT_NONE = 0,
     HASHGRID_ACT_RELU = 1,

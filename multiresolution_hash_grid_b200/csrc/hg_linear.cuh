@@ -97,7 +97,7 @@ __device__ __forceinline__ void activate(float (&y)[kN], int act) {
     switch (act) {
         case kRelu:
 #pragma unroll
-            for (int j = 0; j < kN; ++j) y[j] = fmaxf(y[j], 0.f);  // of a NaN and 0 it returns 0
+            for (int j = 0; j < kN; ++j) asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(y[j]));  // a NaN stays one
             break;
         case kGelu:
 #pragma unroll
@@ -130,7 +130,7 @@ __device__ __forceinline__ void times_slope(float (&d)[kN], const float (&z)[kN]
     switch (act) {
         case kRelu:
 #pragma unroll
-            for (int j = 0; j < kN; ++j) d[j] = z[j] > 0.f ? d[j] : 0.f;
+            for (int j = 0; j < kN; ++j) d[j] = z[j] <= 0.f ? 0.f : d[j];  // at a NaN the gradient, a NaN itself, goes on
             break;
         case kGelu:
 #pragma unroll

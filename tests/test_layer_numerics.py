@@ -31,6 +31,29 @@ def test_long_sums_with_16_bit_results(N, K, M, dtype):
     assert abs(bias) < 4.1e-5 + 8.4e-7 + {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}[dtype] * 4 / (K * M) ** 0.5, bias
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("N,K,M", [(64, 40, 24), (70, 33, 35), (16, 2048, 1024), (9000, 64, 64), (19100, 512, 160)])
+def test_relu_passes_a_nan_on(N, K, M, dtype):
+    """A NaN in a row of x is one in that row of y, as the formula's maximum has it, and no other row has any. Where the loss
+    then gives NaN gradients they go on: z = NaN stops no gradient."""
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    code = hg.HASHGRID_F16 if dtype == torch.float16 else hg.HASHGRID_BF16
+    layer = hg.Linear(K, M, code, hg.HASHGRID_ACT_RELU)
+    x = torch.randn(N, K, device="cuda", generator=gen).to(dtype)
+    w = torch.randn(M, K, device="cuda", generator=gen).to(dtype)
+    x[3, 1] = float("nan")
+    for y in (torch.empty(N, M, device="cuda", dtype=dtype), torch.empty(N, M, device="cuda")):
+        z = torch.empty(N, M, device="cuda", dtype=dtype)
+        layer.forward(x, w, y=y, z=z)
+        assert bool(torch.isnan(y[3]).all()) and int(torch.isnan(y).sum()) == M
+    dy = torch.randn(N, M, device="cuda", generator=gen).to(dtype)
+    dy[3] = float("nan")
+    dx, dw, db = layer.backward(dy, x, w, z=z)
+    assert bool(torch.isnan(dx[3]).all()) and int(torch.isnan(dx).sum()) == K
+    assert bool(torch.isnan(dw).all()) and bool(torch.isnan(db).all())
+    assert not bool(torch.isnan(layer.forward(x, torch.zeros_like(w), torch.full((M,), -1.0, device="cuda"))[:3]).any())
+
+
 @pytest.mark.parametrize("tiles", [6, 7, 12, 13, 18, 25])
 @pytest.mark.parametrize("K,M", [(64, 64), (32, 64), (128, 24), (128, 128), (24, 104)])
 def test_one_pass_backward_over_many_groups_of_tiles(K, M, tiles):
