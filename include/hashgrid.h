@@ -416,7 +416,9 @@ int hashgrid_linear_params(hashgrid_linear_t layer, int *in, int *out, int *dtyp
  * ldy apart; z: NULL, or [N, out] contiguous of the layer's dtype, which the backward pass of
  * a layer with an activation reads. Elements of y's rows beyond `out` are left as they were.
  * Strides are at least the row's width (any value, odd ones included); 0 <= N < 2^31 - 256.
- * residual may be y itself (with ldr == ldy); no other output may overlap an input.
+ * residual may be y itself (with ldr == ldy); no other output (the workspace and the status word
+ * among them) may share a byte with an input or another output (HASHGRID_ERR_ARG). Columns of
+ * one buffer share none.
  * workspace: workspace_bytes >= hashgrid_linear_forward_workspace(layer, N, ldx) of device memory
  * that no other call uses until this one has finished (a captured graph uses it at every
  * replay); its contents need no preparation and mean nothing afterwards.
@@ -455,7 +457,8 @@ size_t hashgrid_linear_backward_workspace(hashgrid_linear_t layer, int64_t N, in
  * [N, in] of dx_dtype (HASHGRID_F32, as hashgrid_backward takes it, or the layer's dtype), rows
  * lddx apart; dL_dw: [out][in] of dw_dtype (HASHGRID_F32 or the layer's dtype), contiguous;
  * dL_db: [out] fp32. Each of the three may be NULL, and is not computed then; all are
- * OVERWRITTEN. N = 0 writes zeros to dL_dw and dL_db. No output may overlap an input.
+ * OVERWRITTEN. N = 0 writes zeros to dL_dw and dL_db. No output may share a byte with another
+ * or with an input that the call reads (HASHGRID_ERR_ARG).
  * workspace: as for the forward call, of hashgrid_linear_backward_workspace bytes. device_status: as
  * for the forward call.
  */

@@ -634,6 +634,57 @@ int check_out_type(const hashgrid_linear_s* layer, int dtype, const char* name) 
     return ok();
 }
 
+// Rows of bytes, `stride` apart.
+struct Region {
+    const char* name;
+    const void* p;
+    int64_t rows, width, stride;
+};
+
+Region region(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld, size_t elem) {
+    if (rows <= 1 || ld == cols) return Region{name, p, 1, rows * cols * (int64_t)elem, rows * cols * (int64_t)elem};
+    return Region{name, p, rows, cols * (int64_t)elem, ld * (int64_t)elem};
+}
+Region region(const char* name, const void* p, size_t bytes) { return Region{name, p, 1, (int64_t)bytes, (int64_t)bytes}; }
+
+// The smallest x >= 0 with lo <= a x mod m <= hi (0 <= a < m, 0 <= lo <= hi < m), or -1. Where no multiple of a lies
+// within [lo, hi], a x - m y does for the smallest y with m y mod a in [-hi, -lo] mod a: Euclid's steps.
+__int128 first_multiple(__int128 a, __int128 m, __int128 lo, __int128 hi) {
+    if (lo == 0) return 0;
+    if (a == 0) return -1;
+    const __int128 x = (lo + a - 1) / a;
+    if (a * x <= hi) return x;
+    const __int128 y = first_multiple(m % a, a, a - hi % a, a - lo % a);
+    return y < 0 ? -1 : (lo + m * y + a - 1) / a;
+}
+
+// Whether any byte belongs to both. Exact, so that columns of one buffer pass as different arrays.
+bool overlap(const Region& a, const Region& b) {
+    if (a.p == nullptr || b.p == nullptr || a.rows * a.width == 0 || b.rows * b.width == 0) return false;
+    const __int128 a0 = (__int128)(uintptr_t)a.p, b0 = (__int128)(uintptr_t)b.p;
+    const __int128 a1 = a0 + (__int128)(a.rows - 1) * a.stride + a.width, b1 = b0 + (__int128)(b.rows - 1) * b.stride + b.width;
+    if (a1 <= b0 || b1 <= a0) return false;
+    // a's first row that ends behind b's start
+    const __int128 i = b0 < a0 + a.width ? 0 : (b0 - a0 - a.width) / a.stride + 1, at = a0 + i * a.stride;
+    if (at <= b0) return true;
+    // the first from there on that begins, in steps of b's rows, less than b's width behind a row's start or less than its own before
+    const __int128 m = b.stride, c = (at - b0) % m;
+    if (c < b.width || c + a.width > m) return i < a.rows && at < b1;
+    const __int128 x = first_multiple(a.stride % m, m, m - a.width + 1 - c, m + b.width - 1 - c);
+    return x >= 0 && i + x < a.rows && at + x * a.stride < b1;
+}
+
+// No output may overlap another one or an input.
+int check_apart(std::initializer_list<Region> outputs, std::initializer_list<Region> inputs) {
+    for (const Region* o = outputs.begin(); o != outputs.end(); ++o) {
+        for (const Region* other = o + 1; other != outputs.end(); ++other)
+            if (overlap(*o, *other)) return fail(HASHGRID_ERR_ARG, "%s and %s overlap", o->name, other->name);
+        for (const Region& in : inputs)
+            if (overlap(*o, in)) return fail(HASHGRID_ERR_ARG, "%s and %s overlap", o->name, in.name);
+    }
+    return ok();
+}
+
 // prepare_smem once for each kernel, size and device: the attribute call costs as much as a small launch's checks.
 template <typename K>
 int prepare_smem_once(K kernel, size_t smem) {
@@ -1704,6 +1755,12 @@ int hashgrid_linear_forward(hashgrid_linear_t l, const void* x, int64_t ldx, int
     if (int rc = check_workspace(workspace, workspace_bytes, need, N)) return rc;
     if (device_status != nullptr)
         if (int rc = check_buffer(device_status, sizeof(int), "device_status")) return rc;
+    const bool in_place = residual == y && (ldr == ldy || N == 1);
+    if (int rc = check_apart({region("y", y, N, l->out, ldy, ys), region("z", z, N, l->out, l->out, 2), region("workspace", workspace, need),
+                              region("device_status", device_status, sizeof(int))},
+                             {region("x", x, N, l->in, ldx, 2), region("w", w, l->out, l->in, l->in, 2), region("b", b, 1, l->out, l->out, 4),
+                              region("residual", in_place ? nullptr : residual, N, l->out, ldr, ys)}))
+        return rc;
     if (int rc = check_given_up()) return rc;
     device_status = status_word(device_status);
     const hg::linear::Epilogue e{b, residual, y, z, ldr, ldy, l->out, y_dtype == HASHGRID_F32, l->act, hg::kChkOut};
@@ -1763,6 +1820,12 @@ int hashgrid_linear_backward(hashgrid_linear_t l, const void* dL_dy, int64_t ldd
     if (int rc = check_workspace(workspace, workspace_bytes, need, N)) return rc;
     if (device_status != nullptr)
         if (int rc = check_buffer(device_status, sizeof(int), "device_status")) return rc;
+    if (int rc = check_apart({region("dL_dx", dL_dx, N, l->in, lddx, xs), region("dL_dw", dL_dw, wb), region("dL_db", dL_db, bb),
+                              region("workspace", workspace, need), region("device_status", device_status, sizeof(int))},
+                             {region("dL_dy", dL_dy, N, l->out, lddy, 2), region("x", dL_dw != nullptr ? x : nullptr, N, l->in, ldx, 2),
+                              region("w", dL_dx != nullptr ? w : nullptr, l->out, l->in, l->in, 2),
+                              region("z", l->act != HASHGRID_ACT_NONE ? z : nullptr, N, l->out, l->out, 2)}))
+        return rc;
     if (int rc = check_given_up()) return rc;
     device_status = status_word(device_status);
     return run_checked(s, {{hg::kChkX, x, strided_bytes(N, l->in, ldx, 2)}, {hg::kChkWeights, w, (size_t)l->in * l->out * 2},
