@@ -317,6 +317,8 @@ def hashgrid_adamw_destroy(opt: int) -> None:
 
 def hashgrid_adamw_step(opt: int, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.99, eps: float = 1e-8,
                         seed: int = 0, zero_grad: bool = False, device_step=None, stream=None) -> None:
+    if seed != 0 and seed & 0xFFFFFFFF == 0:
+        raise HashGridError(HASHGRID_ERR_ARG, f"seed = {seed} is 0 in 32 bits, which would round to nearest")
     _check(lib.hashgrid_adamw_step(opt, step, _ptr(device_step), lr, beta1, beta2, eps, seed & 0xFFFFFFFF,
                                    1 if zero_grad else 0, _stream(stream)))
 

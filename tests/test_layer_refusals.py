@@ -83,3 +83,11 @@ def test_outputs_that_overlap_are_refused_and_columns_of_one_buffer_are_not():
                 layer.backward(dy, x, w, workspace=work, **bad)
     assert layer.backward(dy, x, w, dL_dx=None, dL_dw=f[:256].view(16, 16), dL_db=f[256:272], workspace=work)[0] is None
     layer.backward(dy, dy, w, workspace=work)                    # inputs may be one another
+
+
+@pytest.mark.parametrize("seed", [1 << 32, -(1 << 32), 5 << 33])
+def test_seeds_that_32_bits_make_zero(seed):
+    """Zero means rounding to nearest, which a caller who gave another seed did not ask for."""
+    with pytest.raises(hg.HashGridError, match="seed") as e:
+        hg.hashgrid_adamw_step(None, 1, 1e-3, seed=seed, stream=0)
+    assert e.value.code == A
