@@ -574,7 +574,8 @@ class AdamW:
                     raise HashGridError(HASHGRID_ERR_ARG, f"tensor {k}: {name} has shape {tuple(t.shape)}, strides {t.stride()}: "
                                                           f"{n} contiguous elements are wanted")
             for t in (m[k], v[k]):
-                if (t.element_size() == 1) != coded[k] or not (coded[k] or t.dtype == torch.float32) or                         (coded[k] and t.dtype not in (torch.float8_e4m3fn, torch.uint8)):
+                kinds = (torch.float8_e4m3fn, torch.uint8) if coded[k] else (torch.float32,)
+                if t.dtype not in kinds:
                     raise HashGridError(HASHGRID_ERR_ARG, f"tensor {k}: states of type {m[k].dtype} and {v[k].dtype}")
             blocks = -(-n // HASHGRID_ADAMW_BLOCK)
             for t in (ms[k], vs[k]):
