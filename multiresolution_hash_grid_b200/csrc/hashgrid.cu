@@ -857,7 +857,7 @@ int wide_tile(int64_t N, int most) { return tile_width(N, ceil_div(N, most)); }
 // number of column tiles is the one that costs least in rounds of the device times a tile's width (and
 // 24 columns' worth of what a tile costs anyway), down to 64 columns; if the tiles are still fewer than the SMs, K is
 // split over up to 8 blocks of a cluster, each with two 64-wide steps at least.
-Plan make_plan(int64_t M, int64_t N, int64_t K, int sms) {
+Plan make_plan(int64_t M, int64_t N, int64_t K, bool f32, int sms) {
     const int64_t mt = ceil_div(M, hg::linear::kBm);
     const int64_t pairs = ceil_div(N, 256);
     if (N >= 160 && (int64_t)ceil_div(M, 256) * pairs >= sms / 2 && K >= 512)
@@ -874,6 +874,27 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int sms) {
     }
     const int64_t tiles = mt * ceil_div(N, p.bn);
     while (p.cluster < 8 && tiles * p.cluster * 2 <= 2 * sms && 4 * p.cluster * hg::linear::kBk <= K) p.cluster *= 2;
+    const int64_t steps = ceil_div(K, hg::linear::kBk), most = hg::linear::kSegment16;
+    if (f32 || steps <= most * p.cluster) return p;
+    // A 16-bit result of a sum that would have to be gathered, by one block an SM: it is split into shares that need not be
+    // (65536 x 2048 by 2048: 574 us, gathered 616), or, beyond eight of those, into tiles and shares that leave the last round
+    // of one block an SM full. Of clusters of 4 and 8 such blocks 132 and 120 fit (2^19 x 1280 by 1024: 1.9 ms, 4.3 as above).
+    for (int c = 2 * p.cluster; c <= 8; c *= 2)
+        if (steps <= most * c) {
+            p.cluster = c;
+            return p;
+        }
+    best = INT64_MAX;
+    for (int64_t nt = ceil_div(N, 128); nt <= ceil_div(N, 64); ++nt)
+        for (int c = 1; c <= 8; c *= 2) {
+            const int bn = tile_width(N, nt), fit = c == 8 ? sms * 13 / 16 : c == 4 ? sms * 29 / 32 : sms;
+            const int64_t cost = (mt * ceil_div(N, bn) * c + fit - 1) / fit * (128 + bn) * (8 / c);
+            if (cost < best) {
+                best = cost;
+                p.bn = bn;
+                p.cluster = c;
+            }
+        }
     return p;
 }
 
@@ -1177,7 +1198,7 @@ int launch_linear_forward(const hashgrid_linear_s* l, const void* x, int64_t ldx
     add_copies(copies, both, 2, work);
     hg::linear::Slope none = {};
     if (int rc = launch_prepare<T>(none, false, copies, what, s)) return rc;
-    return launch_gemm<T>(A, B, N, l->out, l->in, e, make_plan(N, l->out, l->in, device_sms()), status, what, s);
+    return launch_gemm<T>(A, B, N, l->out, l->in, e, make_plan(N, l->out, l->in, e.out_f32 != 0, device_sms()), status, what, s);
 }
 
 template <typename T>
@@ -1243,7 +1264,7 @@ int launch_linear_backward(const hashgrid_linear_s* l, const void* dy, int64_t l
     // launch. dW is cut into parts of the rows that the sums kernel adds where its tiles are few.
     constexpr bool half = std::is_same<T, __half>::value;
     const int sms = device_sms();
-    Plan px = make_plan(N, l->in, l->out, sms), pw = make_plan(l->out, l->in, N, sms);
+    Plan px = make_plan(N, l->in, l->out, dx_dtype == HASHGRID_F32, sms), pw = make_plan(l->out, l->in, N, dw_dtype == HASHGRID_F32, sms);
     if (lw.splits > 1) pw = Plan{wide_tile(l->in, 128), 1, lw.splits, false};
     // Up to 16 steps of K one block takes for itself: sharing a launch saves more than splitting K does.
     const bool short_x = ceil_div(l->out, hl::kBk) <= 16, short_w = ceil_div(N, hl::kBk) <= 16 || lw.splits > 1;

@@ -356,8 +356,8 @@ __device__ __forceinline__ void emit_column8(const Epilogue& e, void* out, int64
 // Long sums (kGather): the tensor cores' additions cut off instead of rounding, which for random operands
 // loses 1.1e-9 of the result for each k (measured: 9.1e-6 for K = 8192, where plain fp32 has 9.6e-7, and 5.3e-4 for
 // K = 2^19). So every kSegment steps the accumulator is added to fp32 registers and begins again, where the
-// result is fp32, or where a 16-bit one sums more than kSegment16 steps: what those lose, 1.8e-5, is a
-// twenty-seventh of fp16's half step, and gathering takes one block an SM instead of two.
+// result is fp32, or where a 16-bit one sums more than kSegment16 steps: what those lose, 5e-5, is a
+// tenth of fp16's half step, and gathering takes one block an SM instead of two.
 //
 // Way out: a lane reads 32 columns of its row from TMEM, adds bias, applies the activation and adds
 // the residual in fp32, and rounds. Where rows begin on 16-byte boundaries (kVectors) the chunk of 32 x 32
@@ -370,7 +370,7 @@ constexpr int kBm = 128, kBk = 64;
 constexpr int kOutWarps = 8;
 constexpr int kThreads = 32 * (kOutWarps + 2);
 constexpr int kMaxStages = 16;
-constexpr int kSegment16 = 256;
+constexpr int kSegment16 = 768;
 constexpr int kSegment = 12;  // 64-wide steps of K (16 took it to the 1e-6 of plain fp32 sums, 12 leaves a quarter of room)
 constexpr int kStaging = kOutWarps * 32 * 32 * 4;
 
