@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import multiresolution_hash_grid_b200 as hg
-from tests.test_linear import ACTS, check_backward
+from tests.test_linear import ACTS, check_backward, check_forward
 
 pytestmark = pytest.mark.gpu
 
@@ -29,6 +29,13 @@ def test_long_sums_with_16_bit_results(N, K, M, dtype):
     d = dw.double() - ref
     bias = float((d * ref.sign()).sum() / ref.abs().sum())
     assert abs(bias) < 5.41e-5 + {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}[dtype] * 4 / (K * M) ** 0.5, bias
+
+
+@pytest.mark.parametrize("N,K,M", [(9600, 65536, 512), (1280, 65536, 1024)])
+def test_widest_layers_with_16_bit_results(N, K, M):
+    """The longest sums of the forward pass: gathered by pairs of blocks, and split into shares."""
+    check_forward(N, K, M, hg.HASHGRID_BF16, hg.HASHGRID_ACT_SILU)
+    check_forward(N, K, M, hg.HASHGRID_F16, hg.HASHGRID_ACT_NONE, residual=False, keep=False)
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
