@@ -9,7 +9,7 @@
 // square root there, since 8 bits of v itself would span half the orders of magnitude.
 //
 // A pass over memory: 28 bytes an element with fp32 parameter, gradient and states, 16 with
-// 8-bit states, against 28 (fp32 states) to 85 (8-bit states, stochastic rounding) instructions.
+// 8-bit states, against 36 (fp32 states) to 93 (8-bit states, stochastic rounding) instructions.
 //
 // A warp takes one block of 256 elements, lane j elements 4j..4j+3 and 128+4j..: every array,
 // whatever its type, is read and written in whole coalesced vectors (16, 8 or 4 bytes a lane),
