@@ -792,8 +792,8 @@ hg::linear::Patience patience() {
 }
 
 // A device's status word for layer calls that are given none: pinned memory, which the kernels write and the host reads
-// at the next call. NULL where there is none to be had.
-volatile int* given_up_word() {
+// at the next call. NULL where there is none to be had, or none yet and `make` is not set.
+volatile int* given_up_word(bool make) {
     constexpr int kDevices = 64, kApart = 32;
     static std::mutex lock;
     static std::atomic<int*> words{nullptr};
@@ -803,7 +803,7 @@ volatile int* given_up_word() {
         return nullptr;
     }
     int* p = words.load(std::memory_order_acquire);
-    if (p == nullptr) {
+    if (p == nullptr && make) {
         std::lock_guard<std::mutex> hold(lock);
         p = words.load(std::memory_order_relaxed);
         if (p == nullptr) {
@@ -822,19 +822,19 @@ volatile int* given_up_word() {
             words.store(p, std::memory_order_release);
         }
     }
-    return p + dev * kApart;
+    return p == nullptr ? nullptr : p + dev * kApart;
 }
 
 // Reports, once, that an earlier layer call without a status word gave up.
 int check_given_up() {
-    volatile int* word = given_up_word();
+    volatile int* word = given_up_word(false);
     if (word == nullptr || *word == 0) return ok();
     *word = 0;
     return fail(HASHGRID_ERR_TIMEOUT, "an earlier layer call on this device gave up a wait: its outputs are incomplete");
 }
 
 // The status word of a layer call.
-int* status_word(int* device_status) { return device_status != nullptr ? device_status : const_cast<int*>(given_up_word()); }
+int* status_word(int* device_status) { return device_status != nullptr ? device_status : const_cast<int*>(given_up_word(true)); }
 
 // How a product is cut.
 struct Plan {

@@ -270,3 +270,50 @@ print("ok")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, env=dict(os.environ, HASHGRID_CHECKED="0"), capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "ok" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.mark.gpu
+def test_asking_for_the_status_first_makes_no_context():
+    """A process that has called no layer has nothing to report, and asking leaves the device alone."""
+    import subprocess
+    import sys
+    code = r"""
+import ctypes, multiresolution_hash_grid_b200 as hg
+cu = ctypes.CDLL("libcuda.so.1")
+hg.hashgrid_linear_status()
+flags, active = ctypes.c_uint(), ctypes.c_int(7)
+assert cu.cuInit(0) == 0 and cu.cuDevicePrimaryCtxGetState(0, ctypes.byref(flags), ctypes.byref(active)) == 0
+assert active.value == 0, active.value
+print("ok")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, env=dict(os.environ, HASHGRID_CHECKED="0"), capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "ok" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.mark.gpu
+def test_calls_from_several_threads():
+    """Handles, the wait limit's and the status words' state and the launch attributes are shared between threads."""
+    import threading
+
+    import torch
+
+    import multiresolution_hash_grid_b200 as hg
+    if hg.CHECKED:
+        pytest.skip("the checked build is for one stream at a time")
+    jobs = [calls(hg, torch, shape, y32) for shape in SHAPES for y32 in (False, True)]
+    want = [run() for run in jobs]
+    failed = []
+
+    def work(k):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(5):
+                got, status = jobs[k]()
+                if status != [0, 0] or not all(torch.equal(a, b) for a, b in zip(got, want[k][0])):
+                    failed.append(SHAPES[k // 2])
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert failed == []
