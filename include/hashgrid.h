@@ -448,8 +448,10 @@ size_t hashgrid_linear_backward_workspace(hashgrid_linear_t layer, int64_t N, in
  *   dz[n][o] = dL_dy[n][o] act'(z[n][o]);   dL_dx[n][i] = sum_o dz[n][o] w[o][i];
  *   dL_dw[o][i] = sum_n dz[n][o] x[n][i];   dL_db[o] = sum_n dz[n][o].
  *
- * dz is rounded to the layer's dtype before it enters the two products (without an activation,
- * or with RELU, that changes nothing); sums are fp32, and dL_db sums the unrounded dz. All sums
+ * dz enters the two products as the sum of two numbers of the layer's dtype, off by 2^-16 of itself
+ * (bf16) or 2^-22 (fp16; at least 2^-25); without an activation, or with RELU, it is exact. A
+ * 16-bit dL_dx or dL_dw of a wide layer (512 outputs or rows to sum over, 74 tiles of 256 x 256 or
+ * more) takes dz rounded to the layer's dtype. Sums are fp32, and dL_db sums dz as it is. All sums
  * run in a fixed order: equal calls on one kind of device give equal bits.
  *
  * dL_dy: [N, out] of the layer's dtype, rows lddy apart; x, ldx, w: as in the forward call; z:

@@ -487,8 +487,7 @@ class Linear:
                  stream=None):
         """Returns (dL_dx, dL_dw, dL_db). Each is a tensor to write (dL_dx and dL_dw of the layer's type or fp32, dL_db
         fp32), True to allocate it (the layer's type, fp32, fp32), or None to leave it out. ``z``: what ``forward``
-        wrote (not needed without an activation). With GELU or SILU dL_dx and dL_dw come from dz rounded to the layer's type,
-        as fp32 tensors too."""
+        wrote (not needed without an activation)."""
         N, own, either = dL_dy.shape[0], self._own, self._either
         lddy = _rows(dL_dy, None, self.out_features, own, "dL_dy")
         ldx = _rows(x, N, self.in_features, own, "x")

@@ -955,12 +955,15 @@ struct Product {
     bool vectors, gather;
 };
 
-int set_product(Product& p, bool half, const Array& A, const Array& B, int64_t M, int64_t N, int64_t K, const hg::linear::Epilogue& e,
+// low: A's low part, or NULL.
+int set_product(Product& p, bool half, const Array& A, const Array* low, const Array& B, int64_t M, int64_t N, int64_t K, const hg::linear::Epilogue& e,
                 const Plan& plan, int* status, const char* what) {
     namespace hl = hg::linear;
     const int bn = plan.bn, splits = std::max(plan.splits, plan.cluster), group = plan.pair ? 2 : 1;
     hl::Gemm& g = p.g;
     if (int rc = set_side(g.a, g.ta, A, hl::kBm, what)) return rc;
+    if (low != nullptr)
+        if (int rc = set_map(g.ta_low, *low, g.a.box_rows, what)) return rc;
     if (int rc = set_side(g.b, g.tb, B, bn / group, what)) return rc;
     g.M = M;
     g.N = N;
@@ -968,7 +971,8 @@ int set_product(Product& p, bool half, const Array& A, const Array& B, int64_t M
     g.columns = ceil_div(bn, 32) * 32;
     g.tmem_columns = 64;
     while ((int)g.tmem_columns < 2 * g.columns) g.tmem_columns *= 2;
-    g.kblocks = ceil_div(K, hl::kBk);
+    g.kfold = ceil_div(K, hl::kBk);
+    g.kblocks = low != nullptr ? 2 * g.kfold : g.kfold;
     g.kblocks_per_split = ceil_div(g.kblocks, splits);
     g.mt = ceil_div(M, hl::kBm * group);
     g.nt = ceil_div(N, bn);
@@ -977,8 +981,8 @@ int set_product(Product& p, bool half, const Array& A, const Array& B, int64_t M
     if (tiles > (1 << 30)) return fail(HASHGRID_ERR_ARG, "%s: too many tiles", what);
     // B stays in shared memory where one column tile covers it, it is small and its block has several tiles to compute.
     const bool two = e.out_f32 && e.z != nullptr;  // staging areas
-    g.resident = splits == 1 && group == 1 && g.nt == 1 && g.kblocks * g.b.bytes <= (two ? 8 : 32) * 1024 && g.mt > 2 * sms;
-    const int kept = g.resident ? g.kblocks * g.b.bytes : 0;
+    g.resident = splits == 1 && group == 1 && g.nt == 1 && g.kfold * g.b.bytes <= (two ? 8 : 32) * 1024 && g.mt > 2 * sms;
+    const int kept = g.resident ? g.kfold * g.b.bytes : 0;
     g.stage_bytes = g.a.bytes + (g.resident ? 0 : g.b.bytes);
     g.cluster = plan.cluster;
     // Two blocks a SM where tensor memory and shared memory allow: one's loads and stores then fill the other's gaps. The MMA
@@ -1036,7 +1040,7 @@ template <typename T>
 int launch_gemm(const Array& A, const Array& B, int64_t M, int64_t N, int64_t K, const hg::linear::Epilogue& e, const Plan& plan,
                 int* status, const char* what, cudaStream_t s) {
     Product p;
-    if (int rc = set_product(p, std::is_same<T, __half>::value, A, B, M, N, K, e, plan, status, what)) return rc;
+    if (int rc = set_product(p, std::is_same<T, __half>::value, A, nullptr, B, M, N, K, e, plan, status, what)) return rc;
     return launch_products<T>(&p, 1, plan, what, s);
 }
 
@@ -1082,10 +1086,16 @@ int launch_prepare(const hg::linear::Slope& slope, bool vectors, const hg::linea
     return launch_after(k, dim3((unsigned)blocks), 256, 0, 1, s, what, slope, copies, (int)slope_blocks);
 }
 
+// Numbers of the layer's type that dz is held in: behind a smooth activation one would lose as much as a 16-bit result's own
+// rounding, and all that an fp32 one has more (4099 x 173 -> 257, SiLU, fp16: off by 2.9e-4 instead of 2.1e-4, in 19 us
+// instead of 22; 2^20 x 64 -> 64, GELU: an fp32 dW off by 1.7e-3 instead of below 4e-5, in 113 us instead of 131).
+int dz_pieces(const hashgrid_linear_s* l) { return l->act == HASHGRID_ACT_GELU || l->act == HASHGRID_ACT_SILU ? 2 : 1; }
+
 // The backward pass's workspace: the copies of x and w with aligned rows, dz (where dy is not it), the parts of
 // db, the parts of dw.
 struct LinearWork {
     int64_t lddz;   // elements
+    size_t low;     // offset of dz's low part
     int shares;     // row shares of the db sums
     int splits;     // row shares of dw
     size_t dz, sums, dw, bytes;  // offsets, total
@@ -1111,7 +1121,8 @@ LinearWork linear_work(const hashgrid_linear_s* l, int64_t N, int64_t lddy, int6
     const int64_t tiles = (int64_t)ceil_div(l->out, hg::linear::kBm) * ceil_div(l->in, 128);
     w.splits = N <= 512 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(kWorkSms / tiles, N / (4 * hg::linear::kBk)));
     w.dz = (l->in % 8 != 0 ? realigned_bytes(l->out, l->in) : 0) + (ldx % 8 != 0 ? realigned_bytes(N, l->in) : 0);
-    w.sums = w.dz + (l->act == HASHGRID_ACT_NONE && lddy % 8 == 0 ? 0 : align256((size_t)N * w.lddz * 2));
+    w.low = w.dz + align256((size_t)N * w.lddz * 2);
+    w.sums = w.dz + (l->act == HASHGRID_ACT_NONE && lddy % 8 == 0 ? 0 : dz_pieces(l) * align256((size_t)N * w.lddz * 2));
     w.dw = w.sums + align256((size_t)w.shares * l->out * sizeof(float));
     const size_t split = w.splits > 1 ? (size_t)w.splits * l->in * l->out : 0;
     const size_t narrow = narrow_layer(l, N) ? (size_t)kWorkSms * (l->in + 1) * l->out : 0;
@@ -1136,7 +1147,7 @@ int launch_sums(const hg::linear::Sums* list, int count, const char* what, cudaS
 }
 
 template <typename T>
-int launch_narrow_backward(const hashgrid_linear_s* l, int act, const Array& dy, const Array& x, int64_t N, const Array& w, const void* z, void* dx,
+int launch_narrow_backward(const hashgrid_linear_s* l, int act, int pieces, const Array& dy, const Array& x, int64_t N, const Array& w, const Array& z, void* dx,
                            int64_t lddx, int dx_dtype, bool want_db, float* parts, int* blocks_out, int* status, const char* what,
                            cudaStream_t s) {
     namespace hl = hg::linear;
@@ -1154,10 +1165,12 @@ int launch_narrow_backward(const hashgrid_linear_s* l, int act, const Array& dy,
     g.k_out = ceil_div(l->out, 16) * 16;
     if (int rc = set_map(g.tdy, dy, hl::kBm, what)) return rc;
     if (int rc = set_map(g.tx, x, hl::kBm, what)) return rc;
-    if (z != nullptr)
-        if (int rc = set_map(g.tz, {z, N, l->out, l->out, false, hg::kChkZ}, hl::kBm, what)) return rc;
+    const bool second = act != HASHGRID_ACT_NONE || pieces == 2;
+    g.pieces = pieces;
+    if (second)
+        if (int rc = set_map(g.tz, z, hl::kBm, what)) return rc;
     if (int rc = set_map(g.tw, dx != nullptr ? w : dy, g.k_out, what)) return rc;
-    g.stage_bytes = (g.boxes_out * (act == HASHGRID_ACT_NONE ? 1 : 2) + g.boxes_in) * hl::kBox;
+    g.stage_bytes = (g.boxes_out * (second ? 2 : 1) + g.boxes_in) * hl::kBox;
     g.w_bytes = g.k_out * g.boxes_in * 128;
     g.stages = hl::kNarrowStages;
     while (g.stages > 2 && hl::narrow_smem(g.stages * g.stage_bytes, g.w_bytes) > 226 * 1024) --g.stages;
@@ -1214,6 +1227,8 @@ int launch_linear_backward(const hashgrid_linear_s* l, const void* dy, int64_t l
     // A narrow layer's kernel makes dz and db itself where TMA can read dy and z.
     const bool narrow = dw != nullptr && narrow_layer(l, N), inside = narrow && vectors;
     const bool convert = !inside && (!plain || !aligned_rows(dz)) && (dx != nullptr || dw != nullptr);
+    const int pieces = dz_pieces(l);
+    const Array low{work + lw.low, N, l->out, lw.lddz, false, hg::kChkWork};
     Array* list[2] = {};
     int n = 0;
     if (dx != nullptr) list[n++] = &W;
@@ -1239,6 +1254,7 @@ int launch_linear_backward(const hashgrid_linear_s* l, const void* dy, int64_t l
         slope.cols = l->out;
         slope.act = l->act;
         slope.dz = convert ? work + lw.dz : nullptr;
+        slope.low = convert && pieces == 2 ? work + lw.low : nullptr;
         slope.sums = db == nullptr ? nullptr : lw.shares > 1 ? reinterpret_cast<float*>(work + lw.sums) : db;
         slope.role = lw.shares > 1 ? hg::kChkWork : hg::kChkBias;
         slope.groups = 1;
@@ -1253,7 +1269,8 @@ int launch_linear_backward(const hashgrid_linear_s* l, const void* dy, int64_t l
     float* out = reinterpret_cast<float*>(work + lw.dw);
     if (narrow) {
         int blocks = 0;
-        if (int rc = launch_narrow_backward<T>(l, inside ? l->act : (int)HASHGRID_ACT_NONE, dz, X, N, W, inside && !plain ? z : nullptr, dx, lddx, dx_dtype,
+        const Array Z{z, N, l->out, l->out, false, hg::kChkZ};
+        if (int rc = launch_narrow_backward<T>(l, inside ? l->act : (int)HASHGRID_ACT_NONE, pieces, dz, X, N, W, inside ? Z : low, dx, lddx, dx_dtype,
                                                inside && db != nullptr, out, &blocks, status, what, s))
             return rc;
         sums[nsums++] = hl::Sums{out, nw + l->out, nw, blocks, dw_dtype == HASHGRID_F32 ? 0 : 1, dw, hg::kChkGrad};
@@ -1264,7 +1281,17 @@ int launch_linear_backward(const hashgrid_linear_s* l, const void* dy, int64_t l
     // launch. dW is cut into parts of the rows that the sums kernel adds where its tiles are few.
     constexpr bool half = std::is_same<T, __half>::value;
     const int sms = device_sms();
-    Plan px = make_plan(N, l->in, l->out, dx_dtype == HASHGRID_F32, sms), pw = make_plan(l->out, l->in, N, dw_dtype == HASHGRID_F32, sms);
+    // A product that the tensor cores bound (by pairs), with a 16-bit result, takes dz's high part alone: the result's own
+    // rounding is as large, and both parts take twice as long (8192 x 2048 -> 4096, GELU, fp32 dW: 441 us with both parts in both
+    // products, 345 with the high one alone in dx).
+    auto plan_of = [&](int64_t rows, int64_t cols, int64_t k, bool f32, bool& both) {
+        const Plan one = make_plan(rows, cols, k, f32, sms);
+        both = pieces == 2 && (f32 || !one.pair);
+        return both ? make_plan(rows, cols, 2 * k, f32, sms) : one;
+    };
+    bool both_x = false, both_w = false;
+    Plan px = plan_of(N, l->in, l->out, dx_dtype == HASHGRID_F32, both_x), pw = plan_of(l->out, l->in, N, dw_dtype == HASHGRID_F32, both_w);
+    both_w = both_w || (pieces == 2 && lw.splits > 1);
     if (lw.splits > 1) pw = Plan{wide_tile(l->in, 128), 1, lw.splits, false};
     // Up to 16 steps of K one block takes for itself: sharing a launch saves more than splitting K does.
     const bool short_x = ceil_div(l->out, hl::kBk) <= 16, short_w = ceil_div(N, hl::kBk) <= 16 || lw.splits > 1;
@@ -1275,12 +1302,12 @@ int launch_linear_backward(const hashgrid_linear_s* l, const void* dy, int64_t l
                           hl::kNoAct, parts ? hg::kChkWork : hg::kChkGrad};
     Product p[2];
     int np = 0;
-    Array dzt = dz;
-    dzt.mn = true;
+    Array dzt = dz, lowt = low;
+    dzt.mn = lowt.mn = true;
     if (dw != nullptr)
-        if (int rc = set_product(p[np++], half, dzt, X, l->out, l->in, N, ew, pw, status, what)) return rc;
+        if (int rc = set_product(p[np++], half, dzt, both_w ? &lowt : nullptr, X, l->out, l->in, N, ew, pw, status, what)) return rc;
     if (dx != nullptr)
-        if (int rc = set_product(p[np++], half, dz, W, N, l->in, l->out, ex, px, status, what)) return rc;
+        if (int rc = set_product(p[np++], half, dz, both_x ? &low : nullptr, W, N, l->in, l->out, ex, px, status, what)) return rc;
     if (np == 2 && px.pair == pw.pair && px.cluster == pw.cluster && p[0].gather == p[1].gather) {
         if (int rc = launch_products<T>(p, 2, px, what, s)) return rc;
     } else {

@@ -233,6 +233,37 @@ __device__ __forceinline__ uint4 pack8(const float* y) {
     return make_uint4(pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3]), pack2<T>(y[4], y[5]), pack2<T>(y[6], y[7]));
 }
 
+// The nearest finite numbers of type T (a NaN stays one).
+template <typename T> __device__ __forceinline__ uint32_t pack2_finite(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2_finite<__half>(float a, float b) {
+    uint32_t w;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+    return w;
+}
+template <> __device__ __forceinline__ uint32_t pack2_finite<__nv_bfloat16>(float a, float b) {
+    uint32_t w;
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+    return w;
+}
+// d as the sum of two numbers of type T, each the nearest to what is left: off by the square of a rounding of T. The high
+// one is finite, so that a d beyond T's range is not an infinity less an infinity; an infinite d is so in the low one.
+template <typename T>
+__device__ __forceinline__ uint32_t split2(float a, float b, uint32_t& low) {
+    const uint32_t high = pack2_finite<T>(a, b);
+    const float2 rest = fma2(unpack2<T>(high), both(-1.f), make_float2(a, b));
+    low = pack2<T>(rest.x, rest.y);
+    return high;
+}
+template <typename T>
+__device__ __forceinline__ uint4 split8(const float* d, uint4& low) {
+    uint4 high;
+    high.x = split2<T>(d[0], d[1], low.x);
+    high.y = split2<T>(d[2], d[3], low.y);
+    high.z = split2<T>(d[4], d[5], low.z);
+    high.w = split2<T>(d[6], d[7], low.w);
+    return high;
+}
+
 // kRows rows (row, row + 8, ...) of eight neighbouring values, bias already added, in 16-byte
 // vectors. Rows from `rows` on are not there. q: the 16-bit residuals, if there are any.
 template <typename T, int kRows>
@@ -391,7 +422,7 @@ struct Side {             // one operand's share of a stage: `boxes` boxes of bo
 };
 
 struct Gemm {
-    CUtensorMap ta, tb, ty, tz;
+    CUtensorMap ta, ta_low, tb, ty, tz;
     Side a, b;
     int64_t M, N;
     int bn, columns;      // tile width; columns from one accumulator to the next
@@ -399,6 +430,7 @@ struct Gemm {
     int resident;         // B is staged once, behind the stages
     int cluster;          // blocks that share a tile's K (their shares meet in shared memory), or 1
     int kblocks, kblocks_per_split;
+    int kfold;            // steps from here on multiply A's low part (ta_low) by B once more; kblocks where A has none
     int mt, nt;
     int blocks;           // blocks (or pairs) that take turns at the tiles of a split
     uint32_t idesc, tmem_columns;
@@ -620,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
     const int block = (int)blockIdx.x - (which ? list.second : 0);
     extern __shared__ uint8_t raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-    const int kept = g.resident ? g.kblocks * g.b.bytes : 0;
+    const int kept = g.resident ? g.kfold * g.b.bytes : 0;
     uint8_t* staging = sm + (size_t)g.stages * g.stage_bytes + kept;
     uint64_t* bars = reinterpret_cast<uint64_t*>(staging + (g.e.out_f32 && g.e.z != nullptr ? 2 : 1) * kStaging);  // fp32 y and z side by side
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 6);
@@ -675,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
         const uint32_t bytes = g.a.bytes + (g.resident ? 0 : g.b.bytes);
         if (g.resident && kbs > 0 && issues) {
             arrive_expect(bfull, kept);
-            for (int kb = 0; kb < g.kblocks; ++kb)
+            for (int kb = 0; kb < g.kfold; ++kb)
                 for (int j = 0; j < g.b.boxes; ++j)
                     tma_load(sb0 + kb * g.b.bytes + j * g.b.box_rows * 128, &g.tb, g.b.mn ? 64 * j : kb * kBk, g.b.mn ? kb * kBk : 0, bfull);
         }
@@ -690,13 +722,15 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
             for (int kb = 0; kb < kbs; ++kb) {
                 if (!(ok = warp_waits<kPair>(empty + 8 * r.stage, r.phase ^ 1u, waits))) break;
                 const uint32_t bar = full0 + 8 * r.stage, sa = sm0 + r.stage * g.stage_bytes, sb = sa + g.a.bytes;
-                const int k0 = (kb0 + kb) * kBk;
+                const bool low = kb0 + kb >= g.kfold;
+                const int k0 = (kb0 + kb - (low ? g.kfold : 0)) * kBk;
+                const CUtensorMap* ta = low ? &g.ta_low : &g.ta;
                 if (!kPair && issues) arrive_expect(bar, bytes);
                 if (kPair && rank == 0 && issues) arrive_expect(full + 8 * r.stage, 2 * bytes);  // both blocks' copies
                 for (int j = 0; j < a_boxes; ++j) {
                     const int x = a_mn ? m0 + 64 * j : k0, y = a_mn ? k0 : m0;
-                    if (kPair && issues) tma_load_pair(sa + j * a_step, &g.ta, x, y, bar);
-                    if (!kPair && issues) tma_load(sa + j * a_step, &g.ta, x, y, bar);
+                    if (kPair && issues) tma_load_pair(sa + j * a_step, ta, x, y, bar);
+                    if (!kPair && issues) tma_load(sa + j * a_step, ta, x, y, bar);
                 }
                 for (int j = 0; j < b_boxes; ++j) {
                     const int x = b_mn ? n0 + 64 * j : k0, y = b_mn ? k0 : n0;
@@ -743,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
                     }
                     if (!(ok = warp_waits<kPair>(full + 8 * r.stage, r.phase, waits))) break;
                     mlp::fence_after();
-                    const uint64_t da = a0 + (uint32_t)r.stage * stage, db = b0 + (g.resident ? (uint32_t)kb * next_b : (uint32_t)r.stage * stage);
+                    const uint64_t da = a0 + (uint32_t)r.stage * stage, db = b0 + (g.resident ? (uint32_t)(kb < g.kfold ? kb : kb - g.kfold) * next_b : (uint32_t)r.stage * stage);
 #pragma unroll
                     for (int k = 0; k < kBk / 16; ++k) {
                         if (kPair && issues) mma_pair(acc, da + k * step_a, db + k * step_b, g.idesc, (kseg | k) != 0 ? 1u : 0u);
@@ -1137,7 +1171,8 @@ __device__ __forceinline__ void realign_block(const RealignList& l, int64_t bloc
 //
 // Persistent blocks, one an SM, over tiles of 128 rows. TMA brings a tile of dy, z and x into a stage in
 // the 128-byte-swizzled layout. Eight warps turn dy into dz in place (and keep db's sums in
-// registers). That one copy of dz then serves both products: with rows of 64 outputs it is a k-major
+// registers); behind a smooth activation dz is two numbers, the low one in z's place, and each product
+// runs over both. That one copy of dz then serves both products: with rows of 64 outputs it is a k-major
 // A operand of dx = dz W and, read the other way, an mn-major A operand of dW = dz^T x, as the tile of x
 // is its mn-major B operand. W stays in shared memory. dx goes out as in the kernel above; dW
 // gathers in tensor memory over kFlush tiles, and is then added to fp32 registers (the tensor cores'
@@ -1156,6 +1191,7 @@ struct Narrow {
     int64_t rows;
     int in, out, act;
     int boxes_in, boxes_out, columns;  // 64-wide boxes of x and of dy (and z); columns from one accumulator to the next
+    int pieces;                        // dz's: 2 where its low part takes z's place (or comes as z, without an activation)
     int stages, stage_bytes, w_bytes, k_out;  // k_out: out, rounded up to 16
     uint32_t id_dx, id_dw, tmem_columns;
     Epilogue e;                        // of dx; out NULL: not wanted
@@ -1216,7 +1252,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
     const uint32_t tmem = *tslot;
     const int tiles = (int)((g.rows + kBm - 1) / kBm);
     const int mine = (tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1;  // at least one: the grid has no more blocks than tiles
-    const int dy_bytes = g.boxes_out * kBox, z_at = dy_bytes, x_at = g.act == kNoAct ? dy_bytes : 2 * dy_bytes;
+    const bool second = g.act != kNoAct || g.pieces == 2;  // z, or dz's low part
+    const int dy_bytes = g.boxes_out * kBox, z_at = dy_bytes, x_at = second ? 2 * dy_bytes : dy_bytes;
 
     if (warp == 9) {
         // ------------------------------- TMA copies -------------------------------
@@ -1236,7 +1273,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
             if (issues) {
                 arrive_expect(bar, g.stage_bytes);
                 for (int j = 0; j < g.boxes_out; ++j) tma_load(s + j * kBox, &g.tdy, 64 * j, m0, bar);
-                if (g.act != kNoAct)
+                if (second)
                     for (int j = 0; j < g.boxes_out; ++j) tma_load(s + z_at + j * kBox, &g.tz, 64 * j, m0, bar);
                 for (int j = 0; j < g.boxes_in; ++j) tma_load(s + x_at + j * kBox, &g.tx, 64 * j, m0, bar);
             }
@@ -1265,15 +1302,19 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
             mlp::fence_after();
             const uint32_t off = (uint32_t)r.stage * stage;
             if (dx) {
-                for (int k = 0; k < g.k_out / 16; ++k) {
-                    const uint32_t ak = (k >> 2) * (kBox >> 4) + (k & 3) * 2, bk = k * 128;
-                    if (issues) mlp::mma(tmem + b * g.columns, dz_k + off + ak, w_mn + bk, g.id_dx, k != 0 ? 1u : 0u);
-                }
+                for (int p = 0; p < g.pieces; ++p)
+                    for (int k = 0; k < g.k_out / 16; ++k) {
+                        const uint32_t ak = p * (z_at >> 4) + (k >> 2) * (kBox >> 4) + (k & 3) * 2, bk = k * 128;
+                        if (issues) mlp::mma(tmem + b * g.columns, dz_k + off + ak, w_mn + bk, g.id_dx, (p | k) != 0 ? 1u : 0u);
+                    }
                 if (issues) mlp::commit(done + 8 * b);
             }
+            for (int p = 0; p < g.pieces; ++p)
 #pragma unroll
-            for (int k = 0; k < kBm / 16; ++k)
-                if (issues) mlp::mma(dw0 + f * g.columns, dz_mn + off + k * 128, x_mn + off + k * 128, g.id_dw, (i % kFlush != 0 || k != 0) ? 1u : 0u);
+                for (int k = 0; k < kBm / 16; ++k)
+                    if (issues)
+                        mlp::mma(dw0 + f * g.columns, dz_mn + off + p * (z_at >> 4) + k * 128, x_mn + off + k * 128, g.id_dw,
+                                 (i % kFlush != 0 || (p | k) != 0) ? 1u : 0u);
             if (issues) mlp::commit(empty + 8 * r.stage);
             if (issues && (i % kFlush == kFlush - 1 || i == mine - 1)) mlp::commit(wdone + 8 * f);
             r.next(g.stages);
@@ -1373,11 +1414,13 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
                     const float2 d0 = unpack2<T>(q.x), d1 = unpack2<T>(q.y), d2 = unpack2<T>(q.z), d3 = unpack2<T>(q.w);
                     d[0] = d0.x; d[1] = d0.y; d[2] = d1.x; d[3] = d1.y; d[4] = d2.x; d[5] = d2.y; d[6] = d3.x; d[7] = d3.y;
                     if (g.act != kNoAct) {
-                        const uint4 zq = *reinterpret_cast<const uint4*>(reinterpret_cast<uint8_t*>(at) + z_at);
+                        uint4* zat = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(at) + z_at);
+                        const uint4 zq = *zat;
                         const float2 z0 = unpack2<T>(zq.x), z1 = unpack2<T>(zq.y), z2 = unpack2<T>(zq.z), z3 = unpack2<T>(zq.w);
                         const float z[8] = {z0.x, z0.y, z1.x, z1.y, z2.x, z2.y, z3.x, z3.y};
                         times_slope(d, z, g.act);
-                        *at = pack8<T>(d);
+                        if (g.pieces == 2) *at = split8<T>(d, *zat);
+                        else *at = pack8<T>(d);
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) sum[j] += d[j];
@@ -1444,14 +1487,15 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(g.tmem_columns) : "memory");
 }
 
-// dz = dy act'(z), rounded to T, into dz (NULL: not wanted), and the sums of the unrounded dz over a
-// block's share of the rows into sums[share][col] (NULL: not wanted). A block takes up to 64 columns,
+// dz = dy act'(z), rounded to T, into dz (NULL: not wanted), what the rounding left into low (NULL: nothing, or not
+// wanted), and the sums of the unrounded dz over a block's share of the rows into sums[share][col] (NULL: not wanted). A block takes up to 64 columns,
 // a thread eight neighbouring ones of every (256 / groups)-th row.
 struct Slope {
     Realign dy, z;     // as sources
     int64_t rows, lddz;
     int cols, act;
     void* dz;
+    void* low;
     float* sums;
     int role;          // CheckRole of sums
     int groups;        // column groups of eight in a block: 1, 2, 4 or 8
@@ -1465,6 +1509,7 @@ __device__ __forceinline__ void slope_block(const Slope& a, int block) {
     const T* dy = static_cast<const T*>(a.dy.p);
     const T* z = static_cast<const T*>(a.z.p);
     T* dz = static_cast<T*>(a.dz);
+    T* low = static_cast<T*>(a.low);
     const int col_block = block % a.col_blocks, which = block / a.col_blocks, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = col_block * 64 + 8 * (threadIdx.x % a.groups), r = threadIdx.x / a.groups, step = 256 / a.groups;
     const int64_t share = (a.rows + a.shares - 1) / a.shares, r0 = which * share, r1 = min(a.rows, r0 + share);
@@ -1479,7 +1524,11 @@ __device__ __forceinline__ void slope_block(const Slope& a, int block) {
             times_slope(d, v, a.act);
         }
         // rows of dz are multiples of 8 wide: what lies between `cols` and that is zero
-        if (dz != nullptr && in_bounds<kChkWork>(dz + row * a.lddz + col, 16)) *reinterpret_cast<uint4*>(dz + row * a.lddz + col) = pack8<T>(d);
+        if (dz != nullptr && in_bounds<kChkWork>(dz + row * a.lddz + col, 16)) {
+            uint4 rest;
+            *reinterpret_cast<uint4*>(dz + row * a.lddz + col) = low != nullptr ? split8<T>(d, rest) : pack8<T>(d);
+            if (low != nullptr && in_bounds<kChkWork>(low + row * a.lddz + col, 16)) *reinterpret_cast<uint4*>(low + row * a.lddz + col) = rest;
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) s[j] += d[j];
     };
@@ -1564,7 +1613,7 @@ __device__ __forceinline__ void slope_block(const Slope& a, int block) {
 // What comes before the products, in one launch: dz and db's sums (the first blocks), and the copies of
 // arrays that TMA cannot read as they are.
 template <typename T, bool kVectors>
-__global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ Slope slope, const __grid_constant__ RealignList copies, int slope_blocks) {
+__global__ void __launch_bounds__(256, kVectors ? 1 : 2) prepare_kernel(const __grid_constant__ Slope slope, const __grid_constant__ RealignList copies, int slope_blocks) {
     after_previous_kernel();
     if ((int)blockIdx.x < slope_blocks) slope_block<T, kVectors>(slope, blockIdx.x);
     else realign_block(copies, blockIdx.x - slope_blocks);

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import multiresolution_hash_grid_b200 as hg
-from tests.test_linear import ACTS, check_backward, check_forward
+from tests.test_linear import ACTS, U, check_backward, check_forward, close, half_step, rows_of, slope64
 
 pytestmark = pytest.mark.gpu
 
@@ -59,6 +59,49 @@ def test_relu_passes_a_nan_on(N, K, M, dtype):
     assert bool(torch.isnan(dx[3]).all()) and int(torch.isnan(dx).sum()) == K
     assert bool(torch.isnan(dw).all()) and bool(torch.isnan(db).all())
     assert not bool(torch.isnan(layer.forward(x, torch.zeros_like(w), torch.full((M,), -1.0, device="cuda"))[:3]).any())
+
+
+@pytest.mark.parametrize("act", [hg.HASHGRID_ACT_GELU, hg.HASHGRID_ACT_SILU])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("N,K,M,pad", [(1, 64, 64, 0), (16, 2048, 1024, 0), (200, 48, 72, 8), (4099, 173, 257, 3), (33, 9, 7, 1), (90001, 64, 64, 0),
+                                       (90001, 64, 24, 8), (90001, 27, 31, 3), (20000, 128, 128, 0), (40000, 200, 40, 0), (9700, 1000, 300, 0),
+                                       (19100, 160, 512, 0), (30000, 16, 816, 8), (50000, 64, 4, 0)])
+def test_fp32_gradients_behind_smooth_activations(N, K, M, pad, dtype, act):
+    """dz enters the products as two numbers of the layer's type: off by the square of its half step, 2^-16 for bf16 and 2^-22
+    for fp16 (at least half of fp16's smallest number, 2^-25), not by the half step. The slope is off by 32 * 2^-24 (1 + |z|),
+    and the sums run over twice as many terms, the low half of them 2^-8 as large."""
+    gen = torch.Generator(device="cuda").manual_seed(N + M)
+    x, dy = rows_of(N, K, pad, dtype, gen), rows_of(N, M, pad, dtype, gen)
+    w = (torch.randn(M, K, device="cuda", generator=gen) / M ** 0.5).to(dtype)
+    z = torch.randn(N, M, device="cuda", generator=gen).to(dtype)
+    layer = hg.Linear(K, M, hg.HASHGRID_F16 if dtype == torch.float16 else hg.HASHGRID_BF16, act)
+    dx, dw, db = layer.backward(dy, x, w, z=z, dL_dx=torch.empty(N, K, device="cuda"))
+    X, W, DY, Z = x.double(), w.double(), dy.double(), z.double()
+    dz = DY * slope64(Z, act)
+    slope = 32 * U * (1 + Z.abs()) * DY.abs()
+    err = slope + dz.abs() * half_step(dtype)[0] ** 2 * 1.01 + half_step(dtype)[1]
+    for got, ref, mag, carried, terms, name in ((dx, dz @ W, dz.abs() @ W.abs(), err @ W.abs(), M, "dx"),
+                                                (dw, dz.t() @ X, dz.abs().t() @ X.abs(), err.t() @ X.abs(), N, "dw"),
+                                                (db, dz.sum(0), dz.abs().sum(0), slope.sum(0), N, "db")):
+        close(got, ref, 2 * U * (2 * terms + 4) * mag + carried + 2 * U * ref.abs(), name)
+        assert float((got.double() - ref).norm() / ref.norm()) < 2.0 ** -16 + 2e-5, name
+
+
+@pytest.mark.parametrize("N", [40, 9000])
+def test_gradients_beyond_the_range_of_fp16(N):
+    """A slope above 1 takes dz beyond fp16's largest number: its two parts still hold it, and infinities and NaN stay."""
+    z = torch.full((N, 16), 1.5, device="cuda").half()
+    dy = torch.full((N, 16), 60000.0, device="cuda").half()
+    dy[1, 0], dy[2, 1], dy[3, 2] = float("inf"), float("-inf"), float("nan")
+    w = (torch.eye(16, device="cuda") / 64).half()
+    x = torch.full((N, 16), 2.0 ** -10, device="cuda").half()
+    dx, dw, db = hg.Linear(16, 16, hg.HASHGRID_F16, hg.HASHGRID_ACT_GELU).backward(dy, x, w, z=z, dL_dx=torch.empty(N, 16, device="cuda"))
+    want = float(60000 * slope64(torch.tensor(1.5, dtype=torch.float64), hg.HASHGRID_ACT_GELU))
+    assert want > 65504 and float((dx[4:] * 64 - want).abs().max()) < want * (2.0 ** -22 + 64 * U)
+    assert float((dw[3:] * 1024 - want * N).abs().max()) < want * N * (2.0 ** -22 + 2 * U * (2 * N + 4) + 64 * U)
+    assert float(dw[0, 0]) == float("inf") and float(dw[1, 0]) == float("-inf") and bool(torch.isnan(dw[2]).all())
+    assert bool(torch.isnan(dx[3]).all()) and not bool(torch.isfinite(dx[1:3, :2].diagonal()).any())
+    assert float(db[0]) == float("inf") and float(db[1]) == float("-inf") and bool(torch.isnan(db[2]))
 
 
 @pytest.mark.parametrize("tiles", [6, 7, 12, 13, 18, 25])
