@@ -1082,7 +1082,8 @@ int launch_prepare(const hg::linear::Slope& slope, bool vectors, const hg::linea
     const int64_t slope_blocks = slope.rows == 0 ? 0 : (int64_t)slope.col_blocks * slope.shares, blocks = slope_blocks + (copies.total + 1023) / 1024;
     if (blocks == 0) return ok();
     if (blocks > 0x7fffffffLL) return fail(HASHGRID_ERR_ARG, "%s: too many rows to realign", what);
-    auto k = vectors ? hg::linear::prepare_kernel<T, true> : hg::linear::prepare_kernel<T, false>;
+    auto k = slope.low != nullptr ? (vectors ? hg::linear::prepare_kernel<T, true, true> : hg::linear::prepare_kernel<T, false, true>)
+                                  : (vectors ? hg::linear::prepare_kernel<T, true, false> : hg::linear::prepare_kernel<T, false, false>);
     return launch_after(k, dim3((unsigned)blocks), 256, 0, 1, s, what, slope, copies, (int)slope_blocks);
 }
 

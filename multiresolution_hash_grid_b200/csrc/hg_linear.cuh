@@ -12,6 +12,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "hg_check.cuh"
 #include "hg_mlp.cuh"
 
@@ -719,26 +721,28 @@ __global__ void __launch_bounds__(kThreads, kPair || kGather ? 1 : 2) gemm_kerne
         const uint32_t full0 = kPair ? cluster_address(full, 0) : full;
         for (Tiles t(g, first, step); t.more() && ok; t.next()) {
             const int m0 = (kPair ? 2 * t.m + (int)rank : t.m) * kBm, n0 = t.n * g.bn + (kPair ? (int)rank * (g.bn / 2) : 0);
-            for (int kb = 0; kb < kbs; ++kb) {
-                if (!(ok = warp_waits<kPair>(empty + 8 * r.stage, r.phase ^ 1u, waits))) break;
-                const uint32_t bar = full0 + 8 * r.stage, sa = sm0 + r.stage * g.stage_bytes, sb = sa + g.a.bytes;
+            for (int end, kb = 0; kb < kbs && ok; kb = end) {  // A as it is, and then its low part
                 const bool low = kb0 + kb >= g.kfold;
-                const int k0 = (kb0 + kb - (low ? g.kfold : 0)) * kBk;
                 const CUtensorMap* ta = low ? &g.ta_low : &g.ta;
-                if (!kPair && issues) arrive_expect(bar, bytes);
-                if (kPair && rank == 0 && issues) arrive_expect(full + 8 * r.stage, 2 * bytes);  // both blocks' copies
-                for (int j = 0; j < a_boxes; ++j) {
-                    const int x = a_mn ? m0 + 64 * j : k0, y = a_mn ? k0 : m0;
-                    if (kPair && issues) tma_load_pair(sa + j * a_step, ta, x, y, bar);
-                    if (!kPair && issues) tma_load(sa + j * a_step, ta, x, y, bar);
+                end = low ? kbs : min(kbs, g.kfold - kb0);
+                for (int k0 = (kb0 + kb - (low ? g.kfold : 0)) * kBk; kb < end; ++kb, k0 += kBk) {
+                    if (!(ok = warp_waits<kPair>(empty + 8 * r.stage, r.phase ^ 1u, waits))) break;
+                    const uint32_t bar = full0 + 8 * r.stage, sa = sm0 + r.stage * g.stage_bytes, sb = sa + g.a.bytes;
+                    if (!kPair && issues) arrive_expect(bar, bytes);
+                    if (kPair && rank == 0 && issues) arrive_expect(full + 8 * r.stage, 2 * bytes);  // both blocks' copies
+                    for (int j = 0; j < a_boxes; ++j) {
+                        const int x = a_mn ? m0 + 64 * j : k0, y = a_mn ? k0 : m0;
+                        if (kPair && issues) tma_load_pair(sa + j * a_step, ta, x, y, bar);
+                        if (!kPair && issues) tma_load(sa + j * a_step, ta, x, y, bar);
+                    }
+                    for (int j = 0; j < b_boxes; ++j) {
+                        const int x = b_mn ? n0 + 64 * j : k0, y = b_mn ? k0 : n0;
+                        if (kPair && issues) tma_load_pair(sb + j * b_step, &g.tb, x, y, bar);
+                        if (!kPair && issues) tma_load(sb + j * b_step, &g.tb, x, y, bar);
+                    }
+                    r.next(g.stages);
+                    ++issued;
                 }
-                for (int j = 0; j < b_boxes; ++j) {
-                    const int x = b_mn ? n0 + 64 * j : k0, y = b_mn ? k0 : n0;
-                    if (kPair && issues) tma_load_pair(sb + j * b_step, &g.tb, x, y, bar);
-                    if (!kPair && issues) tma_load(sb + j * b_step, &g.tb, x, y, bar);
-                }
-                r.next(g.stages);
-                ++issued;
             }
         }
         if (lane == 0) copies_issued = issued;
@@ -1304,17 +1308,18 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
             if (dx) {
                 for (int p = 0; p < g.pieces; ++p)
                     for (int k = 0; k < g.k_out / 16; ++k) {
-                        const uint32_t ak = p * (z_at >> 4) + (k >> 2) * (kBox >> 4) + (k & 3) * 2, bk = k * 128;
+                        const uint32_t ak = (p != 0 ? z_at >> 4 : 0) + (k >> 2) * (kBox >> 4) + (k & 3) * 2, bk = k * 128;
                         if (issues) mlp::mma(tmem + b * g.columns, dz_k + off + ak, w_mn + bk, g.id_dx, (p | k) != 0 ? 1u : 0u);
                     }
                 if (issues) mlp::commit(done + 8 * b);
             }
-            for (int p = 0; p < g.pieces; ++p)
+            uint32_t acc = i % kFlush != 0 ? 1u : 0u;
+            for (int p = 0; p < g.pieces; ++p, acc = 1u) {
+                const uint32_t at = off + (p != 0 ? z_at >> 4 : 0);
 #pragma unroll
                 for (int k = 0; k < kBm / 16; ++k)
-                    if (issues)
-                        mlp::mma(dw0 + f * g.columns, dz_mn + off + p * (z_at >> 4) + k * 128, x_mn + off + k * 128, g.id_dw,
-                                 (i % kFlush != 0 || (p | k) != 0) ? 1u : 0u);
+                    if (issues) mlp::mma(dw0 + f * g.columns, dz_mn + at + k * 128, x_mn + off + k * 128, g.id_dw, k != 0 ? 1u : acc);
+            }
             if (issues) mlp::commit(empty + 8 * r.stage);
             if (issues && (i % kFlush == kFlush - 1 || i == mine - 1)) mlp::commit(wdone + 8 * f);
             r.next(g.stages);
@@ -1401,32 +1406,36 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_backward_kernel(cons
             if (lane == 0) mlp::mbar_arrive(wroom + 8 * f);
             return true;
         };
+        // dy becomes dz, of one number or two (kBoth)
+        auto slopes = [&](uint8_t* s, auto both) {
+            constexpr bool kBoth = decltype(both)::value;
+#pragma unroll 2
+            for (int row = row0; row < kBm; row += row_step) {
+                uint4* at = reinterpret_cast<uint4*>(s + row * 128 + ((cc ^ (row & 7)) << 4));
+                const uint4 q = *at;
+                float d[8];
+                const float2 d0 = unpack2<T>(q.x), d1 = unpack2<T>(q.y), d2 = unpack2<T>(q.z), d3 = unpack2<T>(q.w);
+                d[0] = d0.x; d[1] = d0.y; d[2] = d1.x; d[3] = d1.y; d[4] = d2.x; d[5] = d2.y; d[6] = d3.x; d[7] = d3.y;
+                if (kBoth || g.act != kNoAct) {
+                    uint4* zat = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(at) + z_at);
+                    const uint4 zq = *zat;
+                    const float2 z0 = unpack2<T>(zq.x), z1 = unpack2<T>(zq.y), z2 = unpack2<T>(zq.z), z3 = unpack2<T>(zq.w);
+                    const float z[8] = {z0.x, z0.y, z1.x, z1.y, z2.x, z2.y, z3.x, z3.y};
+                    times_slope(d, z, g.act);
+                    if constexpr (kBoth) *at = split8<T>(d, *zat);
+                    else *at = pack8<T>(d);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j] += d[j];
+            }
+            mlp::fence_async_smem();
+        };
         Ring r;
         for (int i = 0; i < mine && ok; ++i) {
             if (!(ok = warp_waits<false>(full + 8 * r.stage, r.phase, waits))) break;
             uint8_t* s = sm + r.stage * g.stage_bytes + box_at;
-            if (g.act != kNoAct || g.want_db) {
-#pragma unroll 2
-                for (int row = row0; row < kBm; row += row_step) {
-                    uint4* at = reinterpret_cast<uint4*>(s + row * 128 + ((cc ^ (row & 7)) << 4));
-                    const uint4 q = *at;
-                    float d[8];
-                    const float2 d0 = unpack2<T>(q.x), d1 = unpack2<T>(q.y), d2 = unpack2<T>(q.z), d3 = unpack2<T>(q.w);
-                    d[0] = d0.x; d[1] = d0.y; d[2] = d1.x; d[3] = d1.y; d[4] = d2.x; d[5] = d2.y; d[6] = d3.x; d[7] = d3.y;
-                    if (g.act != kNoAct) {
-                        uint4* zat = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(at) + z_at);
-                        const uint4 zq = *zat;
-                        const float2 z0 = unpack2<T>(zq.x), z1 = unpack2<T>(zq.y), z2 = unpack2<T>(zq.z), z3 = unpack2<T>(zq.w);
-                        const float z[8] = {z0.x, z0.y, z1.x, z1.y, z2.x, z2.y, z3.x, z3.y};
-                        times_slope(d, z, g.act);
-                        if (g.pieces == 2) *at = split8<T>(d, *zat);
-                        else *at = pack8<T>(d);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) sum[j] += d[j];
-                }
-                mlp::fence_async_smem();
-            }
+            if (g.act != kNoAct && g.pieces == 2) slopes(s, std::true_type());
+            else if (g.act != kNoAct || g.want_db) slopes(s, std::false_type());
             __syncwarp();
             if (lane == 0) mlp::mbar_arrive(ready + 8 * r.stage);
             r.next(g.stages);
@@ -1502,14 +1511,15 @@ struct Slope {
     int col_blocks, shares;
 };
 
-// kVectors: the rows of dy and z begin on 16-byte boundaries and cols is a multiple of 8.
-template <typename T, bool kVectors>
+// kVectors: the rows of dy and z begin on 16-byte boundaries and cols is a multiple of 8. kLow: low is wanted (a kernel of its
+// own, since it takes 110 registers instead of 80).
+template <typename T, bool kVectors, bool kLow>
 __device__ __forceinline__ void slope_block(const Slope& a, int block) {
     __shared__ float part[8][64];
     const T* dy = static_cast<const T*>(a.dy.p);
     const T* z = static_cast<const T*>(a.z.p);
     T* dz = static_cast<T*>(a.dz);
-    T* low = static_cast<T*>(a.low);
+    [[maybe_unused]] T* low = static_cast<T*>(a.low);
     const int col_block = block % a.col_blocks, which = block / a.col_blocks, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = col_block * 64 + 8 * (threadIdx.x % a.groups), r = threadIdx.x / a.groups, step = 256 / a.groups;
     const int64_t share = (a.rows + a.shares - 1) / a.shares, r0 = which * share, r1 = min(a.rows, r0 + share);
@@ -1525,9 +1535,13 @@ __device__ __forceinline__ void slope_block(const Slope& a, int block) {
         }
         // rows of dz are multiples of 8 wide: what lies between `cols` and that is zero
         if (dz != nullptr && in_bounds<kChkWork>(dz + row * a.lddz + col, 16)) {
-            uint4 rest;
-            *reinterpret_cast<uint4*>(dz + row * a.lddz + col) = low != nullptr ? split8<T>(d, rest) : pack8<T>(d);
-            if (low != nullptr && in_bounds<kChkWork>(low + row * a.lddz + col, 16)) *reinterpret_cast<uint4*>(low + row * a.lddz + col) = rest;
+            if constexpr (kLow) {
+                uint4 rest;
+                *reinterpret_cast<uint4*>(dz + row * a.lddz + col) = split8<T>(d, rest);
+                if (in_bounds<kChkWork>(low + row * a.lddz + col, 16)) *reinterpret_cast<uint4*>(low + row * a.lddz + col) = rest;
+            } else {
+                *reinterpret_cast<uint4*>(dz + row * a.lddz + col) = pack8<T>(d);
+            }
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) s[j] += d[j];
@@ -1612,10 +1626,10 @@ __device__ __forceinline__ void slope_block(const Slope& a, int block) {
 
 // What comes before the products, in one launch: dz and db's sums (the first blocks), and the copies of
 // arrays that TMA cannot read as they are.
-template <typename T, bool kVectors>
-__global__ void __launch_bounds__(256, kVectors ? 1 : 2) prepare_kernel(const __grid_constant__ Slope slope, const __grid_constant__ RealignList copies, int slope_blocks) {
+template <typename T, bool kVectors, bool kLow>
+__global__ void __launch_bounds__(256, !kVectors ? 2 : kLow ? 1 : 3) prepare_kernel(const __grid_constant__ Slope slope, const __grid_constant__ RealignList copies, int slope_blocks) {
     after_previous_kernel();
-    if ((int)blockIdx.x < slope_blocks) slope_block<T, kVectors>(slope, blockIdx.x);
+    if ((int)blockIdx.x < slope_blocks) slope_block<T, kVectors, kLow>(slope, blockIdx.x);
     else realign_block(copies, blockIdx.x - slope_blocks);
 }
 

@@ -65,7 +65,8 @@ def test_relu_passes_a_nan_on(N, K, M, dtype):
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("N,K,M,pad", [(1, 64, 64, 0), (16, 2048, 1024, 0), (200, 48, 72, 8), (4099, 173, 257, 3), (33, 9, 7, 1), (90001, 64, 64, 0),
                                        (90001, 64, 24, 8), (90001, 27, 31, 3), (20000, 128, 128, 0), (40000, 200, 40, 0), (9700, 1000, 300, 0),
-                                       (19100, 160, 512, 0), (30000, 16, 816, 8), (50000, 64, 4, 0)])
+                                       (19100, 160, 512, 0), (30000, 16, 816, 8), (50000, 64, 4, 0), (40000, 40, 200, 0),
+                                       (50000, 64, 256, 8), (700, 1100, 1900, 0)])
 def test_fp32_gradients_behind_smooth_activations(N, K, M, pad, dtype, act):
     """dz enters the products as two numbers of the layer's type: off by the square of its half step, 2^-16 for bf16 and 2^-22
     for fp16 (at least half of fp16's smallest number, 2^-25), not by the half step. The slope is off by 32 * 2^-24 (1 + |z|),
