@@ -110,7 +110,7 @@ def calls(hg, torch, shape, y32):
     """One forward and one backward call of a layer as a function that returns their outputs and their status words."""
     N, K, M = shape
     gen = torch.Generator(device="cuda").manual_seed(N + K)
-    layer = hg.Linear(K, M, activation=hg.HASHGRID_ACT_RELU)
+    layer = hg.Linear(K, M, activation=hg.HASHGRID_ACT_SILU if y32 else hg.HASHGRID_ACT_RELU)
     x, w, dy, z = (torch.randn(*s, device="cuda", generator=gen).bfloat16() for s in ((N, K), (M, K), (N, M), (N, M)))
     kind = torch.float32 if y32 else torch.bfloat16
     out = [torch.empty(N, M, device="cuda", dtype=kind), torch.empty(N, K, device="cuda", dtype=kind),
